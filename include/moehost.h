@@ -70,6 +70,21 @@ extern "C" {
 #define MOE_ERR_NOMEM (-6)
 #define MOE_ERR_INJECTED (-7)
 #define MOE_ERR_SCRATCH_TOO_SMALL (-8)
+#define MOE_ERR_BAD_INDEX (-9)
+
+/* Element types of the decoder-layer operators (moe_add_rms_norm, moe_kv_*,
+ * moe_linear).  MOE_E4M3 is the 8-bit float with 4 exponent and 3 mantissa bits,
+ * largest value 448; conversions to it round to nearest, ties to even, and saturate. */
+#define MOE_BF16 0
+#define MOE_F16 1
+#define MOE_F32 2
+#define MOE_E4M3 3
+
+/* Activations of moe_linear.  GELU is the exact form, v * Phi(v). */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1
+#define MOE_ACT_SILU 2
+#define MOE_ACT_GELU 3
 
 /* Layer parameters.
  *  E, k        experts and picks per token ("Milo and James Try Inference
@@ -348,6 +363,125 @@ int moe_residency_plan(const int32_t* counts, const int32_t* loc, int E, int n_h
  *  scales  device uint8 [rows][K/32] out.
  * rows = 0 is valid.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
 int moe_quant_mxfp4(const void* x_bf16, int rows, int K, uint8_t* nib, uint8_t* scales, void* stream);
+
+/* ---- The rest of a decoder layer -------------------------------------------------
+ * The MoE layer takes router logits and activations and returns the experts' sum.
+ * These entry points are what a decoder layer runs around it: residual addition and
+ * norm, position rotation with the append to a paged key-value cache, attention of
+ * one new token per sequence over that cache, and the dense products between them.
+ * All strides are in elements, the innermost dimension is contiguous, and no call
+ * allocates device memory or synchronises, so all can be captured in a graph.  Sums,
+ * statistics and accumulators are fp32; each output is rounded once. */
+
+/* Residual addition and root-mean-square norm:
+ *   s = x + residual;  sum_out = s;  y = s * rsqrt(mean(s^2) + eps) * weight
+ * with s kept in fp32 (the norm is of the unrounded sum).  Each row is independent.
+ *  x         device [T][H] of x_type (MOE_BF16, MOE_F16 or MOE_F32), rows x_stride apart.
+ *  residual  device [T][H] of res_type (same three types), rows res_stride apart, or
+ *            NULL (s = x).
+ *  weight    device [H] of weight_type (same three types), or NULL (ones).
+ *  sum_out   device [T][H] of res_type, rows sum_stride apart, or NULL; may be
+ *            residual or x themselves (same rows, type and stride).
+ *  y         device [T][H] of y_type, rows y_stride apart; may be x itself likewise.
+ *            MOE_E4M3: y holds y / y_scale[t] with y_scale[t] = max(max_j |y_tj| / 448,
+ *            2^-126); a row with a NaN or an infinite square gets a NaN scale.
+ *  y_scale   device fp32 [T], MOE_E4M3 only (else NULL).
+ * 1 <= H <= 32768, eps finite and >= 0; T = 0 is valid.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
+int moe_add_rms_norm(const void* x, int x_type, int64_t x_stride, const void* residual, int res_type,
+                     int64_t res_stride, const void* weight, int weight_type, float eps, int T, int H, void* sum_out,
+                     int64_t sum_stride, void* y, int y_type, int64_t y_stride, float* y_scale, void* stream);
+
+/* A paged key-value cache of one layer.  Token slot s is entry s % page_size of page
+ * s / page_size; element d of key head h there is at
+ *   k_cache[(s / page_size) * page_stride + (s % page_size) * token_stride + h * head_stride + d]
+ * and of v_cache likewise, so both orders of tokens and heads within a page fit.
+ *  type       MOE_BF16, MOE_F16, or MOE_E4M3 with one fp32 scale per key head (value =
+ *             scale * code).
+ *  q_heads    a multiple of kv_heads; query head h reads key head
+ *             h / (q_heads / kv_heads).
+ *  head_dim   a multiple of 16, at most 256.
+ *  page_size  any from 1 to 65536.
+ *  max_batch  most sequences of one moe_kv_attend call, 1 to 65535. */
+typedef struct moe_kv_params {
+    int n_pages, page_size, kv_heads, q_heads, head_dim, type, max_batch;
+    int64_t page_stride, token_stride, head_stride;
+} moe_kv_params;
+
+typedef struct moe_kv moe_kv;
+
+/* Creates the handle: k_cache, v_cache (device, 16-byte aligned, strides whole
+ * 16-byte units) and the scales (device fp32 [kv_heads], both or none: MOE_E4M3 needs
+ * them, the other types take NULL) are borrowed for its life.  The handle owns a
+ * status word and the workspace in which moe_kv_attend joins parts of a sequence, so
+ * calls of moe_kv_attend on one handle must be ordered on one stream or by events.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA, MOE_ERR_NOMEM. */
+int moe_kv_create(const moe_kv_params* p, void* k_cache, void* v_cache, const float* k_scale, const float* v_scale,
+                  moe_kv** out);
+int moe_kv_destroy(moe_kv* kv);
+
+/* Position rotation and append.  For each token t: the first rot_dim elements of
+ * every head of q and k are turned by the token's position,
+ *   (a, b) -> (a cos - b sin, a sin + b cos),
+ * over the pairs (i, i + rot_dim/2), or (2i, 2i + 1) when interleaved is 1; q goes to
+ * q_out, k and v to cache slot slots[t] (E4M3 caches: divided by the head's scale).
+ *  q [T][q_heads][head_dim], k and v [T][kv_heads][head_dim], q_out as q: device, of
+ *  `type` (MOE_BF16, MOE_F16 or MOE_F32), token strides *_ts and head strides *_hs;
+ *  q_out may be q itself.
+ *  positions device int32 [T]; cos_sin device fp32 [n_positions][rot_dim], the row's
+ *  rot_dim/2 cosines, then its sines (both NULL when rot_dim is 0).
+ *  slots device int64 [T]: a negative slot appends nothing (q_out is still written);
+ *  two tokens of a call must not share a slot.
+ * A position outside the table, or a slot past the last page, sets MOE_ERR_BAD_INDEX in
+ * the handle's status: of the first token nothing is written, of the second q_out
+ * alone.  0 <= rot_dim <= head_dim, even; T = 0 is valid.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
+int moe_kv_append(moe_kv* kv, int type, const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts,
+                  int64_t k_hs, const void* v, int64_t v_ts, int64_t v_hs, const int32_t* positions,
+                  const int64_t* slots, const float* cos_sin, int n_positions, int rot_dim, int interleaved, int T,
+                  void* q_out, int64_t qo_ts, int64_t qo_hs, void* stream);
+
+/* Attention of one query token per sequence over the cache:
+ *   out[b][h] = sum_j softmax_j(scale * q[b][h] . k_j) v_j,  j in [max(0, n - window), n)
+ * with n = lengths[b] tokens (window = 0: all of them), k_j and v_j of key head
+ * h / (q_heads / kv_heads) at slot page_table[b][j / page_size] * page_size + j % page_size.
+ *  q, out  device [B][q_heads][head_dim] of type q_type: MOE_BF16 or MOE_F16, the
+ *          cache's own type unless the cache is MOE_E4M3; strides *_ts per sequence and
+ *          *_hs per head; 16-byte aligned, strides whole 16-byte units.
+ *  page_table device int32 [B][max_pages], rows table_stride apart (0: one row for all);
+ *          entries past a sequence's last page (or wholly before its window) are not read.
+ *  lengths device int32 [B].  A sequence of length 0 gets zeros and a log-sum of -inf.
+ *  lse     device fp32 [B][q_heads] out, contiguous: log sum_j exp(scale * q . k_j), or NULL.
+ * Several query tokens of one sequence are several rows with their own lengths and the
+ * same page-table row.  A page id outside [0, n_pages) or a length outside
+ * [0, max_pages * page_size] sets MOE_ERR_BAD_INDEX in the handle's status; the page's
+ * tokens are left out, the length is clamped.  The result does not depend on the
+ * timing of the GPU: the same call gives the same bits.
+ * 0 <= B <= max_batch; scale finite.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
+int moe_kv_attend(moe_kv* kv, const void* q, int q_type, int64_t q_ts, int64_t q_hs, const int32_t* page_table,
+                  int64_t table_stride, int max_pages, const int32_t* lengths, int B, float scale, int window,
+                  void* out, int64_t out_ts, int64_t out_hs, float* lse, void* stream);
+
+/* Reads (synchronous; 0 = no error so far) and clears the handle's status word. */
+int moe_kv_get_status(moe_kv* kv, int* status);
+int moe_kv_clear_status(moe_kv* kv);
+
+/* Matrix product with its epilogue: y = act(x W^T + bias) + residual, and for E4M3
+ * operands y = act(x_scale[t] * w_scale[n] * (x W^T) + bias) + residual.
+ *  x device [T][K], w device [N][K] (one row per output), both of in_type: MOE_BF16,
+ *    MOE_F16 or MOE_E4M3; 16-byte aligned, row strides and K * element size multiples
+ *    of 16 bytes (pad K with zeros otherwise).
+ *  x_scale [T], w_scale [N] device fp32: MOE_E4M3 only, both (else NULL).
+ *  bias device [N] of bias_type (MOE_BF16, MOE_F16, MOE_F32), or NULL.
+ *  act MOE_ACT_*.
+ *  residual device [T][N] of y_type, rows res_stride apart, or NULL; may be y itself.
+ *  y device [T][N] of y_type (MOE_BF16, MOE_F16, MOE_F32), rows y_stride apart.
+ * T, N and the strides of y and residual are free; T = 0 is valid; N, K >= 1.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
+int moe_linear(const void* x, int64_t x_stride, const void* w, int64_t w_stride, int in_type, int T, int N, int K,
+               const float* x_scale, const float* w_scale, const void* bias, int bias_type, int act,
+               const void* residual, int64_t res_stride, void* y, int y_type, int64_t y_stride, void* stream);
 
 /* Copies the placement map to host int32 [E] (synchronous). */
 int moe_layer_get_loc(moe_layer* L, int32_t* loc_host);

@@ -11,7 +11,7 @@ import ctypes
 
 import numpy as np
 
-from ._lib import (LIB_PATH, MOE_ERR_BAD_EXPERT, MOE_ERR_CUDA, MOE_ERR_INJECTED, MOE_ERR_INVALID_ARG,
+from ._lib import (LIB_PATH, MOE_ERR_BAD_EXPERT, MOE_ERR_BAD_INDEX, MOE_ERR_CUDA, MOE_ERR_INJECTED, MOE_ERR_INVALID_ARG,
                    MOE_ERR_NOMEM, MOE_ERR_NONFINITE, MOE_ERR_SCRATCH_TOO_SMALL, MOE_ERR_TIMEOUT,
                    MOE_NOALLOC_SCRATCH_BYTES, MOE_OK, MoeError, check, lib, moe_params, ptr, stream_handle)
 
@@ -19,7 +19,8 @@ __all__ = ["LIB_PATH", "MoeError", "Scratch", "Layer", "StepBuffers", "expert_by
            "moe_grouped_ffn", "moe_combine", "residency_update", "moe_gather_join", "link_probe", "debug_e2m1_pairs", "debug_e2m1_round", "run_step",
            "MOE_OK", "MOE_ERR_INVALID_ARG", "MOE_ERR_CUDA", "MOE_ERR_NONFINITE", "MOE_ERR_BAD_EXPERT",
            "MOE_ERR_TIMEOUT", "MOE_ERR_NOMEM", "MOE_ERR_INJECTED", "MOE_ERR_SCRATCH_TOO_SMALL",
-           "moe_grouped_ffn_noalloc", "residency_plan", "quant_mxfp4", "mxf4_peak_probe"]
+           "moe_grouped_ffn_noalloc", "residency_plan", "quant_mxfp4", "mxf4_peak_probe", "MOE_ERR_BAD_INDEX",
+           "KvCache", "moe_add_rms_norm", "moe_kv_append", "moe_kv_attend", "moe_linear"]
 
 
 def expert_bytes(H: int, I: int) -> int:
@@ -266,3 +267,18 @@ def run_step(layer: Layer, buf: StepBuffers, logits, x, stream=None, residency=T
                     stream=stream)
     moe_combine(buf.y, buf.topk_w, T, layer.k, layer.H, buf.out, buf.out_fp32, stream)
     return residency_update(layer, stream) if residency else 0
+
+
+_DECODER_OPS = ("KvCache", "moe_add_rms_norm", "moe_kv_append", "moe_kv_attend", "moe_linear")
+
+
+def __getattr__(name):
+    """The decoder-layer operators take torch tensors; torch is imported when one is
+    first asked for."""
+    if name in _DECODER_OPS:
+        from . import decoder_ops
+
+        for n in _DECODER_OPS:
+            globals()[n] = getattr(decoder_ops, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -29,6 +29,9 @@ MOE_ERR_TIMEOUT = -5
 MOE_ERR_NOMEM = -6
 MOE_ERR_INJECTED = -7
 MOE_ERR_SCRATCH_TOO_SMALL = -8
+MOE_ERR_BAD_INDEX = -9
+MOE_BF16, MOE_F16, MOE_F32, MOE_E4M3 = range(4)
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU = range(4)
 MOE_NOALLOC_SCRATCH_BYTES = 8 << 20  # size of moe_grouped_ffn_noalloc's static workspace (moehost.h)
 
 
@@ -39,8 +42,17 @@ class moe_params(ctypes.Structure):
                 ("host_mirror", ctypes.c_int), ("zero_copy", ctypes.c_int)]
 
 
+class moe_kv_params(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("q_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("type", ctypes.c_int),
+                ("max_batch", ctypes.c_int), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
+_F = ctypes.c_float
 _Z = ctypes.c_size_t
 
 _SIGS = {
@@ -78,6 +90,14 @@ _SIGS = {
     "moe_debug_e2m1_pairs": (_I, [_P, _P]),
     "moe_debug_e2m1_round": (_I, [_P, _I, _P, _P]),
     "moe_debug_wait_timeout": (_I, [_P, _P, _P]),
+    "moe_add_rms_norm": (_I, [_P, _I, _L, _P, _I, _L, _P, _I, _F, _I, _I, _P, _L, _P, _I, _L, _P, _P]),
+    "moe_kv_create": (_I, [ctypes.POINTER(moe_kv_params), _P, _P, _P, _P, ctypes.POINTER(_P)]),
+    "moe_kv_destroy": (_I, [_P]),
+    "moe_kv_append": (_I, [_P, _I, _P, _L, _L, _P, _L, _L, _P, _L, _L, _P, _P, _P, _I, _I, _I, _I, _P, _L, _L, _P]),
+    "moe_kv_attend": (_I, [_P, _P, _I, _L, _L, _P, _L, _I, _P, _I, _F, _I, _P, _L, _L, _P, _P]),
+    "moe_kv_get_status": (_I, [_P, ctypes.POINTER(_I)]),
+    "moe_kv_clear_status": (_I, [_P]),
+    "moe_linear": (_I, [_P, _L, _P, _L, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _L, _P, _I, _L, _P]),
 }
 
 for _name, (_res, _args) in _SIGS.items():

@@ -15,7 +15,7 @@
 #include <new>
 #include <vector>
 
-#include "internal.cuh"
+#include "host.cuh"
 
 using namespace moe;
 
@@ -76,19 +76,6 @@ struct moe_layer {
 
 namespace {
 
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool is_device_ptr(const void* p) {
-    cudaPointerAttributes at;
-    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    return at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged;
-}
-
 // Returns the device pointer of pinned, mapped host memory, or nullptr.
 void* mapped_host_ptr(void* p) {
     cudaPointerAttributes at;
@@ -104,8 +91,6 @@ void* mapped_host_ptr(void* p) {
     }
     return d;
 }
-
-cudaStream_t S(void* s) { return static_cast<cudaStream_t>(s); }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -894,6 +879,7 @@ const char* moe_strerror(int code) {
         case MOE_ERR_NOMEM: return "out of memory";
         case MOE_ERR_INJECTED: return "injected fault (test hook)";
         case MOE_ERR_SCRATCH_TOO_SMALL: return "batch needs more workspace than the static no-allocation array holds";
+        case MOE_ERR_BAD_INDEX: return "position, slot, page or length out of range";
         default: return "unknown status";
     }
 }

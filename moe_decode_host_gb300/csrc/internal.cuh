@@ -198,4 +198,85 @@ cudaError_t launch_copy_list(const SwapList& s, size_t blob_bytes, int ctas, cud
 
 cudaError_t launch_debug_e2m1(uint32_t* out, cudaStream_t st);
 
+// ---- decoder-layer operators around the MoE layer ------------------------------
+// Strides are in elements; types are moehost.h's MOE_BF16 ...
+
+struct NormArgs {
+    const void *x, *res, *w;  // res, w may be null
+    int x_type, res_type, w_type;
+    int64_t x_stride, res_stride;
+    float eps;
+    int T, H;
+    void* sum;  // of res_type; may be null
+    int64_t sum_stride;
+    void* y;
+    int y_type;
+    int64_t y_stride;
+    float* scale;  // [T], E4M3 output only
+};
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);
+
+// A paged cache as the kernels see it.
+struct KvView {
+    void *k, *v;
+    const float *k_scale, *v_scale;  // [kv_heads], E4M3 caches only, else null
+    int type;
+    int n_pages, page_size, kv_heads, q_heads, head_dim;
+    int64_t page_stride, token_stride, head_stride;
+    int* status;
+};
+
+struct AppendArgs {
+    KvView kv;
+    const void *q, *k, *v;
+    int type;  // of q, k, v and q_out
+    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;
+    const int32_t* positions;
+    const int64_t* slots;
+    const float* cos_sin;
+    int n_positions, rot, interleaved, T;
+    void* q_out;
+    int64_t qo_ts, qo_hs;
+};
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t st);
+
+struct AttendArgs {
+    KvView kv;
+    const void* q;
+    int q_type;  // of q and out
+    int64_t q_ts, q_hs;
+    const int32_t* page_table;
+    int64_t table_stride;
+    int max_pages;
+    const int32_t* lengths;
+    int B;
+    float scale;
+    int window;  // 0: none
+    void* out;
+    int64_t out_ts, out_hs;
+    float* lse;  // [B][q_heads], may be null
+    int sm_count;
+    void* workspace;  // attend_workspace bytes, zero before the handle's first call
+};
+size_t attend_workspace(const KvView& kv, int max_batch, int sm_count);
+cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st);
+
+struct LinearArgs {
+    const void *x, *w;
+    int in_type;
+    int64_t x_stride, w_stride;
+    int T, N, K;
+    const float *x_scale, *w_scale;  // E4M3 operands only, else null
+    const void* bias;                // [N], may be null
+    int bias_type;
+    int act;
+    const void* res;  // of y_type, may be null
+    int64_t res_stride;
+    void* y;
+    int y_type;
+    int64_t y_stride;
+    int sm_count;
+};
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st);
+
 }  // namespace moe
