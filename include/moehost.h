@@ -454,7 +454,7 @@ int moe_kv_append(moe_kv* kv, int type, const void* q, int64_t q_ts, int64_t q_h
  *  lse     device fp32 [B][q_heads] out, contiguous: log sum_j exp(scale * q . k_j), or NULL.
  * Several query tokens of one sequence are several rows with their own lengths and the
  * same page-table row.  A page id outside [0, n_pages) or a length outside
- * [0, max_pages * page_size] sets MOE_ERR_BAD_INDEX in the handle's status; the page's
+ * [0, max_pages * page_size] (or above 2^30) sets MOE_ERR_BAD_INDEX in the handle's status; the page's
  * tokens are left out, the length is clamped.  The result does not depend on the
  * timing of the GPU: the same call gives the same bits.
  * 0 <= B <= max_batch; scale finite.

@@ -258,7 +258,7 @@ struct AttendArgs {
     int sm_count;
     void* workspace;  // attend_workspace bytes, zero before the handle's first call
 };
-size_t attend_workspace(const KvView& kv, int max_batch, int sm_count);
+size_t attend_workspace(const KvView& kv, int sm_count);
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st);
 
 struct LinearArgs {

@@ -2,101 +2,652 @@
 //
 //   o = sum_j softmax_j(scale * q . k_j) v_j,  j in [max(0, len - window), len)
 //
-// Plain form of the kernel: a CTA per query head and sequence, a warp per token, the
-// running maximum and sum of the softmax per warp, joined at the end.
+// Bound by the cache's bytes, each read once for all query heads of a key head.
+//
+// Split.  The attended tokens of a (sequence, key head, block of query heads) form a
+// segment of units of 16 tokens; the segments of a call are laid end to end and every
+// CTA gets the same number of units of that line, whatever the lengths.  A CTA walks
+// its stretch as pieces of segments.  A segment inside one CTA is finished there; the
+// parts of one that spans CTAs go to a workspace, and the CTA that arrives last joins
+// them, always in the order of the line, so the result does not depend on timing.
+//
+// A piece.  Each warp takes every fourth unit through a ring of its own (cp.async, no
+// barrier between warps) with its own running maximum and sum; the warps are joined in
+// shared memory at the piece's end.  The transposed products keep the padding small:
+//   S^T [16 tokens x 8 heads] = K Q^T,   O^T [16 dims x 8 heads] += V^T P^T
+// put the query heads in the 8-wide side of m16n8k16, and a head's statistics in the
+// same lanes for S and O, so rescaling needs no exchange.  E4M3 keys and values become
+// f16 in registers (exactly): the order of dimensions within a 16-wide step of the
+// contraction is free, so a lane's four consecutive bytes serve as its four elements.
 #include "ptx.cuh"
 #include "vec.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kMaxD = 256;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kUnit = 16;        // tokens of a unit
+constexpr int kMaxStages = 8;    // units of a warp's ring
+constexpr int kMinUnits = 4;     // units worth a CTA of its own: one a warp
+constexpr int64_t kMaxTokens = 1 << 30;  // of a sequence: token indexes stay in 32 bits
+constexpr float kLog2e = 1.44269504f;
+constexpr float kLn2 = 0.69314718f;
 
-__device__ __forceinline__ float load_one(const void* p, int64_t at, int type) {
-    if (type == MOE_F32) return static_cast<const float*>(p)[at];
-    if (type == MOE_E4M3) {
-        const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(p)[at], __NV_E4M3);
-        return __half2float(__half(h));
-    }
-    return half_bits_to_f32(static_cast<const uint16_t*>(p)[at], type);
+// What the host derives from the cache and the call.
+struct Plan {
+    int chunk;      // query heads of a segment, at most 8 NT
+    int chunks;     // segments of a key head
+    int pitch;      // bytes of a row in the ring: an odd multiple of 16, so ldmatrix meets no bank twice
+    int stages;
+    int cpr;        // 16-byte pieces of a row
+    uint32_t inv;   // 2^20 / cpr rounded up: row of piece i = i * inv >> 20 (i < 512)
+    int slots;      // CTAs the workspace has room for
+};
+
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-__global__ void __launch_bounds__(kWarps * 32) attend_kernel(const AttendArgs a) {
-    __shared__ float so[kWarps][kMaxD], sm[kWarps], sl[kWarps];
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void cp_wait(int left) {  // until at most `left` groups are in flight
+    switch (left) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    }
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+template <bool BF>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (BF)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two E4M3 codes (the low or high half of w) as f16x2.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+// Attended tokens of sequence b: [first, first + count).
+struct Span {
+    int first, count;
+};
+__host__ __device__ __forceinline__ int64_t room_of(const AttendArgs& a) {  // tokens that a row of the table can hold
+    const int64_t room = (int64_t)a.max_pages * a.kv.page_size;
+    return room < kMaxTokens ? room : kMaxTokens;
+}
+__device__ __forceinline__ Span span_of(const AttendArgs& a, int b) {
+    const int64_t room = room_of(a);
+    int64_t n = a.lengths[b];
+    n = n < 0 ? 0 : (n > room ? room : n);
+    const int first = a.window > 0 && n > a.window ? (int)n - a.window : 0;
+    return {first, (int)n - first};
+}
+__device__ __forceinline__ int units_of(const Span& s) { return (int)(((int64_t)s.count + kUnit - 1) / kUnit); }
+
+// T: 0 bf16, 1 f16, 2 E4M3 (computed in f16).  DP: head_dim rounded up to 64, 128 or
+// 256.  NT: blocks of 8 query heads.
+template <int T, int DP, int NT>
+__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(const AttendArgs a, const Plan p) {
+    constexpr bool BF = T == 0, F8 = T == 2;
+    constexpr int HC = 8 * NT;
+    constexpr int ES = F8 ? 1 : 2;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float s_m[kWarps][HC], s_l[kWarps][HC], s_scale[HC], s_inv[HC];
+    __shared__ uint32_t s_mask[kWarps][kMaxStages];
+    __shared__ long long s_sum[kWarps], s_before;
+    __shared__ int s_b, s_last;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, c = lane & 3;
+    const int D = a.kv.head_dim, steps = D / 16;
+    const int qpitch = D * 2 + 16;
+    const int unit_bytes = 2 * kUnit * p.pitch;
+    uint8_t* s_q = smem;
+    uint8_t* ring = smem + HC * (DP * 2 + 16) + warp * p.stages * unit_bytes;
+    const uint32_t ring_u = smem_u32(ring), q_u = smem_u32(s_q);
+    const int heads = a.kv.q_heads, group = heads / a.kv.kv_heads;
+    const int per_b = a.kv.kv_heads * p.chunks;  // segments of a sequence
     grid_dep_wait();
-    const int h = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kh = h / (a.kv.q_heads / a.kv.kv_heads), D = a.kv.head_dim;
-    int n = a.lengths[b];
-    const int64_t most = (int64_t)a.max_pages * a.kv.page_size;
-    if (n < 0 || n > most) {
-        if (threadIdx.x == 0) set_status(a.kv.status, MOE_ERR_BAD_INDEX);
-        n = n < 0 ? 0 : (int)most;
-    }
-    const int first = a.window > 0 && n > a.window ? n - a.window : 0;
-    float q[8], o[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int d = lane + 32 * i;
-        q[i] = d < D ? load_one(a.q, b * a.q_ts + h * a.q_hs + d, a.q_type) * a.scale : 0.f;
-        o[i] = 0.f;
-    }
-    const float ks = a.kv.k_scale ? a.kv.k_scale[kh] : 1.f, vs = a.kv.v_scale ? a.kv.v_scale[kh] : 1.f;
-    float m = -INFINITY, l = 0.f;
-    for (int j = first + warp; j < n; j += kWarps) {
-        const int page = a.page_table[b * a.table_stride + j / a.kv.page_size];
-        if (page < 0 || page >= a.kv.n_pages) {
-            if (lane == 0) set_status(a.kv.status, MOE_ERR_BAD_INDEX);
-            continue;
+
+    // ---- sequences without a token, and lengths out of range ----
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const int n = a.lengths[b];
+        if ((n < 0 || n > room_of(a)) && tid == 0) set_status(a.kv.status, MOE_ERR_BAD_INDEX);
+        if (span_of(a, b).count > 0) continue;
+        for (int i = tid; i < heads * (D / 2); i += kThreads) {
+            const int h = i / (D / 2), d = i % (D / 2) * 2;
+            uint16_t* o = static_cast<uint16_t*>(a.out) + b * a.out_ts + h * a.out_hs + d;
+            *reinterpret_cast<uint32_t*>(o) = 0u;
         }
-        const int64_t at = page * a.kv.page_stride + (j % a.kv.page_size) * a.kv.token_stride + kh * a.kv.head_stride;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int d = lane + 32 * i;
-            if (d < D) s = fmaf(q[i], load_one(a.kv.k, at + d, a.kv.type), s);
-        }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= ks;
-        const float mn = fmaxf(m, s);
-        const float c = m == -INFINITY ? 0.f : expf(m - mn), p = mn == -INFINITY ? 0.f : expf(s - mn);
-        l = l * c + p;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int d = lane + 32 * i;
-            if (d < D) o[i] = o[i] * c + p * load_one(a.kv.v, at + d, a.kv.type);
-        }
-        m = mn;
+        if (a.lse)
+            for (int h = tid; h < heads; h += kThreads) a.lse[(int64_t)b * heads + h] = -INFINITY;
     }
+
+    // ---- this CTA's stretch of the line ----
+    long long mine = 0;
+    for (int b = tid; b < a.B; b += kThreads) mine += units_of(span_of(a, b));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) so[warp][lane + 32 * i] = o[i];
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) s_sum[warp] = mine;
     __syncthreads();
-    float mt = -INFINITY, lt = 0.f;
-    for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, sm[w]);
-    for (int w = 0; w < kWarps; ++w) lt += sm[w] == -INFINITY ? 0.f : sl[w] * expf(sm[w] - mt);
-    const int d = threadIdx.x;
-    if (d < D) {
-        float v = 0.f;
-        for (int w = 0; w < kWarps; ++w)
-            if (sm[w] != -INFINITY) v += so[w][d] * expf(sm[w] - mt);
-        const float r[1] = {lt > 0.f ? v / lt * vs : 0.f};
-        store_run<1>(a.out, b * a.out_ts + h * a.out_hs + d, a.q_type, r);
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += s_sum[w];
+    total *= per_b;
+    long long ctas = (total + kMinUnits - 1) / kMinUnits;
+    if (ctas > gridDim.x) ctas = gridDim.x;
+    if ((long long)blockIdx.x >= ctas) return;
+    const long long u_begin = total * blockIdx.x / ctas, u_end = total * (blockIdx.x + 1) / ctas;
+    // the sequence that holds unit u_begin: a scan over the lengths, kThreads at a time
+    {
+        long long before = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            const int b = b0 + tid;
+            const long long u = b < a.B ? (long long)units_of(span_of(a, b)) * per_b : 0;
+            long long x = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            __syncthreads();
+            if (lane == 31) s_sum[warp] = x;
+            __syncthreads();
+            long long base = before;
+            for (int w = 0; w < warp; ++w) base += s_sum[w];
+            const long long lo = base + x - u;
+            if (u > 0 && u_begin >= lo && u_begin < lo + u) {
+                s_b = b;
+                s_before = lo;
+            }
+            for (int w = 0; w < kWarps; ++w) before += s_sum[w];
+            if (before > u_begin) break;
+        }
+        __syncthreads();
     }
-    if (d == 0 && a.lse) a.lse[(int64_t)b * a.kv.q_heads + h] = lt > 0.f ? mt + logf(lt) : -INFINITY;
+    int b = s_b;
+    long long before = s_before;  // units ahead of sequence b
+    Span span = span_of(a, b);
+    int ub = units_of(span);
+
+    for (long long u = u_begin; u < u_end;) {
+        while (u >= before + (long long)ub * per_b) {  // next sequence with a token
+            before += (long long)ub * per_b;
+            ++b;
+            span = span_of(a, b);
+            ub = units_of(span);
+        }
+        const int seg = (int)((u - before) / ub);
+        const long long seg_begin = before + (long long)seg * ub;
+        const int first_u = (int)(u - seg_begin);
+        const int last_u = (int)((u_end < seg_begin + ub ? u_end : seg_begin + ub) - seg_begin);
+        const int kh = seg / p.chunks, h0 = kh * group + seg % p.chunks * p.chunk;
+        const int nh = min(p.chunk, kh * group + group - h0);  // query heads of this segment
+
+        // ---- loads: unit x of this warp is first_u + warp + kWarps * x ----
+        const int n_mine = (last_u - first_u - warp + kWarps - 1) / kWarps;
+        const uint8_t* kb = static_cast<const uint8_t*>(a.kv.k) + kh * a.kv.head_stride * ES;
+        const uint8_t* vb = static_cast<const uint8_t*>(a.kv.v) + kh * a.kv.head_stride * ES;
+        const int32_t* table = a.page_table + b * a.table_stride;
+        int next_page = -1, next_entry = 0;  // lanes 0..15: the page and entry of that row of the next unit
+        auto look_up = [&](int x) {
+            const int j = (first_u + warp + kWarps * x) * kUnit + lane;
+            next_page = -1;
+            if (lane < kUnit && x < n_mine && j < span.count) {
+                const int t = span.first + j, pg = t / a.kv.page_size;
+                next_entry = t - pg * a.kv.page_size;
+                next_page = table[pg];
+            }
+        };
+        auto issue = [&](int x) {  // the unit that look_up last saw, into slot x % stages
+            if (x < n_mine) {
+                const int slot = x % p.stages;
+                const bool past = (first_u + warp + kWarps * x) * kUnit + lane >= span.count;
+                const bool bad = lane < kUnit && !past && (next_page < 0 || next_page >= a.kv.n_pages);
+                if (bad) set_status(a.kv.status, MOE_ERR_BAD_INDEX);
+                const bool ok = lane < kUnit && !past && !bad;
+                const int64_t off = ok ? (next_page * a.kv.page_stride + next_entry * a.kv.token_stride) * ES : 0;
+                const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+                if (lane == 0) s_mask[warp][slot] = mask;
+                const uint32_t dst = ring_u + slot * unit_bytes;
+#pragma unroll 4
+                for (int i0 = 0; i0 < kUnit * p.cpr; i0 += 32) {  // kUnit * cpr is a multiple of 16
+                    const int i = i0 + lane;
+                    const int row = (int)((uint32_t)i * p.inv >> 20), col = (i - row * p.cpr) * 16;
+                    const int64_t o = __shfl_sync(0xffffffffu, off, row & 15);
+                    if (row < kUnit) {
+                        const uint32_t bytes = (mask >> row & 1u) ? 16u : 0u;  // rows left out are zeros
+                        cp_async16(dst + row * p.pitch + col, kb + o + col, bytes);
+                        cp_async16(dst + (kUnit + row) * p.pitch + col, vb + o + col, bytes);
+                    }
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        look_up(0);
+        for (int x = 0; x < p.stages - 1; ++x) {
+            issue(x);
+            look_up(x + 1);
+        }
+
+        // ---- queries: 16 bits, row pitch of an odd number of 16-byte pieces ----
+        for (int h = warp; h < HC; h += kWarps) {
+            const uint16_t* src = static_cast<const uint16_t*>(a.q) + b * a.q_ts + (h0 + h) * a.q_hs;
+            float v[DP / 32];
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < DP / 32; ++i) {
+                const int d = lane + 32 * i;
+                v[i] = h < nh && d < D ? half_bits_to_f32(src[d], a.q_type) : 0.f;
+                top = fmaxf(top, fabsf(v[i]));
+            }
+            int e = 0;
+            if constexpr (F8) {
+                // q becomes f16 scaled by a power of two to a largest magnitude in [2^14, 2^15): a bf16
+                // keeps all its bits down to 2^-28 of the largest
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                e = prescale_exp(top);
+            }
+            const float down = F8 ? pow2i(-e) : 1.f;
+#pragma unroll
+            for (int i = 0; i < DP / 32; ++i) {
+                const int d = lane + 32 * i;
+                if (d < D)
+                    reinterpret_cast<uint16_t*>(s_q + h * qpitch)[d] =
+                        (uint16_t)(BF ? pack_bf16(v[i], 0.f) : pack_f16(v[i] * down, 0.f));
+            }
+            if (lane == 0) s_scale[h] = a.scale * kLog2e * (F8 ? a.kv.k_scale[kh] * pow2i(e) : 1.f);
+        }
+        __syncthreads();
+
+        float o[DP / 16][NT][4], m[NT][2], l[NT][2], sc[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[i][t][j] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                m[t][j] = -INFINITY;
+                l[t][j] = 0.f;
+                sc[t][j] = s_scale[8 * t + 2 * c + j];
+            }
+        }
+
+        for (int x = 0; x < n_mine; ++x) {
+            issue(x + p.stages - 1);
+            look_up(x + p.stages);
+            cp_wait(p.stages - 1);
+            __syncwarp();
+            const int slot = x % p.stages;
+            const uint32_t ku = ring_u + slot * unit_bytes, vu = ku + kUnit * p.pitch;
+            const uint32_t mask = s_mask[warp][slot];
+            float s[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+            if constexpr (F8) {
+                // matrices of a load: token halves of 16-byte piece kk, then of piece kk + 1
+                const uint32_t at = ku + ((lane & 7) + (lane & 8)) * p.pitch + (lane >> 4) * 16;
+#pragma unroll
+                for (int kk = 0; kk < DP / 16; kk += 2) {
+                    if (kk < steps) {
+                        uint32_t r[4];
+                        ldsm4(r, at + kk * 16);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (kk + h < steps) {
+                                const uint32_t f[4] = {e4m3_lo(r[2 * h]), e4m3_lo(r[2 * h + 1]), e4m3_hi(r[2 * h]),
+                                                       e4m3_hi(r[2 * h + 1])};
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) {
+                                    const uint2 q = *reinterpret_cast<const uint2*>(s_q + (8 * t + g) * qpitch +
+                                                                                    (kk + h) * 32 + c * 8);
+                                    mma16816<BF>(s[t], f, q.x, q.y);
+                                }
+                            }
+                        }
+                    }
+                }
+            } else {
+                const uint32_t at = ku + ((lane & 7) + (lane & 8)) * p.pitch + (lane >> 4) * 16;
+#pragma unroll
+                for (int kk = 0; kk < DP / 16; ++kk) {
+                    if (kk < steps) {
+                        uint32_t r[4];
+                        ldsm4(r, at + kk * 32);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            const uint8_t* q = s_q + (8 * t + g) * qpitch + kk * 32 + c * 4;
+                            mma16816<BF>(s[t], r, *reinterpret_cast<const uint32_t*>(q),
+                                         *reinterpret_cast<const uint32_t*>(q + 16));
+                        }
+                    }
+                }
+            }
+            // softmax: lane (g, c) holds tokens g, g + 8 of heads 2c, 2c + 1 of each block
+            const bool ok0 = mask >> g & 1u, ok1 = mask >> (g + 8) & 1u;
+            float keep[NT][2];
+            bool grown = false;
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float x0 = ok0 ? s[t][j] * sc[t][j] : -INFINITY;
+                    const float x1 = ok1 ? s[t][2 + j] * sc[t][j] : -INFINITY;
+                    float top = fmaxf(x0, x1);
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    const float mn = fmaxf(m[t][j], top);
+                    const float ref = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every weight is 0
+                    keep[t][j] = fast_exp2(m[t][j] - ref);
+                    grown |= mn != m[t][j];
+                    m[t][j] = mn;
+                    s[t][j] = fast_exp2(x0 - ref);
+                    s[t][2 + j] = fast_exp2(x1 - ref);
+                    l[t][j] = l[t][j] * keep[t][j] + (s[t][j] + s[t][2 + j]);
+                }
+                // the weights are rounded to the values' 16-bit type for the tensor cores (bf16 adds
+                // about as much error as the output's own rounding; f16 an eighth of it); their sum is not
+                pb[t][0] = transpose8x8(BF ? pack_bf16(s[t][0], s[t][1]) : pack_f16(s[t][0], s[t][1]));
+                pb[t][1] = transpose8x8(BF ? pack_bf16(s[t][2], s[t][3]) : pack_f16(s[t][2], s[t][3]));
+            }
+            if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[i][t][j] *= keep[t][j & 1];
+            }
+            if constexpr (F8) {
+                const uint32_t at = vu + ((lane & 7) + (lane & 8)) * p.pitch + (lane >> 4) * 16;
+#pragma unroll
+                for (int i = 0; i < DP / 16; i += 2) {
+                    if (i < steps) {
+                        uint32_t r[4];
+                        ldsm4_t(r, at + i * 16);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (i + h < steps) {
+                                // bytes (token, dim): (2c, 2g), (2c, 2g+1), (2c+1, 2g), (2c+1, 2g+1)
+                                const uint32_t w0 = __byte_perm(r[2 * h], 0, 0x3120), w1 = __byte_perm(r[2 * h + 1], 0, 0x3120);
+                                const uint32_t f[4] = {e4m3_lo(w0), e4m3_hi(w0), e4m3_lo(w1), e4m3_hi(w1)};
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) mma16816<BF>(o[i + h][t], f, pb[t][0], pb[t][1]);
+                            }
+                        }
+                    }
+                }
+            } else {
+                const uint32_t at = vu + ((lane & 7) + ((lane >> 4) << 3)) * p.pitch + (lane & 8) * 2;
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i) {
+                    if (i < steps) {
+                        uint32_t r[4];
+                        ldsm4_t(r, at + i * 32);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) mma16816<BF>(o[i][t], r, pb[t][0], pb[t][1]);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+
+        // ---- join the warps ----
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float y = l[t][j];
+                y += __shfl_xor_sync(0xffffffffu, y, 4);
+                y += __shfl_xor_sync(0xffffffffu, y, 8);
+                y += __shfl_xor_sync(0xffffffffu, y, 16);
+                if (g == 0) {
+                    s_m[warp][8 * t + 2 * c + j] = m[t][j];
+                    s_l[warp][8 * t + 2 * c + j] = y;
+                }
+            }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        float* mine_o = reinterpret_cast<float*>(ring);  // [HC][D + 4]; the ring is empty now
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int h = 8 * t + 2 * c + j;
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][h]);
+                const float f = m[t][j] == -INFINITY ? 0.f : fast_exp2(m[t][j] - top);
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i) {
+                    if (i < steps) {
+                        // rows g and g + 8 of the block: dims g, g + 8, or for E4M3 2g, 2g + 1
+                        mine_o[h * (D + 4) + 16 * i + (F8 ? 2 * g : g)] = o[i][t][j] * f;
+                        mine_o[h * (D + 4) + 16 * i + (F8 ? 2 * g + 1 : g + 8)] = o[i][t][2 + j] * f;
+                    }
+                }
+            }
+        __syncthreads();
+        const bool whole = first_u == 0 && last_u == ub;
+        float* slot_base = nullptr;
+        int i0 = 0, i1 = 0;
+        if (!whole) {
+            // CTAs that hold the segment's first and last unit
+            i0 = (int)(((seg_begin + 1) * ctas - 1) / total);
+            i1 = (int)(((seg_begin + ub) * ctas - 1) / total);
+            const int slot = 2 * blockIdx.x + ((int)blockIdx.x == i0 ? 1 : 0);
+            slot_base = static_cast<float*>(a.workspace) + p.slots + (int64_t)slot * HC * (D + 2);
+        }
+        if (tid < HC) {
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][tid]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) sum += s_m[w][tid] == -INFINITY ? 0.f : s_l[w][tid] * fast_exp2(s_m[w][tid] - top);
+            if (whole) {
+                s_inv[tid] = (F8 ? a.kv.v_scale[kh] : 1.f) / sum;
+                if (!(sum != 0.f)) s_inv[tid] = 0.f;
+                if (a.lse && tid < nh) a.lse[(int64_t)b * heads + h0 + tid] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            } else {
+                slot_base[tid] = top;
+                slot_base[HC + tid] = sum;
+            }
+        }
+        __syncthreads();
+        {
+            const float* all = reinterpret_cast<const float*>(smem + HC * (DP * 2 + 16));
+            const int step = p.stages * unit_bytes / 4;
+            for (int i = tid; i < nh * (D / 2); i += kThreads) {
+                const int h = i / (D / 2), d = i % (D / 2) * 2;
+                float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 y = *reinterpret_cast<const float2*>(all + w * step + h * (D + 4) + d);
+                    v.x += y.x;
+                    v.y += y.y;
+                }
+                if (whole) {
+                    const float f = s_inv[h];
+                    uint16_t* dst = static_cast<uint16_t*>(a.out) + b * a.out_ts + (h0 + h) * a.out_hs + d;
+                    *reinterpret_cast<uint32_t*>(dst) =
+                        a.q_type == MOE_BF16 ? pack_bf16(v.x * f, v.y * f) : pack_f16(v.x * f, v.y * f);
+                } else {
+                    *reinterpret_cast<float2*>(slot_base + 2 * HC + h * D + d) = v;
+                }
+            }
+        }
+        if (!whole) {
+            // ---- join the CTAs: the last to arrive, in the order of the line ----
+            __threadfence();
+            __syncthreads();
+            int* counters = static_cast<int*>(a.workspace);
+            if (tid == 0) {
+                const int parts = i1 - i0 + 1;
+                s_last = atomicAdd(counters + i0, 1) == parts - 1;
+                if (s_last) counters[i0] = 0;  // as the next call expects it
+            }
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                const float* base = static_cast<const float*>(a.workspace) + p.slots;
+                auto part = [&](int i) { return base + (int64_t)(2 * i + (i == i0 ? 1 : 0)) * HC * (D + 2); };
+                if (tid < nh) {
+                    float top = -INFINITY, sum = 0.f;
+                    for (int i = i0; i <= i1; ++i) top = fmaxf(top, part(i)[tid]);
+                    for (int i = i0; i <= i1; ++i) {
+                        const float mi = part(i)[tid];
+                        sum += mi == -INFINITY ? 0.f : part(i)[HC + tid] * fast_exp2(mi - top);
+                    }
+                    s_scale[tid] = top;
+                    s_inv[tid] = sum != 0.f ? (F8 ? a.kv.v_scale[kh] : 1.f) / sum : 0.f;
+                    if (a.lse) a.lse[(int64_t)b * heads + h0 + tid] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+                }
+                __syncthreads();
+                for (int i = tid; i < nh * (D / 2); i += kThreads) {
+                    const int h = i / (D / 2), d = i % (D / 2) * 2;
+                    const float top = s_scale[h];
+                    float2 v = make_float2(0.f, 0.f);
+#pragma unroll 4
+                    for (int k = i0; k <= i1; ++k) {
+                        const float mi = part(k)[h];
+                        const float f = mi == -INFINITY ? 0.f : fast_exp2(mi - top);
+                        const float2 y = *reinterpret_cast<const float2*>(part(k) + 2 * HC + h * D + d);
+                        v.x = fmaf(y.x, f, v.x);
+                        v.y = fmaf(y.y, f, v.y);
+                    }
+                    const float f = s_inv[h];
+                    uint16_t* dst = static_cast<uint16_t*>(a.out) + b * a.out_ts + (h0 + h) * a.out_hs + d;
+                    *reinterpret_cast<uint32_t*>(dst) =
+                        a.q_type == MOE_BF16 ? pack_bf16(v.x * f, v.y * f) : pack_f16(v.x * f, v.y * f);
+                }
+            }
+        }
+        __syncthreads();  // shared memory is free for the next piece
+        u = seg_begin + last_u;
+    }
+}
+
+int blocks_of_heads(const KvView& kv) {  // NT
+    const int group = kv.q_heads / kv.kv_heads;
+    if (group <= 8) return 1;
+    return group <= 16 || kv.head_dim > 128 ? 2 : 4;
+}
+
+int dim_class(const KvView& kv) { return kv.head_dim <= 64 ? 64 : (kv.head_dim <= 128 ? 128 : 256); }
+
+int ctas_per_sm(const KvView& kv) { return kv.head_dim <= 128 ? 2 : 1; }
+
+int smem_of(const KvView& kv, const Plan& p) {
+    return 8 * blocks_of_heads(kv) * (dim_class(kv) * 2 + 16) + kWarps * p.stages * 2 * kUnit * p.pitch + 16;
+}
+
+Plan plan_of(const KvView& kv, int sm_count) {
+    Plan p;
+    const int hc = 8 * blocks_of_heads(kv), group = kv.q_heads / kv.kv_heads, es = type_bytes(kv.type);
+    p.chunks = (group + hc - 1) / hc;
+    p.chunk = (group + p.chunks - 1) / p.chunks;
+    p.cpr = kv.head_dim * es / 16;
+    p.inv = ((1u << 20) + p.cpr - 1) / p.cpr;
+    p.pitch = (p.cpr | 1) * 16;
+    p.slots = (ctas_per_sm(kv) * sm_count + 1) / 2 * 2;  // even: the sums behind the counters are read in pairs
+    // as many units in flight as fit beside the other CTA of the SM; the ring also holds
+    // the warp's [hc][head_dim + 4] sums when a piece ends
+    const int budget = (ctas_per_sm(kv) == 2 ? 110 : 222) * 1024;
+    const int least = (hc * (kv.head_dim + 4) * 4 + 2 * kUnit * p.pitch - 1) / (2 * kUnit * p.pitch);
+    p.stages = kMaxStages;
+    while (p.stages > 3 && p.stages > least && smem_of(kv, p) > budget) --p.stages;
+    return p;
+}
+
+template <int T, int DP, int NT>
+cudaError_t launch(const AttendArgs& a, const Plan& p, cudaStream_t st) {
+    static std::atomic<uint64_t> configured;
+    const int smem = smem_of(a.kv, p);
+    // one limit serves every head_dim of the class; the CTAs share the SM's whole memory
+    cudaError_t err = ensure_smem_limit((const void*)attend_kernel<T, DP, NT>, (DP <= 128 ? 113 : 224) * 1024, configured);
+    if (err != cudaSuccess) return err;
+    const int64_t per_b = (int64_t)a.kv.kv_heads * p.chunks;
+    const int64_t room = room_of(a);
+    const int64_t most = a.window > 0 && room > a.window ? a.window : room;
+    const int64_t units = (most + kUnit - 1) / kUnit * per_b * a.B;
+    int64_t grid = (units + kMinUnits - 1) / kMinUnits;
+    if (grid > p.slots) grid = p.slots;
+    if (grid < 1) grid = 1;
+    return launch_pdl(attend_kernel<T, DP, NT>, dim3((unsigned)grid), dim3(kThreads), smem, st, a, p);
+}
+
+template <int T>
+cudaError_t pick(const AttendArgs& a, const Plan& p, cudaStream_t st) {
+    const int nt = blocks_of_heads(a.kv);
+    switch (dim_class(a.kv)) {
+        case 64: return nt == 1 ? launch<T, 64, 1>(a, p, st) : nt == 2 ? launch<T, 64, 2>(a, p, st) : launch<T, 64, 4>(a, p, st);
+        case 128:
+            return nt == 1 ? launch<T, 128, 1>(a, p, st) : nt == 2 ? launch<T, 128, 2>(a, p, st) : launch<T, 128, 4>(a, p, st);
+        default: return nt == 1 ? launch<T, 256, 1>(a, p, st) : launch<T, 256, 2>(a, p, st);
+    }
 }
 
 }  // namespace
 
-size_t attend_workspace(const KvView&, int, int) { return 256; }
+// A counter a CTA, then two slots of partial sums a CTA: maxima and sums of the block's
+// heads, and their [heads][head_dim] outputs.
+size_t attend_workspace(const KvView& kv, int sm_count) {
+    const Plan p = plan_of(kv, sm_count);
+    return sizeof(float) * ((size_t)p.slots + (size_t)2 * p.slots * 8 * blocks_of_heads(kv) * (kv.head_dim + 2));
+}
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     if (a.B == 0) return cudaSuccess;
-    return launch_pdl(attend_kernel, dim3(a.kv.q_heads, a.B), dim3(kWarps * 32), 0, st, a);
+    const Plan p = plan_of(a.kv, a.sm_count);
+    if (a.kv.type == MOE_BF16) return pick<0>(a, p, st);
+    if (a.kv.type == MOE_F16) return pick<1>(a, p, st);
+    return pick<2>(a, p, st);
 }
 
 }  // namespace moe

@@ -84,7 +84,7 @@ int moe_kv_create(const moe_kv_params* pp, void* k_cache, void* v_cache, const f
         delete kv;
         return MOE_ERR_CUDA;
     }
-    const size_t ws = attend_workspace(kv->view, p.max_batch, kv->sm_count);
+    const size_t ws = attend_workspace(kv->view, kv->sm_count);
     cudaError_t err = cudaMalloc(&kv->d_status, sizeof(int));
     err = err ? err : cudaMemset(kv->d_status, 0, sizeof(int));
     err = err ? err : cudaMalloc(&kv->workspace, ws);

@@ -425,7 +425,8 @@ def test_attend_far_offsets(m):
     # and the append writes there
     slots = torch.tensor([(n_pages - 1) * page + 3], device="cuda")
     x = randn(g, 1, 48, D).to(BF16)
-    m.moe_kv_append(kv, x[:, :32], x[:, 32:40], x[:, 40:], None, slots, None, torch.empty_like(q))
+    # k and v are the same memory here: both get the same values
+    m.moe_kv_append(kv, x[:, :32], x[:, 40:], x[:, 40:], None, slots, None, torch.empty_like(q))
     assert torch.equal(k[n_pages - 1, 3], x[0, 40:])
 
 
