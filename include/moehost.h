@@ -477,11 +477,14 @@ int moe_kv_clear_status(moe_kv* kv);
  *  act MOE_ACT_*.
  *  residual device [T][N] of y_type, rows res_stride apart, or NULL; may be y itself.
  *  y device [T][N] of y_type (MOE_BF16, MOE_F16, MOE_F32), rows y_stride apart.
- * T, N and the strides of y and residual are free; T = 0 is valid; N, K >= 1.
+ *  status_dev device int, or NULL: set to MOE_ERR_TIMEOUT when a bounded device wait ran
+ *    out (zero it first; y is then undefined).
+ * T, N (at most 2^22) and the strides of y and residual are free; T = 0 is valid; N, K >= 1.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
 int moe_linear(const void* x, int64_t x_stride, const void* w, int64_t w_stride, int in_type, int T, int N, int K,
                const float* x_scale, const float* w_scale, const void* bias, int bias_type, int act,
-               const void* residual, int64_t res_stride, void* y, int y_type, int64_t y_stride, void* stream);
+               const void* residual, int64_t res_stride, void* y, int y_type, int64_t y_stride, int* status_dev,
+               void* stream);
 
 /* Copies the placement map to host int32 [E] (synchronous). */
 int moe_layer_get_loc(moe_layer* L, int32_t* loc_host);

@@ -97,7 +97,7 @@ _SIGS = {
     "moe_kv_attend": (_I, [_P, _P, _I, _L, _L, _P, _L, _I, _P, _I, _F, _I, _P, _L, _L, _P, _P]),
     "moe_kv_get_status": (_I, [_P, ctypes.POINTER(_I)]),
     "moe_kv_clear_status": (_I, [_P]),
-    "moe_linear": (_I, [_P, _L, _P, _L, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _L, _P, _I, _L, _P]),
+    "moe_linear": (_I, [_P, _L, _P, _L, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _L, _P, _I, _L, _P, _P]),
 }
 
 for _name, (_res, _args) in _SIGS.items():

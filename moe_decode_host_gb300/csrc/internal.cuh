@@ -275,6 +275,7 @@ struct LinearArgs {
     void* y;
     int y_type;
     int64_t y_stride;
+    int* status;  // may be null
     int sm_count;
 };
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st);

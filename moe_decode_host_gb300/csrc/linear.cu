@@ -1,21 +1,108 @@
 // Matrix product with an epilogue: y = act(x W^T [* sx_t * sw_n] + bias) + residual.
 //
-// Plain form of the kernel: 16 x 16 tiles through shared memory, fp32 sums.
+// Both kernels run on tcgen05 with operands staged by TMA (128-byte rows of K, 128-byte
+// swizzle) and fp32 accumulators in tensor memory; bf16 and f16 use kind::f16, E4M3
+// kind::f8f6f4, whose stages and descriptors are the same bytes (a step is 32 bytes of
+// K either way).  Rows past T and N and bytes past K arrive as zeros.
+//
+//  split kernel   few output tiles: the weights' bytes (or the latency of one pass over
+//                 K) bound the call.  The weight rows take the 128-wide side of the MMA
+//                 and the tokens its free side (a multiple of 16), so a token tile costs
+//                 what it holds; K is split over the CTAs of a cluster, which join their
+//                 sums through distributed shared memory in rank order.
+//  tiled kernel   many tiles: the tensor cores bound the call.  A CTA pair works on 256
+//                 tokens x up to 256 outputs (cta_group::2: each CTA stages half of both
+//                 operands), persistent, with two accumulators so that the epilogue of a
+//                 tile runs under the next tile's products.
 #include "ptx.cuh"
 #include "vec.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTile = 16;
+constexpr int kThreads = 192;          // warp 0 loads, warp 1 issues, warps 2-5 read the accumulators
+constexpr int kRowBytes = 128;         // bytes of K in a stage
+constexpr int kABytes = 128 * kRowBytes;
+constexpr int kMaxStages = 12;
+constexpr int kSplitRing = 196608;     // bytes of the split kernel's ring
+constexpr int kSplitMax = 8;           // CTAs of a cluster
+constexpr int kTileStages = 6;
+constexpr int kTileStage = 2 * kABytes;
+constexpr int kEpiBytes = 32 * 64 * 4;  // staging of an epilogue warp: 32 rows x 64 columns
 
-__device__ __forceinline__ float load_one(const void* p, int64_t at, int type) {
-    if (type == MOE_E4M3) {
-        const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(p)[at], __NV_E4M3);
-        return __half2float(__half(h));
-    }
-    if (type == MOE_F32) return static_cast<const float*>(p)[at];
-    return half_bits_to_f32(static_cast<const uint16_t*>(p)[at], type);
+struct Head {
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    uint32_t tmem;
+    int abort;
+};
+constexpr int kSplitSmem = 1024 + kSplitRing + (int)sizeof(Head);
+constexpr int kTileSmem = 1024 + kTileStages * kTileStage + 4 * kEpiBytes + (int)sizeof(Head);
+static_assert(kTileSmem <= 227 * 1024, "shared memory of a CTA");
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A wait taken by a whole converged warp; false when it ran out.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, unsigned parity, Head& hd, int* status, int where, int slot) {
+    return __all_sync(0xffffffffu,
+                      mbar_wait_fast(bar, parity, &hd.abort, status, nullptr, where, slot, 0, 0));
+}
+
+// The loading warp's end, at ring position (s, ph) after `loads` stages: waits until the
+// products have read every stage (the last arrivals on these barriers), or after an abort
+// until the copies have landed, so that nothing reaches the CTA's memory after it ended.
+__device__ __forceinline__ void drain(Head& hd, int s, unsigned ph, int stages, int64_t loads) {
+    const bool gone = *reinterpret_cast<volatile int*>(&hd.abort) != 0;
+    if ((threadIdx.x & 31) == 0)
+        for (int k = 0; k < stages && k < loads; ++k) mbar_drain(gone ? &hd.full[k] : &hd.empty[k], k < s ? ph : ph ^ 1u);
+    __syncwarp();
+}
+
+// One k-step by an elected lane of a converged warp.
+template <bool F8, int CG>
+__device__ __forceinline__ void mma_elect(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+    if constexpr (F8 && CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+            : "memory");
+    else if constexpr (F8)
+        asm volatile(
+            "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+            : "memory");
+    else if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+            : "memory");
+}
+
+// Instruction descriptor: fp32 sums, operand formats (f16 and E4M3 are 0, bf16 is 1),
+// M rows and N columns.
+__device__ __forceinline__ uint32_t mma_idesc(int in_type, int m, int n) {
+    const uint32_t f = in_type == MOE_BF16 ? 1u : 0u;
+    return (1u << 4) | (f << 7) | (f << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 __device__ __forceinline__ float activate(float v, int act) {
@@ -25,35 +112,428 @@ __device__ __forceinline__ float activate(float v, int act) {
     return v;
 }
 
-__global__ void linear_kernel(const LinearArgs a) {
-    __shared__ float sx[kTile][kTile + 1], sw[kTile][kTile + 1];
-    grid_dep_wait();
-    const int tx = threadIdx.x, ty = threadIdx.y;
-    const int n = blockIdx.x * kTile + tx, t = blockIdx.y * kTile + ty, nr = blockIdx.x * kTile + ty;
-    float acc = 0.f;
-    for (int k = 0; k < a.K; k += kTile) {
-        sx[ty][tx] = t < a.T && k + tx < a.K ? load_one(a.x, t * a.x_stride + k + tx, a.in_type) : 0.f;
-        sw[ty][tx] = nr < a.N && k + tx < a.K ? load_one(a.w, nr * a.w_stride + k + tx, a.in_type) : 0.f;
-        __syncthreads();
+// VEC consecutive outputs of token t from n on, all in range.
+template <int VEC>
+__device__ __forceinline__ void finish(const LinearArgs& a, int64_t t, int n, float (&v)[VEC]) {
+    if (a.x_scale) {
+        const float sx = a.x_scale[t];
 #pragma unroll
-        for (int i = 0; i < kTile; ++i) acc = fmaf(sx[ty][i], sw[tx][i], acc);
-        __syncthreads();
+        for (int i = 0; i < VEC; ++i) v[i] *= sx * a.w_scale[n + i];
     }
-    if (t >= a.T || n >= a.N) return;
-    if (a.x_scale) acc *= a.x_scale[t] * a.w_scale[n];
-    if (a.bias) acc += load_one(a.bias, n, a.bias_type);
-    acc = activate(acc, a.act);
-    if (a.res) acc += load_one(a.res, t * a.res_stride + n, a.y_type);
-    const float r[1] = {acc};
-    store_run<1>(a.y, t * a.y_stride + n, a.y_type, r);
+    if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            v[i] += a.bias_type == MOE_F32 ? static_cast<const float*>(a.bias)[n + i]
+                                           : half_bits_to_f32(static_cast<const uint16_t*>(a.bias)[n + i], a.bias_type);
+    }
+    if (a.act != MOE_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = activate(v[i], a.act);
+    }
+    if (a.res) {
+        Raw<VEC> r;
+        float f[VEC];
+        r.load(a.res, t * a.res_stride + n, a.y_type);
+        r.get(a.y_type, f);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] += f[i];
+    }
+    store_run<VEC>(a.y, t * a.y_stride + n, a.y_type, v);
+}
+
+// The same where the run may reach past N or is not aligned.
+template <int VEC>
+__device__ __forceinline__ void finish_any(const LinearArgs& a, int64_t t, int n, float (&v)[VEC], bool vec) {
+    if (vec && n + VEC <= a.N) {
+        finish<VEC>(a, t, n, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            if (n + i < a.N) {
+                float one[1] = {v[i]};
+                finish<1>(a, t, n + i, one);
+            }
+        }
+    }
+}
+
+// ---- split kernel ------------------------------------------------------------
+
+// Grid: x the cluster's K parts, y blocks of 128 outputs, z blocks of bn tokens.
+template <bool F8>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_split_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap wmap,
+                        const __grid_constant__ CUtensorMap xmap, int bn, int stages, bool vec) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    Head& hd = *reinterpret_cast<Head*>(base + kSplitRing);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = gridDim.x, rank = blockIdx.x;
+    const int n0 = blockIdx.y * 128, t0 = blockIdx.z * bn;
+    const int nkb = (int)(((int64_t)a.K * (F8 ? 1 : 2) + kRowBytes - 1) / kRowBytes);
+    const int kb0 = (int)((int64_t)nkb * rank / S), kb1 = (int)((int64_t)nkb * (rank + 1) / S);
+    const int stage_bytes = kABytes + bn * kRowBytes;
+    const int tcols = bn <= 32 ? 32 : (bn <= 64 ? 64 : (bn <= 128 ? 128 : 256));
+    if (threadIdx.x == 0) {
+        hd.abort = 0;
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&hd.full[s], 1);
+            mbar_init(&hd.empty[s], 1);
+        }
+        mbar_init(&hd.acc_full[0], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&hd.tmem)),
+                     "r"(tcols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = hd.tmem;
+    grid_dep_wait();
+    if (warp == 0) {
+        const uint64_t first = l2_policy_evict_first(), last = l2_policy_evict_last();
+        int s = 0;
+        unsigned ph = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!wait_warp(&hd.empty[s], ph ^ 1u, hd, a.status, 2, s)) break;
+            uint8_t* st = base + (size_t)s * stage_bytes;
+            mbar_arrive_expect_tx_elect(&hd.full[s], stage_bytes);
+            tma_load_2d_hint_elect(st, &wmap, kb * (F8 ? 128 : 64), n0, &hd.full[s], first);
+            tma_load_2d_hint_elect(st + kABytes, &xmap, kb * (F8 ? 128 : 64), t0, &hd.full[s], last);
+            advance(s, ph, stages);
+        }
+        drain(hd, s, ph, stages, kb1 - kb0);
+    } else if (warp == 1) {
+        const uint32_t idesc = mma_idesc(a.in_type, 128, bn);
+        int s = 0;
+        unsigned ph = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!wait_warp(&hd.full[s], ph, hd, a.status, 1, s)) break;
+            tc_fence_after();
+            const uint64_t ad = sw128_desc(smem_u32(base + (size_t)s * stage_bytes));
+            const uint64_t bd = sw128_desc(smem_u32(base + (size_t)s * stage_bytes + kABytes));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_elect<F8, 1>(tmem, ad + 2 * k, bd + 2 * k, idesc, kb > kb0 || k > 0);
+            tc_commit_elect(&hd.empty[s]);
+            advance(s, ph, stages);
+        }
+        tc_commit_elect(&hd.acc_full[0]);
+    }
+    // ---- sums to shared memory, [token][128 outputs]; the ring is idle by then ----
+    float* dump = reinterpret_cast<float*>(base);
+    const int cols = min(bn, a.T - t0);
+    if (warp >= 2) {
+        const int q = warp & 3;
+        wait_warp(&hd.acc_full[0], 0, hd, a.status, 3, 0);
+        tc_fence_after();
+        for (int c = 0; c < cols; c += 16) {
+            float v[16];
+            tc_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dump[(c + i) * 128 + q * 32 + lane] = v[i];
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tcols) : "memory");
+    }
+    // ---- this rank's tokens: the parts in rank order, then the epilogue ----
+    const int c0 = cols * rank / S, c1 = cols * (rank + 1) / S;
+    for (int i = threadIdx.x; i < (c1 - c0) * 32; i += kThreads) {
+        const int c = c0 + i / 32, r = i % 32 * 4;
+        if (n0 + r >= a.N) continue;
+        const uint32_t at = smem_u32(dump + c * 128 + r);
+        float4 p[kSplitMax];
+#pragma unroll
+        for (int k = 0; k < kSplitMax; ++k)
+            if (k < S)
+                asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                             : "=f"(p[k].x), "=f"(p[k].y), "=f"(p[k].z), "=f"(p[k].w)
+                             : "r"(map_rank(at, k)));
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < kSplitMax; ++k)
+            if (k < S) {
+                v[0] += p[k].x;
+                v[1] += p[k].y;
+                v[2] += p[k].z;
+                v[3] += p[k].w;
+            }
+        finish_any<4>(a, t0 + c, n0 + r, v, vec);
+    }
+    __syncwarp();
+    cluster_sync();  // the others may still read this CTA's sums
+}
+
+// ---- tiled kernel --------------------------------------------------------------
+
+__device__ __forceinline__ void tma_load_pair_elect(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar,
+                                                    uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy)
+        : "memory");
+}
+// Arrives on the barrier at this place in both CTAs when the MMAs issued so far are done.
+__device__ __forceinline__ void commit_pair_elect(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\telect.sync _|e, 0xffffffff;\n\tmov.u16 m, 3;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+            smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+struct TileGrid {
+    int tm, tn, bn;  // tiles along tokens (of 256) and outputs (of bn)
+};
+
+// Tile i: bands of 8 token tiles, the outputs' tiles walked within a band, so that the
+// tiles in flight share operands in L2.
+__device__ __forceinline__ void tile_at(const TileGrid& g, int i, int& m, int& n) {
+    const int band = 8 * g.tn, b = i / band, r = i - b * band;
+    const int rows = min(8, g.tm - 8 * b);
+    n = r / rows;
+    m = 8 * b + r - n * rows;
+}
+
+template <bool F8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    linear_tile_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap wmap,
+                       const __grid_constant__ CUtensorMap xmap, const TileGrid g, bool vec) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t* epi = base + kTileStages * kTileStage;
+    Head& hd = *reinterpret_cast<Head*>(epi + 4 * kEpiBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int nkb = (int)(((int64_t)a.K * (F8 ? 1 : 2) + kRowBytes - 1) / kRowBytes);
+    const int tiles = g.tm * g.tn, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    if (threadIdx.x == 0) {
+        hd.abort = 0;
+        for (int s = 0; s < kTileStages; ++s) {
+            mbar_init(&hd.full[s], 1);
+            mbar_init(&hd.empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&hd.acc_full[s], 1);
+            mbar_init(&hd.acc_empty[s], 8);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&hd.tmem)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = hd.tmem;
+    grid_dep_wait();
+    bool ok = true;
+    if (warp == 0) {
+        // each CTA stages its half: 128 tokens and bn / 2 outputs; the leader's barrier counts both
+        const uint64_t keep = l2_policy_evict_last();
+        const int half = g.bn / 2;
+        const unsigned bytes = 2u * (unsigned)(kABytes + half * kRowBytes);
+        int s = 0;
+        unsigned ph = 0;
+        for (int i = pair; i < tiles && ok; i += pairs) {
+            int m, n;
+            tile_at(g, i, m, n);
+            const int t0 = m * 256 + (int)rank * 128, n0 = n * g.bn + (int)rank * half;
+            for (int kb = 0; kb < nkb; ++kb) {
+                if (!wait_warp(&hd.empty[s], ph ^ 1u, hd, a.status, 2, s)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* st = base + (size_t)s * kTileStage;
+                const uint32_t bar = map_rank(smem_u32(&hd.full[s]), 0);
+                if (rank == 0) mbar_arrive_expect_tx_elect(&hd.full[s], bytes);
+                tma_load_pair_elect(st, &xmap, kb * (F8 ? 128 : 64), t0, bar, keep);
+                tma_load_pair_elect(st + kABytes, &wmap, kb * (F8 ? 128 : 64), n0, bar, keep);
+                advance(s, ph, kTileStages);
+            }
+        }
+        if (ok) drain(hd, s, ph, kTileStages, (int64_t)nkb * ((tiles - pair + pairs - 1) / pairs));
+    } else if (warp == 1 && rank == 0) {
+        const uint32_t idesc = mma_idesc(a.in_type, 256, g.bn);
+        int s = 0, buf = 0;
+        unsigned ph = 0, accph = 0;
+        for (int i = pair; i < tiles && ok; i += pairs) {
+            if (!wait_warp(&hd.acc_empty[buf], ((accph >> buf) & 1u) ^ 1u, hd, a.status, 4, buf)) break;
+            accph ^= 1u << buf;
+            tc_fence_after();
+            for (int kb = 0; kb < nkb; ++kb) {
+                if (!wait_warp(&hd.full[s], ph, hd, a.status, 1, s)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t ad = sw128_desc(smem_u32(base + (size_t)s * kTileStage));
+                const uint64_t bd = sw128_desc(smem_u32(base + (size_t)s * kTileStage + kABytes));
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_elect<F8, 2>(tmem + buf * 256, ad + 2 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
+                commit_pair_elect(&hd.empty[s]);
+                advance(s, ph, kTileStages);
+            }
+            if (!ok) break;
+            commit_pair_elect(&hd.acc_full[buf]);
+            buf ^= 1;
+        }
+    } else if (warp >= 2) {
+        const int q = warp & 3;
+        uint8_t* stage = epi + (warp - 2) * kEpiBytes;
+        int buf = 0;
+        unsigned accph = 0;
+        for (int i = pair; i < tiles; i += pairs) {
+            int m, n;
+            tile_at(g, i, m, n);
+            const int t0 = m * 256 + (int)rank * 128 + q * 32, n0 = n * g.bn;
+            if (!wait_warp(&hd.acc_full[buf], (accph >> buf) & 1u, hd, a.status, 3, buf)) break;
+            accph ^= 1u << buf;
+            tc_fence_after();
+            const int cols = min(g.bn, a.N - n0);
+            for (int c = 0; c < cols; c += 64) {
+                // 64 columns of 32 tokens: a lane holds a token; 16-byte piece j of its row goes to
+                // piece j ^ (row % 8), so neither side of the exchange meets a bank twice in 8 lanes
+#pragma unroll
+                for (int h = 0; h < 64; h += 16) {
+                    float v[16];
+                    tc_ld16(tmem + ((uint32_t)(q * 32) << 16) + buf * 256 + c + h, v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<float4*>(stage + lane * 256 + (((h / 4 + j) ^ (lane & 7)) << 4)) =
+                            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                }
+                __syncwarp();
+                // a lane takes 8 outputs of every fourth token: whole 128-byte lines of y and residual
+                const int nn = n0 + c + (lane & 7) * 8;
+#pragma unroll 2
+                for (int r = lane >> 3; r < 32; r += 4) {
+                    const float4 lo = *reinterpret_cast<const float4*>(stage + r * 256 + (((2 * (lane & 7)) ^ (r & 7)) << 4));
+                    const float4 hi =
+                        *reinterpret_cast<const float4*>(stage + r * 256 + (((2 * (lane & 7) + 1) ^ (r & 7)) << 4));
+                    float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    // columns past this tile belong to the next one
+                    if (t0 + r < a.T && c + (lane & 7) * 8 < cols) finish_any<8>(a, t0 + r, nn, v, vec);
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(map_rank(smem_u32(&hd.acc_empty[buf]), 0));
+            buf ^= 1;
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (*reinterpret_cast<volatile int*>(&hd.abort)) {
+        // a wait ran out: give the copies still in flight time to land before the CTA ends
+        const uint64_t t = globaltimer();
+        while (globaltimer() - t < 1000000ull) {
+        }
+    }
+    tc_fence_before();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+bool encode_rows(CUtensorMap* map, const LinearArgs& a, const void* p, int rows, int64_t stride, int box) {
+    const int es = type_bytes(a.in_type);
+    const CUtensorMapDataType dt = a.in_type == MOE_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : a.in_type == MOE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    return encode_tmap_2d(map, dt, p, (uint64_t)a.K, (uint64_t)rows, (uint64_t)(stride * es), kRowBytes / es, box,
+                          CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <bool F8>
+cudaError_t launch_split(const LinearArgs& a, int bn, int ksplit, bool vec, cudaStream_t st) {
+    CUtensorMap wmap, xmap;
+    if (!encode_rows(&wmap, a, a.w, a.N, a.w_stride, 128) || !encode_rows(&xmap, a, a.x, a.T, a.x_stride, bn))
+        return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> configured;
+    cudaError_t err = ensure_smem_limit((const void*)linear_split_kernel<F8>, kSplitSmem, configured);
+    if (err != cudaSuccess) return err;
+    int stages = kSplitRing / (kABytes + bn * kRowBytes);
+    if (stages > kMaxStages) stages = kMaxStages;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ksplit, (a.N + 127) / 128, (a.T + bn - 1) / bn);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSplitSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ksplit;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, linear_split_kernel<F8>, a, wmap, xmap, bn, stages, vec);
+}
+
+template <bool F8>
+cudaError_t launch_tiles(const LinearArgs& a, const TileGrid& g, bool vec, cudaStream_t st) {
+    CUtensorMap wmap, xmap;
+    if (!encode_rows(&wmap, a, a.w, a.N, a.w_stride, g.bn / 2) || !encode_rows(&xmap, a, a.x, a.T, a.x_stride, 128))
+        return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> configured;
+    cudaError_t err = ensure_smem_limit((const void*)linear_tile_kernel<F8>, kTileSmem, configured);
+    if (err != cudaSuccess) return err;
+    const int pairs = min(a.sm_count / 2, g.tm * g.tn);
+    return launch_pdl(linear_tile_kernel<F8>, dim3(2 * pairs), dim3(kThreads), kTileSmem, st, a, wmap, xmap, g, vec);
 }
 
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
-    return launch_pdl(linear_kernel, dim3((a.N + kTile - 1) / kTile, (a.T + kTile - 1) / kTile), dim3(kTile, kTile), 0,
-                      st, a);
+    const bool f8 = a.in_type == MOE_E4M3;
+    const bool vec = runs_aligned(a.y, a.y_type, 8, a.y_stride) && (!a.res || runs_aligned(a.res, a.y_type, 8, a.res_stride));
+    const int pairs = a.sm_count / 2;
+    // the width of the tiled kernel's tiles that leaves the least work to the last round
+    TileGrid g{(a.T + 255) / 256, 0, 0};
+    int64_t best = INT64_MAX;
+    for (int bn = 256; bn >= 128; bn -= 32) {
+        const int64_t tn = (a.N + bn - 1) / bn, rounds = (g.tm * tn + pairs - 1) / pairs;
+        const int64_t cost = rounds * (bn + 16);
+        if (cost < best) {
+            best = cost;
+            g.tn = (int)tn;
+            g.bn = bn;
+        }
+    }
+    if ((int64_t)g.tm * g.tn >= pairs) return f8 ? launch_tiles<true>(a, g, vec, st) : launch_tiles<false>(a, g, vec, st);
+    // fewer tiles than pairs: token blocks as even as they come, and K over what is left of the SMs
+    const int tz = (a.T + 255) / 256, bn = ((a.T + tz - 1) / tz + 15) / 16 * 16;
+    const int64_t blocks = (int64_t)((a.N + 127) / 128) * tz;
+    const int nkb = (int)(((int64_t)a.K * type_bytes(a.in_type) + kRowBytes - 1) / kRowBytes);
+    int ksplit = (int)(a.sm_count / blocks);
+    if (ksplit > kSplitMax) ksplit = kSplitMax;
+    if (ksplit > nkb) ksplit = nkb;
+    if (ksplit < 1) ksplit = 1;
+    return f8 ? launch_split<true>(a, bn, ksplit, vec, st) : launch_split<false>(a, bn, ksplit, vec, st);
 }
 
 }  // namespace moe

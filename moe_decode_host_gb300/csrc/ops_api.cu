@@ -36,6 +36,9 @@ int sm_count_now(int* out) {
     return MOE_OK;
 }
 
+// Most tokens and outputs of a moe_linear call: tile counts and grid dimensions stay in range.
+constexpr int kMaxExtent = 1 << 22;
+
 bool whole16(const void* p, int type, int64_t s0, int64_t s1) {
     return aligned(p, 16) && s0 * type_bytes(type) % 16 == 0 && s1 * type_bytes(type) % 16 == 0;
 }
@@ -153,8 +156,9 @@ int moe_kv_clear_status(moe_kv* kv) {
 
 int moe_linear(const void* x, int64_t x_stride, const void* w, int64_t w_stride, int in_type, int T, int N, int K,
                const float* x_scale, const float* w_scale, const void* bias, int bias_type, int act,
-               const void* residual, int64_t res_stride, void* y, int y_type, int64_t y_stride, void* stream) {
-    if (T < 0 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
+               const void* residual, int64_t res_stride, void* y, int y_type, int64_t y_stride, int* status_dev,
+               void* stream) {
+    if (T < 0 || N < 1 || K < 1 || N > kMaxExtent || T > kMaxExtent) return MOE_ERR_INVALID_ARG;
     if ((!is_float16(in_type) && in_type != MOE_E4M3) || !is_float_type(y_type)) return MOE_ERR_INVALID_ARG;
     if (act < MOE_ACT_NONE || act > MOE_ACT_GELU) return MOE_ERR_INVALID_ARG;
     if (bias && !is_float_type(bias_type)) return MOE_ERR_INVALID_ARG;
@@ -167,7 +171,7 @@ int moe_linear(const void* x, int64_t x_stride, const void* w, int64_t w_stride,
     if (x_stride < K || w_stride < K || (int64_t)K * type_bytes(in_type) % 16) return MOE_ERR_INVALID_ARG;
     if (!whole16(x, in_type, x_stride, 0) || !whole16(w, in_type, w_stride, 0)) return MOE_ERR_INVALID_ARG;
     LinearArgs a{x, w, in_type, x_stride, w_stride, T, N, K, x_scale, w_scale, bias, bias_type, act, residual,
-                 res_stride, y, y_type, y_stride, 0};
+                 res_stride, y, y_type, y_stride, status_dev, 0};
     const int rc = sm_count_now(&a.sm_count);
     if (rc != MOE_OK) return rc;
     return cuda_status(launch_linear(a, S(stream)));

@@ -196,13 +196,14 @@ def moe_kv_attend(kv: KvCache, q, page_table, lengths, out, scale=None, window=0
                             scale, window, op, o0, o1, zp, stream_handle(stream)), w)
 
 
-def moe_linear(x, w, y, bias=None, act="none", residual=None, x_scale=None, w_scale=None, stream=None):
+def moe_linear(x, w, y, bias=None, act="none", residual=None, x_scale=None, w_scale=None, status=None,
+               stream=None):
     """y = act(x w^T [* x_scale[t] * w_scale[n]] + bias) + residual.
 
     x [T, K] and w [N, K] of one type: bfloat16, float16, or float8_e4m3fn with
     x_scale fp32 [T] and w_scale fp32 [N]; y [T, N] bfloat16, float16 or float32;
     bias [N]; residual [T, N] of y's type (may be y); act "none", "relu", "silu" or
-    "gelu" (exact)."""
+    "gelu" (exact); status int32 [1], set to MOE_ERR_TIMEOUT if a device wait ran out."""
     f = "moe_linear"
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
         _refuse(f, "x is not [T, K] or w is not [N, K]")
@@ -226,6 +227,9 @@ def moe_linear(x, w, y, bias=None, act="none", residual=None, x_scale=None, w_sc
         xs = _vector(x_scale, T, torch.float32, f, "x_scale")
     if w_scale is not None:
         ws = _vector(w_scale, N, torch.float32, f, "w_scale")
+    sp = 0
+    if status is not None:
+        sp = _vector(status, 1, torch.int32, f, "status")
     a = _ACT.get(act, -1)
     check(lib.moe_linear(x.data_ptr(), x.stride(0), w.data_ptr(), w.stride(0), code, T, N, K, xs, ws, bp, bt, a, rp,
-                         rs, y.data_ptr(), yt, y.stride(0), stream_handle(stream)), f)
+                         rs, y.data_ptr(), yt, y.stride(0), sp, stream_handle(stream)), f)

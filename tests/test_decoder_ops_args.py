@@ -71,7 +71,7 @@ def _linear(m, **kw):
     a = dict(x=FAKE, xs=64, w=FAKE, ws=64, it=BF16, T=2, N=8, K=64, xsc=None, wsc=None, bias=None, bt=F32, act=0,
              res=None, rs=8, y=FAKE, yt=BF16, ys=8)
     a.update(kw)
-    return m.lib.moe_linear(*a.values(), None)
+    return m.lib.moe_linear(*a.values(), None, None)
 
 
 @pytest.mark.parametrize("bad", [

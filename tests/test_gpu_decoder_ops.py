@@ -542,13 +542,14 @@ def check_linear(m, g, T, N, K, xt, yt, act="none", bias=None, res=False, ragged
 @pytest.mark.parametrize("T,N,K", [(1, 1, 16), (1, 8, 64), (1, 4096, 4096), (2, 100, 208), (7, 384, 512), (16, 129, 256),
                                    (17, 1000, 1040), (32, 6144, 4096), (33, 65, 80), (64, 256, 4096), (65, 127, 144),
                                    (100, 4096, 64), (127, 640, 1024), (128, 128, 128), (129, 257, 272), (200, 72, 8192),
-                                   (256, 512, 4096), (511, 1021, 528), (1000, 1536, 768), (2049, 640, 320)])
+                                   (256, 512, 4096), (511, 1021, 528), (1000, 1536, 768), (2049, 640, 320),
+                                   (3000, 2056, 192), (5001, 1023, 80), (2500, 4100, 1040), (8192, 640, 4096)])
 @pytest.mark.parametrize("xt,yt", [(BF16, BF16), (F16, F32), (E4M3, BF16)])
 def test_linear(m, T, N, K, xt, yt):
     check_linear(m, gen(T + N + K), T, N, K, xt, yt)
 
 
-@pytest.mark.parametrize("T", [1, 5, 40, 130, 300])
+@pytest.mark.parametrize("T", [1, 5, 40, 130, 300, 10001])
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
 @pytest.mark.parametrize("xt,yt,bias,res", [(BF16, BF16, BF16, True), (BF16, F32, F32, False), (F16, F16, F16, True),
                                             (E4M3, BF16, F32, True), (E4M3, F32, None, True), (F16, BF16, None, False)])
