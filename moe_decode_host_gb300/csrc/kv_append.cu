@@ -23,6 +23,7 @@ constexpr int kAppendThreads = 256;
 
 template <int VEC>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+    grid_launch_next();
     grid_dep_wait();
     const int t = blockIdx.x;
     const int items = a.kv.head_dim / (2 * VEC);  // of one head

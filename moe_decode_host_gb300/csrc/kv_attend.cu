@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
     const uint32_t ring_u = smem_u32(ring), q_u = smem_u32(s_q);
     const int heads = a.kv.q_heads, group = heads / a.kv.kv_heads;
     const int per_b = a.kv.kv_heads * p.chunks;  // segments of a sequence
+    grid_launch_next();
     grid_dep_wait();
 
     // ---- sequences without a token, and lengths out of range ----

@@ -28,7 +28,9 @@ constexpr int kSplitRing = 196608;     // bytes of the split kernel's ring
 constexpr int kSplitMax = 8;           // CTAs of a cluster
 constexpr int kTileStages = 6;
 constexpr int kTileStage = 2 * kABytes;
-constexpr int kEpiBytes = 32 * 64 * 4;  // staging of an epilogue warp: 32 rows x 64 columns
+constexpr int kTileThreads = 320;       // the tiled kernel: warps 2-9 read the accumulators
+constexpr int kEpiWarps = 8;
+constexpr int kEpiBytes = 32 * 32 * 4;  // staging of one of them: 32 tokens x 32 outputs
 
 struct Head {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
@@ -36,7 +38,7 @@ struct Head {
     int abort;
 };
 constexpr int kSplitSmem = 1024 + kSplitRing + (int)sizeof(Head);
-constexpr int kTileSmem = 1024 + kTileStages * kTileStage + 4 * kEpiBytes + (int)sizeof(Head);
+constexpr int kTileSmem = 1024 + kTileStages * kTileStage + kEpiWarps * kEpiBytes + (int)sizeof(Head);
 static_assert(kTileSmem <= 227 * 1024, "shared memory of a CTA");
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -105,53 +107,79 @@ __device__ __forceinline__ uint32_t mma_idesc(int in_type, int m, int n) {
     return (1u << 4) | (f << 7) | (f << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-__device__ __forceinline__ float activate(float v, int act) {
-    if (act == MOE_ACT_RELU) return v < 0.f ? 0.f : v;
-    if (act == MOE_ACT_SILU) return v / (1.f + expf(-v));
-    if (act == MOE_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678f));
-    return v;
+// GELU(v) = v * Phi(v).  Phi(-|v|) = erfc(|v| / sqrt 2) / 2 by Abramowitz and Stegun 7.1.26
+// (t = 1 / (1 + p x), a polynomial in t times exp(-x^2); absolute error of erf 1.5e-7).
+__device__ __forceinline__ float gelu(float v) {
+    const float x = fabsf(v) * 0.70710678f;
+    const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+    float p = fmaf(1.061405429f, t, -1.453152027f);
+    p = fmaf(p, t, 1.421413741f);
+    p = fmaf(p, t, -0.284496736f);
+    p = fmaf(p, t, 0.254829592f);
+    const float tail = 0.5f * p * t * __expf(-x * x);
+    return v * (v > 0.f ? 1.f - tail : tail);
 }
 
-// VEC consecutive outputs of token t from n on, all in range.
 template <int VEC>
-__device__ __forceinline__ void finish(const LinearArgs& a, int64_t t, int n, float (&v)[VEC]) {
-    if (a.x_scale) {
-        const float sx = a.x_scale[t];
+__device__ __forceinline__ void activate(float (&v)[VEC], int act) {
+    if (act == MOE_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] *= sx * a.w_scale[n + i];
-    }
-    if (a.bias) {
+        for (int i = 0; i < VEC; ++i) v[i] = gelu(v[i]);
+    } else if (act == MOE_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            v[i] += a.bias_type == MOE_F32 ? static_cast<const float*>(a.bias)[n + i]
-                                           : half_bits_to_f32(static_cast<const uint16_t*>(a.bias)[n + i], a.bias_type);
-    }
-    if (a.act != MOE_ACT_NONE) {
+        for (int i = 0; i < VEC; ++i) v[i] = __fdividef(v[i], 1.f + __expf(-v[i]));
+    } else if (act == MOE_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = activate(v[i], a.act);
+        for (int i = 0; i < VEC; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];
     }
-    if (a.res) {
-        Raw<VEC> r;
-        float f[VEC];
-        r.load(a.res, t * a.res_stride + n, a.y_type);
-        r.get(a.y_type, f);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] += f[i];
-    }
-    store_run<VEC>(a.y, t * a.y_stride + n, a.y_type, v);
 }
 
-// The same where the run may reach past N or is not aligned.
+// Scales and biases of VEC outputs from n on (1 and 0 where there are none).
 template <int VEC>
-__device__ __forceinline__ void finish_any(const LinearArgs& a, int64_t t, int n, float (&v)[VEC], bool vec) {
-    if (vec && n + VEC <= a.N) {
-        finish<VEC>(a, t, n, v);
+struct Columns {
+    float scale[VEC], bias[VEC];
+    __device__ __forceinline__ void load(const LinearArgs& a, int n) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            scale[i] = a.w_scale && n + i < a.N ? a.w_scale[n + i] : 1.f;
+            bias[i] = 0.f;
+            if (a.bias && n + i < a.N)
+                bias[i] = a.bias_type == MOE_F32
+                              ? static_cast<const float*>(a.bias)[n + i]
+                              : half_bits_to_f32(static_cast<const uint16_t*>(a.bias)[n + i], a.bias_type);
+        }
+    }
+};
+
+// The epilogue of VEC outputs of token t from n on; `whole`: all in range and aligned.
+// res holds the residual's bits when whole, loaded ahead.
+template <int VEC>
+__device__ __forceinline__ void finish(const LinearArgs& a, int64_t t, int n, float sx, const Columns<VEC>& col,
+                                       const Raw<VEC>& res, float (&v)[VEC], bool whole) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = fmaf(v[i], sx * col.scale[i], col.bias[i]);
+    activate<VEC>(v, a.act);
+    if (whole) {
+        if (a.res) {
+            float f[VEC];
+            res.get(a.y_type, f);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] += f[i];
+        }
+        store_run<VEC>(a.y, t * a.y_stride + n, a.y_type, v);
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             if (n + i < a.N) {
                 float one[1] = {v[i]};
-                finish<1>(a, t, n + i, one);
+                if (a.res) {
+                    Raw<1> r;
+                    float f[1];
+                    r.load(a.res, t * a.res_stride + n + i, a.y_type);
+                    r.get(a.y_type, f);
+                    one[0] += f[0];
+                }
+                store_run<1>(a.y, t * a.y_stride + n + i, a.y_type, one);
             }
         }
     }
@@ -175,6 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int stage_bytes = kABytes + bn * kRowBytes;
     const int tcols = bn <= 32 ? 32 : (bn <= 64 ? 64 : (bn <= 128 ? 128 : 256));
     if (threadIdx.x == 0) {
+        prefetch_tmap(&wmap);
+        prefetch_tmap(&xmap);
         hd.abort = 0;
         for (int s = 0; s < stages; ++s) {
             mbar_init(&hd.full[s], 1);
@@ -193,7 +223,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = hd.tmem;
+    grid_launch_next();
     grid_dep_wait();
+    // ---- this rank's tokens are [c0, c1); thread x of the last four warps finishes outputs
+    // 4 (x % 32) .. + 3 of every fourth, and has their scales, biases and first residuals
+    // in hand before the sums are ----
+    const int cols = min(bn, a.T - t0);
+    const int c0 = cols * rank / S, c1 = cols * (rank + 1) / S;
+    const int mine = n0 + lane * 4;
+    const bool whole = vec && mine + 4 <= a.N;
+    Columns<4> col;
+    Raw<4> res[2];
+    float sx[2] = {1.f, 1.f};
+    if (warp >= 2) {
+        col.load(a, mine);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c = c0 + warp - 2 + 4 * k;
+            if (c < c1) {
+                if (a.res && whole) res[k].load(a.res, (int64_t)(t0 + c) * a.res_stride + mine, a.y_type);
+                if (a.x_scale) sx[k] = a.x_scale[t0 + c];
+            }
+        }
+    }
     if (warp == 0) {
         const uint64_t first = l2_policy_evict_first(), last = l2_policy_evict_last();
         int s = 0;
@@ -225,7 +277,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // ---- sums to shared memory, [token][128 outputs]; the ring is idle by then ----
     float* dump = reinterpret_cast<float*>(base);
-    const int cols = min(bn, a.T - t0);
     if (warp >= 2) {
         const int q = warp & 3;
         wait_warp(&hd.acc_full[0], 0, hd, a.status, 3, 0);
@@ -244,29 +295,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tcols) : "memory");
     }
-    // ---- this rank's tokens: the parts in rank order, then the epilogue ----
-    const int c0 = cols * rank / S, c1 = cols * (rank + 1) / S;
-    for (int i = threadIdx.x; i < (c1 - c0) * 32; i += kThreads) {
-        const int c = c0 + i / 32, r = i % 32 * 4;
-        if (n0 + r >= a.N) continue;
-        const uint32_t at = smem_u32(dump + c * 128 + r);
-        float4 p[kSplitMax];
+    // ---- the parts in rank order, then the epilogue ----
+    if (warp >= 2) {
+        int k = 0;
+        for (int c = c0 + warp - 2; c < c1; c += 4, ++k) {
+            const uint32_t at = smem_u32(dump + c * 128 + lane * 4);
+            float4 p[kSplitMax];
 #pragma unroll
-        for (int k = 0; k < kSplitMax; ++k)
-            if (k < S)
-                asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                             : "=f"(p[k].x), "=f"(p[k].y), "=f"(p[k].z), "=f"(p[k].w)
-                             : "r"(map_rank(at, k)));
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < kSplitMax; ++j)
+                if (j < S)
+                    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                 : "=f"(p[j].x), "=f"(p[j].y), "=f"(p[j].z), "=f"(p[j].w)
+                                 : "r"(map_rank(at, j)));
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < kSplitMax; ++k)
-            if (k < S) {
-                v[0] += p[k].x;
-                v[1] += p[k].y;
-                v[2] += p[k].z;
-                v[3] += p[k].w;
+            for (int j = 0; j < kSplitMax; ++j)
+                if (j < S) {
+                    v[0] += p[j].x;
+                    v[1] += p[j].y;
+                    v[2] += p[j].z;
+                    v[3] += p[j].w;
+                }
+            if (mine >= a.N) continue;
+            Raw<4> r = k == 0 ? res[0] : res[1];
+            float s = k == 0 ? sx[0] : sx[1];
+            if (k > 1) {
+                if (a.res && whole) r.load(a.res, (int64_t)(t0 + c) * a.res_stride + mine, a.y_type);
+                s = a.x_scale ? a.x_scale[t0 + c] : 1.f;
             }
-        finish_any<4>(a, t0 + c, n0 + r, v, vec);
+            finish<4>(a, t0 + c, mine, s, col, r, v, whole);
+        }
     }
     __syncwarp();
     cluster_sync();  // the others may still read this CTA's sums
@@ -309,18 +367,20 @@ __device__ __forceinline__ void tile_at(const TileGrid& g, int i, int& m, int& n
 }
 
 template <bool F8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     linear_tile_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap wmap,
                        const __grid_constant__ CUtensorMap xmap, const TileGrid g, bool vec) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* epi = base + kTileStages * kTileStage;
-    Head& hd = *reinterpret_cast<Head*>(epi + 4 * kEpiBytes);
+    Head& hd = *reinterpret_cast<Head*>(epi + kEpiWarps * kEpiBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int nkb = (int)(((int64_t)a.K * (F8 ? 1 : 2) + kRowBytes - 1) / kRowBytes);
     const int tiles = g.tm * g.tn, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
     if (threadIdx.x == 0) {
+        prefetch_tmap(&wmap);
+        prefetch_tmap(&xmap);
         hd.abort = 0;
         for (int s = 0; s < kTileStages; ++s) {
             mbar_init(&hd.full[s], 1);
@@ -328,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&hd.acc_full[s], 1);
-            mbar_init(&hd.acc_empty[s], 8);
+            mbar_init(&hd.acc_empty[s], 2 * kEpiWarps);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -343,6 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = hd.tmem;
+    grid_launch_next();
     grid_dep_wait();
     bool ok = true;
     if (warp == 0) {
@@ -409,29 +470,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             accph ^= 1u << buf;
             tc_fence_after();
             const int cols = min(g.bn, a.N - n0);
-            for (int c = 0; c < cols; c += 64) {
-                // 64 columns of 32 tokens: a lane holds a token; 16-byte piece j of its row goes to
-                // piece j ^ (row % 8), so neither side of the exchange meets a bank twice in 8 lanes
+            // two warps share a quarter of the lanes and take every other 32 outputs
+            for (int c = (warp - 2) / 4 * 32; c < cols; c += 64) {
+                // on the way out a lane takes 8 outputs of every eighth token; their scales, biases and
+                // residuals are fetched while the sums go through shared memory
+                const int nn = n0 + c + (lane & 3) * 8;
+                const bool in = nn < n0 + cols, whole = vec && nn + 8 <= a.N;
+                Columns<8> col;
+                Raw<8> res[4];
+                float sx[4];
+                if (in) {
+                    col.load(a, nn);
 #pragma unroll
-                for (int h = 0; h < 64; h += 16) {
-                    float v[16];
-                    tc_ld16(tmem + ((uint32_t)(q * 32) << 16) + buf * 256 + c + h, v);
+                    for (int k = 0; k < 4; ++k) {
+                        const int t = t0 + (lane >> 2) + 8 * k;
+                        sx[k] = 1.f;
+                        if (t < a.T) {
+                            if (a.res && whole) res[k].load(a.res, (int64_t)t * a.res_stride + nn, a.y_type);
+                            if (a.x_scale) sx[k] = a.x_scale[t];
+                        }
+                    }
+                }
+                // in: a lane holds a token.  16-byte piece j of its row goes to piece j ^ (row % 8): neither
+                // side of the exchange meets a bank twice within 8 lanes
+                float v0[16], v1[16];
+                const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + buf * 256 + c;
+                tc_ld16x2(at, at + 16, v0, v1);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<float4*>(stage + lane * 256 + (((h / 4 + j) ^ (lane & 7)) << 4)) =
-                            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                for (int j = 0; j < 4; ++j) {
+                    *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                        make_float4(v0[4 * j], v0[4 * j + 1], v0[4 * j + 2], v0[4 * j + 3]);
+                    *reinterpret_cast<float4*>(stage + lane * 128 + (((j + 4) ^ (lane & 7)) << 4)) =
+                        make_float4(v1[4 * j], v1[4 * j + 1], v1[4 * j + 2], v1[4 * j + 3]);
                 }
                 __syncwarp();
-                // a lane takes 8 outputs of every fourth token: whole 128-byte lines of y and residual
-                const int nn = n0 + c + (lane & 7) * 8;
-#pragma unroll 2
-                for (int r = lane >> 3; r < 32; r += 4) {
-                    const float4 lo = *reinterpret_cast<const float4*>(stage + r * 256 + (((2 * (lane & 7)) ^ (r & 7)) << 4));
-                    const float4 hi =
-                        *reinterpret_cast<const float4*>(stage + r * 256 + (((2 * (lane & 7) + 1) ^ (r & 7)) << 4));
-                    float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                    // columns past this tile belong to the next one
-                    if (t0 + r < a.T && c + (lane & 7) * 8 < cols) finish_any<8>(a, t0 + r, nn, v, vec);
+                if (in) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = (lane >> 2) + 8 * k;
+                        const uint8_t* row = stage + r * 128;
+                        const float4 lo = *reinterpret_cast<const float4*>(row + (((2 * (lane & 3)) ^ (r & 7)) << 4));
+                        const float4 hi = *reinterpret_cast<const float4*>(row + (((2 * (lane & 3) + 1) ^ (r & 7)) << 4));
+                        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                        if (t0 + r < a.T) finish<8>(a, t0 + r, nn, sx[k], col, res[k], v, whole);
+                    }
                 }
                 __syncwarp();
             }
@@ -502,7 +584,7 @@ cudaError_t launch_tiles(const LinearArgs& a, const TileGrid& g, bool vec, cudaS
     cudaError_t err = ensure_smem_limit((const void*)linear_tile_kernel<F8>, kTileSmem, configured);
     if (err != cudaSuccess) return err;
     const int pairs = min(a.sm_count / 2, g.tm * g.tn);
-    return launch_pdl(linear_tile_kernel<F8>, dim3(2 * pairs), dim3(kThreads), kTileSmem, st, a, wmap, xmap, g, vec);
+    return launch_pdl(linear_tile_kernel<F8>, dim3(2 * pairs), dim3(kTileThreads), kTileSmem, st, a, wmap, xmap, g, vec);
 }
 
 }  // namespace

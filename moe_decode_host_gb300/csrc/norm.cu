@@ -21,6 +21,7 @@ constexpr int kNormThreads = 1024;
 template <int VEC, int NV>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a) {
     __shared__ float2 part[kNormThreads / 32];
+    grid_launch_next();
     grid_dep_wait();
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = row < a.T;
