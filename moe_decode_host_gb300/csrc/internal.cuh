@@ -18,14 +18,18 @@ constexpr int kMaxSwaps = 64;
 // Raises a kernel's dynamic shared-memory limit to `bytes` once per device (the
 // attribute belongs to the device the calling thread has current): `done` holds
 // one bit per device ordinal below 64; higher ordinals set it on every call.
-// Setting it twice is harmless, so racing first calls need no lock.
-inline cudaError_t ensure_smem_limit(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+// Setting it twice is harmless, so racing first calls need no lock.  `whole`: also asks
+// for the SM's whole shared memory, so that launches below the limit run several CTAs
+// an SM.
+inline cudaError_t ensure_smem_limit(const void* kernel, int bytes, std::atomic<uint64_t>& done, bool whole = false) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
     if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && whole)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_release);
     return e;
 }

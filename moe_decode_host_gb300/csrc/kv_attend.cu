@@ -611,7 +611,7 @@ cudaError_t launch(const AttendArgs& a, const Plan& p, cudaStream_t st) {
     static std::atomic<uint64_t> configured;
     const int smem = smem_of(a.kv, p);
     // one limit serves every head_dim of the class; the CTAs share the SM's whole memory
-    cudaError_t err = ensure_smem_limit((const void*)attend_kernel<T, DP, NT>, (DP <= 128 ? 113 : 224) * 1024, configured);
+    cudaError_t err = ensure_smem_limit((const void*)attend_kernel<T, DP, NT>, (DP <= 128 ? 113 : 224) * 1024, configured, true);
     if (err != cudaSuccess) return err;
     const int64_t per_b = (int64_t)a.kv.kv_heads * p.chunks;
     const int64_t room = room_of(a);

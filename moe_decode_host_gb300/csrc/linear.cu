@@ -20,24 +20,25 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 192;          // warp 0 loads, warp 1 issues, warps 2-5 read the accumulators
+constexpr int kEpiWarps = 8;           // warps 2-9 read the accumulators and finish the outputs
+constexpr int kThreads = 64 + 32 * kEpiWarps;  // warp 0 loads, warp 1 issues
 constexpr int kRowBytes = 128;         // bytes of K in a stage
 constexpr int kABytes = 128 * kRowBytes;
 constexpr int kMaxStages = 12;
-constexpr int kSplitRing = 196608;     // bytes of the split kernel's ring
+// Bytes of the split kernel's ring, CTAS of which share an SM: two while a token block's
+// sums ([128][128] fp32 at most) fit the smaller ring, so that more clusters run at once.
+__host__ __device__ constexpr int split_ring(int ctas) { return ctas == 2 ? 104 * 1024 : 192 * 1024; }
 constexpr int kSplitMax = 8;           // CTAs of a cluster
 constexpr int kTileStages = 6;
 constexpr int kTileStage = 2 * kABytes;
-constexpr int kTileThreads = 320;       // the tiled kernel: warps 2-9 read the accumulators
-constexpr int kEpiWarps = 8;
-constexpr int kEpiBytes = 32 * 32 * 4;  // staging of one of them: 32 tokens x 32 outputs
+constexpr int kEpiBytes = 32 * 32 * 4;  // staging of an epilogue warp of the tiled kernel: 32 tokens x 32 outputs
 
 struct Head {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int abort;
 };
-constexpr int kSplitSmem = 1024 + kSplitRing + (int)sizeof(Head);
+constexpr int split_smem(int ctas) { return 1024 + split_ring(ctas) + (int)sizeof(Head); }
 constexpr int kTileSmem = 1024 + kTileStages * kTileStage + kEpiWarps * kEpiBytes + (int)sizeof(Head);
 static_assert(kTileSmem <= 227 * 1024, "shared memory of a CTA");
 
@@ -53,6 +54,15 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
 }
 
 // A wait taken by a whole converged warp; false when it ran out.
@@ -188,13 +198,13 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int64_t t, int n, fl
 // ---- split kernel ------------------------------------------------------------
 
 // Grid: x the cluster's K parts, y blocks of 128 outputs, z blocks of bn tokens.
-template <bool F8>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool F8, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS)
     linear_split_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap wmap,
                         const __grid_constant__ CUtensorMap xmap, int bn, int stages, bool vec) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    Head& hd = *reinterpret_cast<Head*>(base + kSplitRing);
+    Head& hd = *reinterpret_cast<Head*>(base + split_ring(CTAS));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = gridDim.x, rank = blockIdx.x;
     const int n0 = blockIdx.y * 128, t0 = blockIdx.z * bn;
@@ -225,21 +235,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = hd.tmem;
     grid_launch_next();
     grid_dep_wait();
-    // ---- this rank's tokens are [c0, c1); thread x of the last four warps finishes outputs
-    // 4 (x % 32) .. + 3 of every fourth, and has their scales, biases and first residuals
-    // in hand before the sums are ----
+    // ---- this rank's tokens are [c0, c1); each epilogue warp finishes every eighth, four
+    // outputs a lane, and has their scales, biases and first residuals in hand before the
+    // sums are ----
     const int cols = min(bn, a.T - t0);
     const int c0 = cols * rank / S, c1 = cols * (rank + 1) / S;
     const int mine = n0 + lane * 4;
     const bool whole = vec && mine + 4 <= a.N;
     Columns<4> col;
-    Raw<4> res[2];
+    Raw<4> res[CTAS == 1 ? 2 : 1];
     float sx[2] = {1.f, 1.f};
     if (warp >= 2) {
         col.load(a, mine);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int c = c0 + warp - 2 + 4 * k;
+        for (int k = 0; k < (CTAS == 1 ? 2 : 1); ++k) {
+            const int c = c0 + warp - 2 + kEpiWarps * k;
             if (c < c1) {
                 if (a.res && whole) res[k].load(a.res, (int64_t)(t0 + c) * a.res_stride + mine, a.y_type);
                 if (a.x_scale) sx[k] = a.x_scale[t0 + c];
@@ -281,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = warp & 3;
         wait_warp(&hd.acc_full[0], 0, hd, a.status, 3, 0);
         tc_fence_after();
-        for (int c = 0; c < cols; c += 16) {
+        for (int c = (warp - 2) / 4 * 16; c < cols; c += 32) {  // two warps share a quarter of the lanes
             float v[16];
             tc_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, v);
 #pragma unroll
@@ -297,33 +307,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // ---- the parts in rank order, then the epilogue ----
     if (warp >= 2) {
-        int k = 0;
-        for (int c = c0 + warp - 2; c < c1; c += 4, ++k) {
-            const uint32_t at = smem_u32(dump + c * 128 + lane * 4);
-            float4 p[kSplitMax];
-#pragma unroll
-            for (int j = 0; j < kSplitMax; ++j)
-                if (j < S)
-                    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                                 : "=f"(p[j].x), "=f"(p[j].y), "=f"(p[j].z), "=f"(p[j].w)
-                                 : "r"(map_rank(at, j)));
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
+        // two tokens at a time where there are registers for the parts of both on their way together
+        constexpr int kAhead = CTAS == 1 ? 2 : 1;
+        for (int c = c0 + warp - 2, k = 0; c < c1; c += kAhead * kEpiWarps, ++k) {
+            float4 p[kAhead][kSplitMax];
 #pragma unroll
             for (int j = 0; j < kSplitMax; ++j)
                 if (j < S) {
-                    v[0] += p[j].x;
-                    v[1] += p[j].y;
-                    v[2] += p[j].z;
-                    v[3] += p[j].w;
+#pragma unroll
+                    for (int h = 0; h < kAhead; ++h)  // a second token past the end rereads the first
+                        p[h][j] = ld_cluster(map_rank(smem_u32(dump + (c + (c + kEpiWarps * h < c1 ? kEpiWarps * h : 0)) * 128 + lane * 4), j));
                 }
-            if (mine >= a.N) continue;
-            Raw<4> r = k == 0 ? res[0] : res[1];
-            float s = k == 0 ? sx[0] : sx[1];
-            if (k > 1) {
-                if (a.res && whole) r.load(a.res, (int64_t)(t0 + c) * a.res_stride + mine, a.y_type);
-                s = a.x_scale ? a.x_scale[t0 + c] : 1.f;
+            if (k > 0 && mine < a.N) {
+#pragma unroll
+                for (int h = 0; h < kAhead; ++h) {
+                    const int t = t0 + c + kEpiWarps * h;
+                    if (c + kEpiWarps * h < c1) {
+                        if (a.res && whole) res[h].load(a.res, (int64_t)t * a.res_stride + mine, a.y_type);
+                        if (a.x_scale) sx[h] = a.x_scale[t];
+                    }
+                }
             }
-            finish<4>(a, t0 + c, mine, s, col, r, v, whole);
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h) {
+                float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < kSplitMax; ++j)
+                    if (j < S) {
+                        v[0] += p[h][j].x;
+                        v[1] += p[h][j].y;
+                        v[2] += p[h][j].z;
+                        v[3] += p[h][j].w;
+                    }
+                if (mine < a.N && c + kEpiWarps * h < c1)
+                    finish<4>(a, t0 + c + kEpiWarps * h, mine, sx[h], col, res[h], v, whole);
+            }
         }
     }
     __syncwarp();
@@ -367,7 +385,7 @@ __device__ __forceinline__ void tile_at(const TileGrid& g, int i, int& m, int& n
 }
 
 template <bool F8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_tile_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap wmap,
                        const __grid_constant__ CUtensorMap xmap, const TileGrid g, bool vec) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -548,20 +566,71 @@ bool encode_rows(CUtensorMap* map, const LinearArgs& a, const void* p, int rows,
                           CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <bool F8>
-cudaError_t launch_split(const LinearArgs& a, int bn, int ksplit, bool vec, cudaStream_t st) {
+// A cluster's CTAs: the most (up to kSplitMax and the blocks of K) with which all blocks of
+// outputs still run at once, for a second round costs more than a longer pass over K
+// (32 x 6144 x 4096 E4M3, 48 blocks: 8.1 us with 2, 6.7 with 3 to 5, 11.4 with 6, of which
+// 46 fit).  How many clusters of a size run at once is asked of the runtime, once a device,
+// for a kernel of the same footprint without tensor memory: for one that allocates tensor
+// memory the runtime answers as if each CTA took all 512 columns.
+template <int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) footprint_kernel() {}
+
+template <int CTAS>
+cudaError_t cluster_size(int64_t blocks, int nkb, int* out) {
+    static std::atomic<int> known[64][kSplitMax + 1];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    static std::atomic<uint64_t> configured;
+    err = ensure_smem_limit((const void*)footprint_kernel<CTAS>, split_smem(CTAS), configured, true);
+    if (err != cudaSuccess) return err;
+    *out = 1;
+    for (int s = min(kSplitMax, nkb); s > 1; --s) {
+        std::atomic<int>* slot = dev < 64 ? &known[dev][s] : nullptr;
+        int n = slot ? slot->load(std::memory_order_relaxed) : 0;
+        if (n == 0) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(s);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = split_smem(CTAS);
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = s;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            err = cudaOccupancyMaxActiveClusters(&n, footprint_kernel<CTAS>, &cfg);
+            if (err != cudaSuccess) return err;
+            if (n < 1) n = 1;
+            if (slot) slot->store(n, std::memory_order_relaxed);
+        }
+        if (n >= blocks) {
+            *out = s;
+            break;
+        }
+    }
+    return cudaSuccess;
+}
+
+template <bool F8, int CTAS>
+cudaError_t launch_split(const LinearArgs& a, int bn, bool vec, cudaStream_t st) {
     CUtensorMap wmap, xmap;
     if (!encode_rows(&wmap, a, a.w, a.N, a.w_stride, 128) || !encode_rows(&xmap, a, a.x, a.T, a.x_stride, bn))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> configured;
-    cudaError_t err = ensure_smem_limit((const void*)linear_split_kernel<F8>, kSplitSmem, configured);
+    cudaError_t err = ensure_smem_limit((const void*)linear_split_kernel<F8, CTAS>, split_smem(CTAS), configured, true);
     if (err != cudaSuccess) return err;
-    int stages = kSplitRing / (kABytes + bn * kRowBytes);
+    const int tz = (a.T + bn - 1) / bn;
+    const int nkb = (int)(((int64_t)a.K * type_bytes(a.in_type) + kRowBytes - 1) / kRowBytes);
+    int ksplit = 1;
+    err = cluster_size<CTAS>((int64_t)((a.N + 127) / 128) * tz, nkb, &ksplit);
+    if (err != cudaSuccess) return err;
+    int stages = split_ring(CTAS) / (kABytes + bn * kRowBytes);
     if (stages > kMaxStages) stages = kMaxStages;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ksplit, (a.N + 127) / 128, (a.T + bn - 1) / bn);
+    cfg.gridDim = dim3(ksplit, (a.N + 127) / 128, tz);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSplitSmem;
+    cfg.dynamicSmemBytes = split_smem(CTAS);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -572,7 +641,7 @@ cudaError_t launch_split(const LinearArgs& a, int bn, int ksplit, bool vec, cuda
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, linear_split_kernel<F8>, a, wmap, xmap, bn, stages, vec);
+    return cudaLaunchKernelEx(&cfg, linear_split_kernel<F8, CTAS>, a, wmap, xmap, bn, stages, vec);
 }
 
 template <bool F8>
@@ -584,7 +653,7 @@ cudaError_t launch_tiles(const LinearArgs& a, const TileGrid& g, bool vec, cudaS
     cudaError_t err = ensure_smem_limit((const void*)linear_tile_kernel<F8>, kTileSmem, configured);
     if (err != cudaSuccess) return err;
     const int pairs = min(a.sm_count / 2, g.tm * g.tn);
-    return launch_pdl(linear_tile_kernel<F8>, dim3(2 * pairs), dim3(kTileThreads), kTileSmem, st, a, wmap, xmap, g, vec);
+    return launch_pdl(linear_tile_kernel<F8>, dim3(2 * pairs), dim3(kThreads), kTileSmem, st, a, wmap, xmap, g, vec);
 }
 
 }  // namespace
@@ -607,15 +676,10 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st) {
         }
     }
     if ((int64_t)g.tm * g.tn >= pairs) return f8 ? launch_tiles<true>(a, g, vec, st) : launch_tiles<false>(a, g, vec, st);
-    // fewer tiles than pairs: token blocks as even as they come, and K over what is left of the SMs
+    // fewer tiles than pairs: token blocks as even as they come, and K over what is left of the GPU
     const int tz = (a.T + 255) / 256, bn = ((a.T + tz - 1) / tz + 15) / 16 * 16;
-    const int64_t blocks = (int64_t)((a.N + 127) / 128) * tz;
-    const int nkb = (int)(((int64_t)a.K * type_bytes(a.in_type) + kRowBytes - 1) / kRowBytes);
-    int ksplit = (int)(a.sm_count / blocks);
-    if (ksplit > kSplitMax) ksplit = kSplitMax;
-    if (ksplit > nkb) ksplit = nkb;
-    if (ksplit < 1) ksplit = 1;
-    return f8 ? launch_split<true>(a, bn, ksplit, vec, st) : launch_split<false>(a, bn, ksplit, vec, st);
+    if (bn <= 128) return f8 ? launch_split<true, 2>(a, bn, vec, st) : launch_split<false, 2>(a, bn, vec, st);
+    return f8 ? launch_split<true, 1>(a, bn, vec, st) : launch_split<false, 1>(a, bn, vec, st);
 }
 
 }  // namespace moe
