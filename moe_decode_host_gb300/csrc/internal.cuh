@@ -217,6 +217,8 @@ struct NormArgs {
     int y_type;
     int64_t y_stride;
     float* scale;  // [T], E4M3 output only
+    float inv_h;   // 1 / H
+    int sm_count;
 };
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);
 

@@ -11,8 +11,9 @@
 // Memory bound: q, k, v in, q_out and the slots out, each once.  An item is 2 * VEC
 // elements of one head that hold VEC whole pairs (two runs rot/2 apart, or one double
 // run), so in both pairings item j uses table entries [j VEC, j VEC + VEC).  Thread x of
-// a CTA keeps item x % items of its token and walks the heads: its table entries are
-// read once.
+// a token's CTA keeps item x % items and takes heads x / items + i * step, kHeads of them
+// at once: their loads are issued before the token's position is known, and its table
+// entries are read once.
 #include "ptx.cuh"
 #include "vec.cuh"
 
@@ -20,16 +21,19 @@ namespace moe {
 namespace {
 
 constexpr int kAppendThreads = 256;
+constexpr int kHeads = 4;
 
-template <int VEC>
+// WIDE: q, k and v may be fp32.
+template <int VEC, bool WIDE>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
     grid_launch_next();
     grid_dep_wait();
     const int t = blockIdx.x;
     const int items = a.kv.head_dim / (2 * VEC);  // of one head
     const int j = threadIdx.x % items;
-    const int step = kAppendThreads / items;
-    if (threadIdx.x >= step * items) return;
+    const int step = blockDim.x / items;
+    const int g = threadIdx.x / items;
+    if (g >= step) return;
     const int half = a.rot / 2;
     const bool turn = j * VEC < half;  // whether the item is rotated, else copied
     // element offsets of the item's two runs
@@ -41,6 +45,22 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
         e0 = j * VEC;
         e1 = e0 + half;
     }
+    const int hq = a.kv.q_heads, hkv = a.kv.kv_heads, heads = hq + 2 * hkv;
+    Raw<VEC, WIDE> r0[kHeads], r1[kHeads];
+    auto fetch = [&](int h0) {
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            const int h = h0 + i * step;
+            if (h >= heads) break;
+            const void* src = h < hq ? a.q : (h < hq + hkv ? a.k : a.v);
+            const int64_t at = h < hq         ? t * a.q_ts + h * a.q_hs
+                               : h < hq + hkv ? t * a.k_ts + (h - hq) * a.k_hs
+                                              : t * a.v_ts + (h - hq - hkv) * a.v_hs;
+            r0[i].load(src, at + e0, a.type);
+            r1[i].load(src, at + e1, a.type);
+        }
+    };
+    fetch(g);
     const int pos = a.rot > 0 ? a.positions[t] : 0;
     if (a.rot > 0 && (pos < 0 || pos >= a.n_positions)) {  // no table row: nothing of this token is written
         if (threadIdx.x == 0) set_status(a.kv.status, MOE_ERR_BAD_INDEX);
@@ -67,63 +87,61 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
             sn[i] = row[half + i];
         }
     }
-    const int hq = a.kv.q_heads, hkv = a.kv.kv_heads;
-    for (int h = threadIdx.x / items; h < hq + 2 * hkv; h += step) {
-        const int kind = h < hq ? 0 : (h < hq + hkv ? 1 : 2);
-        if (kind != 0 && !put) continue;
-        const int hh = kind == 0 ? h : (kind == 1 ? h - hq : h - hq - hkv);
-        const void* src = kind == 0 ? a.q : (kind == 1 ? a.k : a.v);
-        const int64_t at = kind == 0   ? t * a.q_ts + hh * a.q_hs
-                           : kind == 1 ? t * a.k_ts + hh * a.k_hs
-                                       : t * a.v_ts + hh * a.v_hs;
-        Raw<VEC> r0, r1;
-        r0.load(src, at + e0, a.type);
-        r1.load(src, at + e1, a.type);
-        float x0[VEC], x1[VEC];
-        r0.get(a.type, x0);
-        r1.get(a.type, x1);
-        if (turn && kind != 2) {
-            if (a.interleaved) {
-                // pair i is elements 2i, 2i + 1 of the double run
-                if constexpr (VEC == 1) {
-                    const float p = x0[0], q = x1[0];
-                    x0[0] = p * cs[0] - q * sn[0];
-                    x1[0] = p * sn[0] + q * cs[0];
+    for (int h0 = g; h0 < heads; h0 += kHeads * step) {
+        if (h0 != g) fetch(h0);
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            const int h = h0 + i * step;
+            if (h >= heads) break;
+            const int kind = h < hq ? 0 : (h < hq + hkv ? 1 : 2);
+            if (kind != 0 && !put) continue;
+            const int hh = kind == 0 ? h : (kind == 1 ? h - hq : h - hq - hkv);
+            float x0[VEC], x1[VEC];
+            r0[i].get(a.type, x0);
+            r1[i].get(a.type, x1);
+            if (turn && kind != 2) {
+                if (a.interleaved) {
+                    // pair i is elements 2i, 2i + 1 of the double run
+                    if constexpr (VEC == 1) {
+                        const float p = x0[0], q = x1[0];
+                        x0[0] = p * cs[0] - q * sn[0];
+                        x1[0] = p * sn[0] + q * cs[0];
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < VEC / 2; ++j) {
+                            const float p = x0[2 * j], q = x0[2 * j + 1], u = x1[2 * j], v = x1[2 * j + 1];
+                            x0[2 * j] = p * cs[j] - q * sn[j];
+                            x0[2 * j + 1] = p * sn[j] + q * cs[j];
+                            x1[2 * j] = u * cs[VEC / 2 + j] - v * sn[VEC / 2 + j];
+                            x1[2 * j + 1] = u * sn[VEC / 2 + j] + v * cs[VEC / 2 + j];
+                        }
+                    }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < VEC / 2; ++i) {
-                        const float p = x0[2 * i], q = x0[2 * i + 1], u = x1[2 * i], v = x1[2 * i + 1];
-                        x0[2 * i] = p * cs[i] - q * sn[i];
-                        x0[2 * i + 1] = p * sn[i] + q * cs[i];
-                        x1[2 * i] = u * cs[VEC / 2 + i] - v * sn[VEC / 2 + i];
-                        x1[2 * i + 1] = u * sn[VEC / 2 + i] + v * cs[VEC / 2 + i];
+                    for (int j = 0; j < VEC; ++j) {
+                        const float p = x0[j], q = x1[j];
+                        x0[j] = p * cs[j] - q * sn[j];
+                        x1[j] = p * sn[j] + q * cs[j];
                     }
                 }
+            }
+            if (kind == 0) {
+                store_run<VEC>(a.q_out, t * a.qo_ts + hh * a.qo_hs + e0, a.type, x0);
+                store_run<VEC>(a.q_out, t * a.qo_ts + hh * a.qo_hs + e1, a.type, x1);
             } else {
+                const float* scale = kind == 1 ? a.kv.k_scale : a.kv.v_scale;
+                if (scale) {
+                    const float inv = 1.f / scale[hh];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float p = x0[i], q = x1[i];
-                    x0[i] = p * cs[i] - q * sn[i];
-                    x1[i] = p * sn[i] + q * cs[i];
+                    for (int j = 0; j < VEC; ++j) {
+                        x0[j] *= inv;
+                        x1[j] *= inv;
+                    }
                 }
+                void* cache = kind == 1 ? a.kv.k : a.kv.v;
+                store_run<VEC>(cache, dst + hh * a.kv.head_stride + e0, a.kv.type, x0);
+                store_run<VEC>(cache, dst + hh * a.kv.head_stride + e1, a.kv.type, x1);
             }
-        }
-        if (kind == 0) {
-            store_run<VEC>(a.q_out, t * a.qo_ts + hh * a.qo_hs + e0, a.type, x0);
-            store_run<VEC>(a.q_out, t * a.qo_ts + hh * a.qo_hs + e1, a.type, x1);
-        } else {
-            const float* scale = kind == 1 ? a.kv.k_scale : a.kv.v_scale;
-            if (scale) {
-                const float s = scale[hh];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    x0[i] = x0[i] / s;
-                    x1[i] = x1[i] / s;
-                }
-            }
-            void* cache = kind == 1 ? a.kv.k : a.kv.v;
-            store_run<VEC>(cache, dst + hh * a.kv.head_stride + e0, a.kv.type, x0);
-            store_run<VEC>(cache, dst + hh * a.kv.head_stride + e1, a.kv.type, x1);
         }
     }
 }
@@ -135,13 +153,20 @@ bool fits(const AppendArgs& a, int vec) {
            runs_aligned(a.q_out, a.type, vec, a.qo_ts, a.qo_hs);
 }
 
+template <int VEC>
+cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
+    const int items = a.kv.head_dim / (2 * VEC), heads = a.kv.q_heads + 2 * a.kv.kv_heads;
+    int threads = (items * ((heads + kHeads - 1) / kHeads) + 31) / 32 * 32;
+    if (threads > kAppendThreads) threads = kAppendThreads;
+    if (a.type == MOE_F32) return launch_pdl(append_kernel<VEC, true>, dim3(a.T), dim3(threads), 0, st, a);
+    return launch_pdl(append_kernel<VEC, false>, dim3(a.T), dim3(threads), 0, st, a);
+}
+
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
-    if (fits(a, 8)) return launch_pdl(append_kernel<8>, dim3(a.T), dim3(kAppendThreads), 0, st, a);
-    if (fits(a, 4)) return launch_pdl(append_kernel<4>, dim3(a.T), dim3(kAppendThreads), 0, st, a);
-    return launch_pdl(append_kernel<1>, dim3(a.T), dim3(kAppendThreads), 0, st, a);
+    return fits(a, 8) ? launch<8>(a, st) : fits(a, 4) ? launch<4>(a, st) : launch<1>(a, st);
 }
 
 }  // namespace moe

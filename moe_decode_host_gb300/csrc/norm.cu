@@ -7,6 +7,8 @@
 // reduction and the outputs.  One reduction carries both statistics: the norm's factor
 // is common to the row, so max |y| = rsqrt(...) * max |s * w| and the maximum can be
 // taken before the factor is known.
+#include <algorithm>
+
 #include "ptx.cuh"
 #include "vec.cuh"
 
@@ -14,103 +16,233 @@ namespace moe {
 namespace {
 
 constexpr float kE4M3Max = 448.f;
-constexpr int kNormThreads = 1024;
+constexpr int kRingBytes = 48 * 1024;  // of a CTA, where two stages fit
+constexpr int kAny = -1;  // a type known only at run time
 
-// A row is handled by blockDim.x threads (whole warps), NV runs of VEC elements each,
-// blockDim.y rows a CTA.
-template <int VEC, int NV>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a) {
-    __shared__ float2 part[kNormThreads / 32];
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_wait(int left) {  // until at most `left` groups are in flight
+    switch (left) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    }
+}
+
+// A row is handled by blockDim.x threads (whole warps) with NV runs of VEC elements each,
+// blockDim.y rows a CTA at a time.  A CTA walks rows gridDim.x * blockDim.y apart; the next
+// row's loads are issued before the current row is reduced, so that reads stay in flight
+// through the reduction and the stores.  The usual types are template arguments: with the
+// types at run time the conversions made the kernel issue bound (52 instructions an
+// element and 77 us for 8192 x 4096 to E4M3).
+template <int VEC, int NV, int THREADS, int XT, int RT, int WT, int YT>
+__global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a, int stages) {
+    constexpr bool kRing = VEC == 8 && THREADS <= 256;
+    constexpr bool kAhead = !kRing && THREADS * NV * VEC <= 8192;  // registers for the next row
+    constexpr bool XW = XT == kAny || XT == MOE_F32, RW = RT == kAny || RT == MOE_F32;
+    constexpr int kPlanes = (XW ? 2 : 1) + (RW ? 2 : 1);  // 16-byte pieces of a run of x and r
+    extern __shared__ uint4 ring[];  // [stage][run][piece][thread]
+    __shared__ float2 part[2][THREADS / 32];
+    const int xt = XT == kAny ? a.x_type : XT, rt = RT == kAny ? a.res_type : RT;
+    const int wt = WT == kAny ? a.w_type : WT, yt = YT == kAny ? a.y_type : YT;
     grid_launch_next();
     grid_dep_wait();
-    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const bool live = row < a.T;
-    Raw<VEC> rx[NV], rr[NV], rw[NV];
+    const int warps = blockDim.x >> 5, w0 = threadIdx.y * warps;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int e0 = threadIdx.x * VEC, de = blockDim.x * VEC;
+    const int all = blockDim.x * blockDim.y, me = threadIdx.y * blockDim.x + threadIdx.x;
+    Raw<VEC, XW> rx[NV];
+    Raw<VEC, RW> rr[NV];
+    // a thread reads back only what it copied itself: no barrier but its own wait
+    auto copy = [&](int64_t r, int stage) {
+        if (r < a.T) {
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int e = (threadIdx.x + n * blockDim.x) * VEC;
-        if (live && e < a.H) {
-            rx[n].load(a.x, row * a.x_stride + e, a.x_type);
-            if (a.res) rr[n].load(a.res, row * a.res_stride + e, a.res_type);
-            if (a.w) rw[n].load(a.w, e, a.w_type);
+            for (int n = 0; n < NV; ++n)
+                if (e0 + n * de < a.H) {
+                    uint4* d = ring + (stage * NV + n) * kPlanes * all + me;
+                    const uint8_t* gx = static_cast<const uint8_t*>(a.x) + (r * a.x_stride + e0 + n * de) * type_bytes(xt);
+                    cp_async16(d, gx);
+                    if (XW && xt == MOE_F32) cp_async16(d + all, gx + 16);
+                    if (a.res) {
+                        const uint8_t* gr =
+                            static_cast<const uint8_t*>(a.res) + (r * a.res_stride + e0 + n * de) * type_bytes(rt);
+                        cp_async16(d + (XW ? 2 : 1) * all, gr);
+                        if (RW && rt == MOE_F32) cp_async16(d + (XW ? 3 : 2) * all, gr + 16);
+                    }
+                }
         }
-    }
-    float s[NV][VEC];
-    float ss = 0.f, top = 0.f;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto take = [&](int stage) {
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int e = (threadIdx.x + n * blockDim.x) * VEC;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) s[n][i] = 0.f;
-        if (live && e < a.H) {
-            rx[n].get(a.x_type, s[n]);
-            if (a.res) {
-                float r[VEC];
-                rr[n].get(a.res_type, r);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) s[n][i] += r[i];
+        for (int n = 0; n < NV; ++n) {
+            const uint4* d = ring + (stage * NV + n) * kPlanes * all + me;
+            if constexpr (VEC == 8) {
+                rx[n].set(d, all);
+                if (a.res) rr[n].set(d + (XW ? 2 : 1) * all, all);
             }
-            if (a.sum) store_run<VEC>(a.sum, row * a.sum_stride + e, a.res_type, s[n]);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) ss = fmaf(s[n][i], s[n][i], ss);
-            if (a.w) {
-                float w[VEC];
-                rw[n].get(a.w_type, w);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) s[n][i] *= w[i];
-            }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) top = fmaxf(top, fabsf(s[n][i]));
         }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    }
-    if (blockDim.x > 32) {
-        const int warps = blockDim.x >> 5, w0 = threadIdx.y * warps;
-        if ((threadIdx.x & 31) == 0) part[w0 + (threadIdx.x >> 5)] = make_float2(ss, top);
-        __syncthreads();
-        ss = 0.f;
-        top = 0.f;
-        for (int i = 0; i < warps; ++i) {  // the same order for every thread: one result a row
-            const float2 p = part[w0 + i];
-            ss += p.x;
-            top = fmaxf(top, p.y);
-        }
-    }
-    if (!live) return;
-    float f = 1.f / sqrtf(ss / (float)a.H + a.eps);
-    if (a.y_type == MOE_E4M3) {
-        // a row with a NaN or an infinity gets a NaN scale (fmaxf alone would hide it)
-        const float m = top * f;
-        const float scale = m == m && f == f ? fmaxf(m / kE4M3Max, 1.17549435e-38f) : __uint_as_float(0x7fc00000u);
-        if (threadIdx.x == 0) a.scale[row] = scale;
+    };
+    auto fetch = [&](int64_t r) {
+        if (r >= a.T) return;
 #pragma unroll
         for (int n = 0; n < NV; ++n)
+            if (e0 + n * de < a.H) {
+                rx[n].load(a.x, r * a.x_stride + e0 + n * de, xt);
+                if (a.res) rr[n].load(a.res, r * a.res_stride + e0 + n * de, rt);
+            }
+    };
+    if (kAhead) fetch(row);
+    if (kRing)
+        for (int i = 0; i < stages - 1; ++i) copy(row + i * step, i);
+    int slot = 0;
+    // every thread of the CTA makes the same number of rounds (their barriers)
+    int flip = 0;
+    for (int64_t first = (int64_t)blockIdx.x * blockDim.y; first < a.T; first += step, row += step, flip ^= 1) {
+        const bool live = row < a.T;
+        Raw<VEC, WT == kAny || WT == MOE_F32> rw[NV];
+        if (kRing) {
+            const int next = slot == 0 ? stages - 1 : slot - 1;  // the slot of the row before
+            copy(row + (stages - 1) * step, next);
+            cp_wait(stages - 1);
+            take(slot);
+            slot = slot + 1 == stages ? 0 : slot + 1;
+        } else if (!kAhead) {
+            fetch(row);
+        }
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) s[n][i] = s[n][i] * f / scale;
-    } else {
+        for (int n = 0; n < NV; ++n)
+            if (a.w && e0 + n * de < a.H) rw[n].load(a.w, e0 + n * de, wt);
+        float s[NV][VEC];
+        float ss = 0.f, top = 0.f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) s[n][i] = 0.f;
+            if (live && e0 + n * de < a.H) {
+                rx[n].get(xt, s[n]);
+                if (a.res) {
+                    float r[VEC];
+                    rr[n].get(rt, r);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) s[n][i] += r[i];
+                }
+            }
+        }
+        if (kAhead) fetch(row + step);
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            if (e0 + n * de < a.H) {
+                if (a.sum && live) store_run<VEC>(a.sum, row * a.sum_stride + e0 + n * de, rt, s[n]);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) ss = fmaf(s[n][i], s[n][i], ss);
+                if (a.w) {
+                    float w[VEC];
+                    rw[n].get(wt, w);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) s[n][i] *= w[i];
+                }
+                if (yt == MOE_E4M3) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) top = fmaxf(top, fabsf(s[n][i]));
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (yt == MOE_E4M3) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        }
+        if (warps > 1) {
+            // two sets of partials: the next round's writes meet no reader of this round's
+            if ((threadIdx.x & 31) == 0) part[flip][w0 + (threadIdx.x >> 5)] = make_float2(ss, top);
+            __syncthreads();
+            ss = top = 0.f;
+            for (int i = 0; i < warps; ++i) {  // in the same order for every thread: one result a row
+                const float2 v = part[flip][w0 + i];
+                ss += v.x;
+                top = fmaxf(top, v.y);
+            }
+        }
+        if (!live) continue;
+        float f = rsqrtf(fmaf(ss, a.inv_h, a.eps));
+        if (yt == MOE_E4M3) {
+            // a row with a NaN or an infinity gets a NaN scale (fmaxf alone would hide it)
+            const float m = top * f;
+            const float scale = m == m && f == f ? fmaxf(m * (1.f / kE4M3Max), 1.17549435e-38f) : __uint_as_float(0x7fc00000u);
+            if (threadIdx.x == 0) a.scale[row] = scale;
+            if (top > 1e-30f) {
+                f = kE4M3Max / top;  // = f / scale
+            } else {  // f / scale could overflow: the row is multiplied by both
+                const float inv = 1.f / scale;  // finite, as scale >= 2^-126
+#pragma unroll
+                for (int n = 0; n < NV; ++n)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) s[n][i] *= inv;
+            }
+        }
 #pragma unroll
         for (int n = 0; n < NV; ++n)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) s[n][i] *= f;
-    }
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int e = (threadIdx.x + n * blockDim.x) * VEC;
-        if (e < a.H) store_run<VEC>(a.y, row * a.y_stride + e, a.y_type, s[n]);
+        for (int n = 0; n < NV; ++n)
+            if (e0 + n * de < a.H) store_run<VEC>(a.y, row * a.y_stride + e0 + n * de, yt, s[n]);
     }
 }
 
-template <int VEC, int NV>
+template <int VEC, int NV, int THREADS, int XT, int RT, int WT, int YT>
 cudaError_t launch(const NormArgs& a, cudaStream_t st) {
     const int runs = (a.H + VEC - 1) / VEC;
     const int tx = ((runs + NV - 1) / NV + 31) / 32 * 32;
     const int ty = tx >= 128 ? 1 : 128 / tx;
-    const int64_t grid = ((int64_t)a.T + ty - 1) / ty;
-    return launch_pdl(norm_kernel<VEC, NV>, dim3((unsigned)grid), dim3(tx, ty), 0, st, a);
+    const auto kernel = norm_kernel<VEC, NV, THREADS, XT, RT, WT, YT>;
+    // one round of CTAs: a CTA that had to wait for another to end would walk its rows alone
+    static std::atomic<int> resident[THREADS / 32 + 1];  // CTAs an SM holds, by warps
+    const int warps = tx * ty / 32;
+    constexpr bool kRing = VEC == 8 && THREADS <= 256;
+    constexpr int kPlanes = (XT == kAny || XT == MOE_F32 ? 2 : 1) + (RT == kAny || RT == MOE_F32 ? 2 : 1);
+    const int stage_bytes = NV * kPlanes * 32 * warps * 16;
+    const int stages = kRing ? std::max(2, std::min(4, kRingBytes / stage_bytes)) : 0;
+    const int smem = stages * stage_bytes;
+    if (kRing) {
+        static std::atomic<uint64_t> configured;
+        cudaError_t err = ensure_smem_limit((const void*)kernel, std::max(kRingBytes, 2 * NV * kPlanes * THREADS * 16), configured, true);
+        if (err != cudaSuccess) return err;
+    }
+    int per_sm = resident[warps].load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, 32 * warps, smem);
+        if (err != cudaSuccess) return err;
+        if (per_sm < 1) per_sm = 1;
+        resident[warps].store(per_sm, std::memory_order_relaxed);
+    }
+    int64_t grid = ((int64_t)a.T + ty - 1) / ty;
+    if (grid > (int64_t)per_sm * a.sm_count) grid = (int64_t)per_sm * a.sm_count;
+    return launch_pdl(kernel, dim3((unsigned)grid), dim3(tx, ty), smem, st, a, stages);
+}
+
+// The weights of x's type and y of x's type or E4M3: types as template arguments.
+template <int VEC, int NV, int THREADS, int XT>
+cudaError_t typed(const NormArgs& a, cudaStream_t st) {
+    const bool wide = (a.res || a.sum) && a.res_type == MOE_F32;
+    if (a.y_type == MOE_E4M3)
+        return wide ? launch<VEC, NV, THREADS, XT, MOE_F32, XT, MOE_E4M3>(a, st)
+                    : launch<VEC, NV, THREADS, XT, XT, XT, MOE_E4M3>(a, st);
+    return wide ? launch<VEC, NV, THREADS, XT, MOE_F32, XT, XT>(a, st) : launch<VEC, NV, THREADS, XT, XT, XT, XT>(a, st);
+}
+
+template <int VEC, int NV, int THREADS>
+cudaError_t pick(const NormArgs& a, cudaStream_t st) {
+    const bool usual = (!a.w || a.w_type == a.x_type) && (a.y_type == a.x_type || a.y_type == MOE_E4M3) &&
+                       (!(a.res || a.sum) || a.res_type == a.x_type || a.res_type == MOE_F32);
+    if (usual && a.x_type == MOE_BF16) return typed<VEC, NV, THREADS, MOE_BF16>(a, st);
+    if (usual && a.x_type == MOE_F16) return typed<VEC, NV, THREADS, MOE_F16>(a, st);
+    if (usual && a.x_type == MOE_F32) return typed<VEC, NV, THREADS, MOE_F32>(a, st);
+    return launch<VEC, NV, THREADS, kAny, kAny, kAny, kAny>(a, st);
 }
 
 }  // namespace
@@ -123,12 +255,14 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
                      (!a.sum || runs_aligned(a.sum, a.res_type, 8, a.sum_stride)) &&
                      runs_aligned(a.y, a.y_type, 8, a.y_stride);
     if (vec) {
-        if (a.H <= 8192) return launch<8, 1>(a, st);
-        return launch<8, 4>(a, st);
+        if (a.H <= 2048) return pick<8, 1, 256>(a, st);
+        if (a.H <= 4096) return pick<8, 2, 256>(a, st);
+        if (a.H <= 8192) return pick<8, 4, 256>(a, st);
+        return launch<8, 4, 1024, kAny, kAny, kAny, kAny>(a, st);
     }
-    if (a.H <= 1024) return launch<1, 1>(a, st);
-    if (a.H <= 8192) return launch<1, 8>(a, st);
-    return launch<1, 32>(a, st);
+    if (a.H <= 5120) return pick<1, 5, 1024>(a, st);
+    if (a.H <= 8192) return pick<1, 8, 1024>(a, st);
+    return launch<1, 32, 1024, kAny, kAny, kAny, kAny>(a, st);
 }
 
 }  // namespace moe

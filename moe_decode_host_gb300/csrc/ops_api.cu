@@ -58,7 +58,9 @@ int moe_add_rms_norm(const void* x, int x_type, int64_t x_stride, const void* re
     if (!x || !y || (y_type == MOE_E4M3) != (y_scale != nullptr)) return MOE_ERR_INVALID_ARG;
     if (T == 1) x_stride = res_stride = sum_stride = y_stride = 0;  // of no meaning for one row
     NormArgs a{x, residual, weight, x_type, res_type, weight_type, x_stride, res_stride, eps, T, H, sum_out,
-               sum_stride, y, y_type, y_stride, y_scale};
+               sum_stride, y, y_type, y_stride, y_scale, 1.f / (float)H, 0};
+    const int rc = sm_count_now(&a.sm_count);
+    if (rc != MOE_OK) return rc;
     return cuda_status(launch_norm(a, S(stream)));
 }
 

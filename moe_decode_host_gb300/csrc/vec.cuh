@@ -28,27 +28,31 @@ __device__ __forceinline__ float half_bits_to_f32(uint32_t h, int type) {
 }
 
 // VEC consecutive bf16, f16 or fp32 elements as raw bits.  The loads are plain
-// (coherent): outputs may be the inputs' own memory.
-template <int VEC>
+// (coherent): outputs may be the inputs' own memory.  WIDE = false: never fp32, half the
+// registers.
+template <int VEC, bool WIDE = true>
 struct Raw {
-    static constexpr int kWords = VEC;  // fp32; the 16-bit types use the first half
-    uint32_t w[VEC < 2 ? 1 : VEC];
+    uint32_t w[VEC < 2 ? 1 : (WIDE ? VEC : VEC / 2)];
 
     __device__ __forceinline__ void load(const void* p, int64_t at, int type) {
         if constexpr (VEC == 8) {
-            if (type == MOE_F32) {
+            if constexpr (WIDE) if (type == MOE_F32) {
                 const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
                 const uint4 a = q[0], b = q[1];
                 w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-            } else {
+                return;
+            }
+            {
                 const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
                 w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
             }
         } else if constexpr (VEC == 4) {
-            if (type == MOE_F32) {
+            if constexpr (WIDE) if (type == MOE_F32) {
                 const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
                 w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-            } else {
+                return;
+            }
+            {
                 const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
                 w[0] = a.x, w[1] = a.y;
             }
@@ -58,11 +62,24 @@ struct Raw {
         }
     }
 
+    // From shared memory: 16-byte pieces `apart` pieces from one another.
+    __device__ __forceinline__ void set(const uint4* p, int apart) {
+        static_assert(VEC == 8, "runs of 8");
+        const uint4 a = p[0];
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        if constexpr (WIDE) {
+            const uint4 b = p[apart];
+            w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        }
+    }
+
     __device__ __forceinline__ void get(int type, float (&v)[VEC]) const {
-        if (type == MOE_F32) {
+        if constexpr (WIDE) if (type == MOE_F32) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) v[i] = __uint_as_float(w[i]);
-        } else if constexpr (VEC == 1) {
+            return;
+        }
+        if constexpr (VEC == 1) {
             v[0] = half_bits_to_f32(w[0], type);
         } else if (type == MOE_BF16) {
 #pragma unroll
