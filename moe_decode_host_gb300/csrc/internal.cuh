@@ -243,6 +243,7 @@ struct AppendArgs {
     int n_positions, rot, interleaved, T;
     void* q_out;
     int64_t qo_ts, qo_hs;
+    int sm_count;
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st);
 

@@ -126,7 +126,7 @@ int moe_kv_append(moe_kv* kv, int type, const void* q, int64_t q_ts, int64_t q_h
     if (kv->view.q_heads == 1) q_hs = qo_hs = 0;
     if (kv->view.kv_heads == 1) k_hs = v_hs = 0;
     AppendArgs a{kv->view, q, k, v, type, q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, positions, slots, cos_sin, n_positions,
-                 rot_dim, interleaved, T, q_out, qo_ts, qo_hs};
+                 rot_dim, interleaved, T, q_out, qo_ts, qo_hs, kv->sm_count};
     return cuda_status(launch_append(a, S(stream)));
 }
 
