@@ -402,7 +402,10 @@ int moe_add_rms_norm(const void* x, int x_type, int64_t x_stride, const void* re
  *             h / (q_heads / kv_heads).
  *  head_dim   a multiple of 16, at most 256.
  *  page_size  any from 1 to 65536.
- *  max_batch  most sequences of one moe_kv_attend call, 1 to 65535. */
+ *  max_batch  most sequences of one moe_kv_attend call, 1 to 65535.
+ * The last token's offset must be below 2^32 times the largest power of two (in bytes)
+ * that divides both page and token stride: 64 GB for the narrowest rows of 16 bytes, more
+ * than the GPU holds for any row of 128 bytes. */
 typedef struct moe_kv_params {
     int n_pages, page_size, kv_heads, q_heads, head_dim, type, max_batch;
     int64_t page_stride, token_stride, head_stride;

@@ -265,6 +265,8 @@ struct AttendArgs {
     int sm_count;
     void* workspace;  // attend_workspace bytes, zero before the handle's first call
 };
+// Whether the rows' offsets fit the kernel's 32 bits (in units of what the strides share).
+bool attend_fits(const KvView& kv);
 size_t attend_workspace(const KvView& kv, int sm_count);
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st);
 

@@ -5,7 +5,7 @@
 // Bound by the cache's bytes, each read once for all query heads of a key head.
 //
 // Split.  The attended tokens of a (sequence, key head, block of query heads) form a
-// segment of units of 16 tokens; the segments of a call are laid end to end and every
+// segment of units of 16 tokens (32 where a row is at most 128 bytes); the segments of a call are laid end to end and every
 // CTA gets the same number of units of that line, whatever the lengths.  A CTA walks
 // its stretch as pieces of segments.  A segment inside one CTA is finished there; the
 // parts of one that spans CTAs go to a workspace, and the CTA that arrives last joins
@@ -27,7 +27,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kUnit = 16;        // tokens of a unit
+// Tokens of a unit, for rows of `bytes` (head_dim rounded up): the wider unit halves the
+// work a token that does not depend on its row (page look-up, the maxima's exchange).
+__host__ __device__ constexpr int unit_tokens(int bytes) { return bytes <= 128 ? 32 : 16; }
 constexpr int kMaxStages = 8;    // units of a warp's ring
 constexpr int kMinUnits = 4;     // units worth a CTA of its own: one a warp
 constexpr int64_t kMaxTokens = 1 << 30;  // of a sequence: token indexes stay in 32 bits
@@ -42,6 +44,7 @@ struct Plan {
     int stages;
     int cpr;        // 16-byte pieces of a row
     uint32_t inv;   // 2^20 / cpr rounded up: row of piece i = i * inv >> 20 (i < 512)
+    int shift;      // offsets of rows in the cache are kept in units of 2^shift bytes
     int slots;      // CTAs the workspace has room for
 };
 
@@ -53,6 +56,10 @@ __device__ __forceinline__ float fast_exp2(float x) {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void cp_wait(int left) {  // until at most `left` groups are in flight
@@ -97,6 +104,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// 2^(s * scale - ref), 0 for a score left out (-inf).
+__device__ __forceinline__ float weight(float s, float scale, float ref) {
+    return s == -INFINITY ? 0.f : fast_exp2(fmaf(s, scale, -ref));
+}
+
 // Two E4M3 codes (the low or high half of w) as f16x2.
 __device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
     uint32_t r;
@@ -124,7 +136,7 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int b) {
     const int first = a.window > 0 && n > a.window ? (int)n - a.window : 0;
     return {first, (int)n - first};
 }
-__device__ __forceinline__ int units_of(const Span& s) { return (int)(((int64_t)s.count + kUnit - 1) / kUnit); }
+__device__ __forceinline__ int units_of(const Span& s, int unit) { return (s.count + unit - 1) / unit; }
 
 // T: 0 bf16, 1 f16, 2 E4M3 (computed in f16).  DP: head_dim rounded up to 64, 128 or
 // 256.  NT: blocks of 8 query heads.
@@ -133,6 +145,8 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
     constexpr bool BF = T == 0, F8 = T == 2;
     constexpr int HC = 8 * NT;
     constexpr int ES = F8 ? 1 : 2;
+    constexpr int U = unit_tokens(DP * ES), MT = U / 16;  // tokens of a unit, in tiles of 16
+    constexpr uint32_t kAll = U == 32 ? 0xffffffffu : 0xffffu;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_m[kWarps][HC], s_l[kWarps][HC], s_scale[HC], s_inv[HC];
     __shared__ uint32_t s_mask[kWarps][kMaxStages];
@@ -142,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
     const int g = lane >> 2, c = lane & 3;
     const int D = a.kv.head_dim, steps = D / 16;
     const int qpitch = D * 2 + 16;
-    const int unit_bytes = 2 * kUnit * p.pitch;
+    const int unit_bytes = 2 * U * p.pitch;
     uint8_t* s_q = smem;
     uint8_t* ring = smem + HC * (DP * 2 + 16) + warp * p.stages * unit_bytes;
     const uint32_t ring_u = smem_u32(ring), q_u = smem_u32(s_q);
@@ -167,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
 
     // ---- this CTA's stretch of the line ----
     long long mine = 0;
-    for (int b = tid; b < a.B; b += kThreads) mine += units_of(span_of(a, b));
+    for (int b = tid; b < a.B; b += kThreads) mine += units_of(span_of(a, b), U);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if (lane == 0) s_sum[warp] = mine;
@@ -185,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
         long long before = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             const int b = b0 + tid;
-            const long long u = b < a.B ? (long long)units_of(span_of(a, b)) * per_b : 0;
+            const long long u = b < a.B ? (long long)units_of(span_of(a, b), U) * per_b : 0;
             long long x = u;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -210,14 +224,14 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
     int b = s_b;
     long long before = s_before;  // units ahead of sequence b
     Span span = span_of(a, b);
-    int ub = units_of(span);
+    int ub = units_of(span, U);
 
     for (long long u = u_begin; u < u_end;) {
         while (u >= before + (long long)ub * per_b) {  // next sequence with a token
             before += (long long)ub * per_b;
             ++b;
             span = span_of(a, b);
-            ub = units_of(span);
+            ub = units_of(span, U);
         }
         const int seg = (int)((u - before) / ub);
         const long long seg_begin = before + (long long)seg * ub;
@@ -231,12 +245,11 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
         const uint8_t* kb = static_cast<const uint8_t*>(a.kv.k) + kh * a.kv.head_stride * ES;
         const uint8_t* vb = static_cast<const uint8_t*>(a.kv.v) + kh * a.kv.head_stride * ES;
         const int32_t* table = a.page_table + b * a.table_stride;
-        int next_page = -1, next_entry = 0;  // lanes 0..15: the page and entry of that row of the next unit
+        int next_page = -1, next_entry = 0;  // the page and entry of row `lane` of the next unit
         auto look_up = [&](int x) {
-            const int j = (first_u + warp + kWarps * x) * kUnit + lane;
-            next_page = -1;
-            if (lane < kUnit && x < n_mine && j < span.count) {
-                const int t = span.first + j, pg = t / a.kv.page_size;
+            const int j = (first_u + warp + kWarps * x) * U + lane;
+            if (lane < U && x < n_mine && j < span.count) {
+                const uint32_t t = span.first + j, pg = t / (uint32_t)a.kv.page_size;
                 next_entry = t - pg * a.kv.page_size;
                 next_page = table[pg];
             }
@@ -244,23 +257,35 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
         auto issue = [&](int x) {  // the unit that look_up last saw, into slot x % stages
             if (x < n_mine) {
                 const int slot = x % p.stages;
-                const bool past = (first_u + warp + kWarps * x) * kUnit + lane >= span.count;
-                const bool bad = lane < kUnit && !past && (next_page < 0 || next_page >= a.kv.n_pages);
-                if (bad) set_status(a.kv.status, MOE_ERR_BAD_INDEX);
-                const bool ok = lane < kUnit && !past && !bad;
-                const int64_t off = ok ? (next_page * a.kv.page_stride + next_entry * a.kv.token_stride) * ES : 0;
+                const bool in = lane < U && (first_u + warp + kWarps * x) * U + lane < span.count;
+                const bool ok = in && next_page >= 0 && next_page < a.kv.n_pages;
+                if (in && !ok) set_status(a.kv.status, MOE_ERR_BAD_INDEX);
+                const uint32_t off =
+                    ok ? (uint32_t)(((next_page * a.kv.page_stride + next_entry * a.kv.token_stride) * ES) >> p.shift) : 0u;
                 const uint32_t mask = __ballot_sync(0xffffffffu, ok);
                 if (lane == 0) s_mask[warp][slot] = mask;
                 const uint32_t dst = ring_u + slot * unit_bytes;
-#pragma unroll 4
-                for (int i0 = 0; i0 < kUnit * p.cpr; i0 += 32) {  // kUnit * cpr is a multiple of 16
-                    const int i = i0 + lane;
-                    const int row = (int)((uint32_t)i * p.inv >> 20), col = (i - row * p.cpr) * 16;
-                    const int64_t o = __shfl_sync(0xffffffffu, off, row & 15);
-                    if (row < kUnit) {
-                        const uint32_t bytes = (mask >> row & 1u) ? 16u : 0u;  // rows left out are zeros
-                        cp_async16(dst + row * p.pitch + col, kb + o + col, bytes);
-                        cp_async16(dst + (kUnit + row) * p.pitch + col, vb + o + col, bytes);
+                constexpr int CPR = DP * ES / 16;
+                if (mask == kAll && p.cpr == CPR) {
+                    // lanes cover 32 / CPR whole rows at a time
+                    const int col = lane % CPR * 16, row = lane / CPR;
+                    const uint32_t at = dst + row * p.pitch + col;
+#pragma unroll
+                    for (int i = 0; i < U * CPR / 32; ++i) {
+                        const int64_t o = (int64_t)((uint64_t)__shfl_sync(0xffffffffu, off, i * (32 / CPR) + row) << p.shift) + col;
+                        cp_async16(at + i * (32 / CPR) * p.pitch, kb + o);
+                        cp_async16(at + (U + i * (32 / CPR)) * p.pitch, vb + o);
+                    }
+                } else {
+                    for (int i0 = 0; i0 < U * p.cpr; i0 += 32) {
+                        const int i = i0 + lane;
+                        const int row = (int)((uint32_t)i * p.inv >> 20), col = (i - row * p.cpr) * 16;
+                        const int64_t o = (int64_t)((uint64_t)__shfl_sync(0xffffffffu, off, row & (U - 1)) << p.shift) + col;
+                        if (row < U) {
+                            const uint32_t bytes = (mask >> row & 1u) ? 16u : 0u;  // rows left out are zeros
+                            cp_async16(dst + row * p.pitch + col, kb + o, bytes);
+                            cp_async16(dst + (U + row) * p.pitch + col, vb + o, bytes);
+                        }
                     }
                 }
             }
@@ -291,15 +316,16 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
                 for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 e = prescale_exp(top);
             }
-            const float down = F8 ? pow2i(-e) : 1.f;
+            // a negative scale is folded into q, so that the largest raw score is the largest score
+            const float down = copysignf(F8 ? pow2i(-e) : 1.f, a.scale);
 #pragma unroll
             for (int i = 0; i < DP / 32; ++i) {
                 const int d = lane + 32 * i;
                 if (d < D)
                     reinterpret_cast<uint16_t*>(s_q + h * qpitch)[d] =
-                        (uint16_t)(BF ? pack_bf16(v[i], 0.f) : pack_f16(v[i] * down, 0.f));
+                        (uint16_t)(BF ? pack_bf16(v[i] * down, 0.f) : pack_f16(v[i] * down, 0.f));
             }
-            if (lane == 0) s_scale[h] = a.scale * kLog2e * (F8 ? a.kv.k_scale[kh] * pow2i(e) : 1.f);
+            if (lane == 0) s_scale[h] = fabsf(a.scale) * kLog2e * (F8 ? a.kv.k_scale[kh] * pow2i(e) : 1.f);
         }
         __syncthreads();
 
@@ -324,78 +350,103 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
             cp_wait(p.stages - 1);
             __syncwarp();
             const int slot = x % p.stages;
-            const uint32_t ku = ring_u + slot * unit_bytes, vu = ku + kUnit * p.pitch;
+            const uint32_t ku = ring_u + slot * unit_bytes, vu = ku + U * p.pitch;
             const uint32_t mask = s_mask[warp][slot];
-            float s[NT][4];
+            float s[MT][NT][4];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) s[i][t][0] = s[i][t][1] = s[i][t][2] = s[i][t][3] = 0.f;
+            // matrices of a load: token halves of a 16-byte piece of the rows, then of the next piece
+            const uint32_t k_at = ku + ((lane & 7) + (lane & 8)) * p.pitch + (lane >> 4) * 16;
             if constexpr (F8) {
-                // matrices of a load: token halves of 16-byte piece kk, then of piece kk + 1
-                const uint32_t at = ku + ((lane & 7) + (lane & 8)) * p.pitch + (lane >> 4) * 16;
 #pragma unroll
                 for (int kk = 0; kk < DP / 16; kk += 2) {
                     if (kk < steps) {
-                        uint32_t r[4];
-                        ldsm4(r, at + kk * 16);
+                        uint32_t r[MT][4];
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) ldsm4(r[i], k_at + i * 16 * p.pitch + kk * 16);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             if (kk + h < steps) {
-                                const uint32_t f[4] = {e4m3_lo(r[2 * h]), e4m3_lo(r[2 * h + 1]), e4m3_hi(r[2 * h]),
-                                                       e4m3_hi(r[2 * h + 1])};
+                                uint2 q[NT];
 #pragma unroll
-                                for (int t = 0; t < NT; ++t) {
-                                    const uint2 q = *reinterpret_cast<const uint2*>(s_q + (8 * t + g) * qpitch +
-                                                                                    (kk + h) * 32 + c * 8);
-                                    mma16816<BF>(s[t], f, q.x, q.y);
+                                for (int t = 0; t < NT; ++t)
+                                    q[t] = *reinterpret_cast<const uint2*>(s_q + (8 * t + g) * qpitch + (kk + h) * 32 + c * 8);
+#pragma unroll
+                                for (int i = 0; i < MT; ++i) {
+                                    const uint32_t f[4] = {e4m3_lo(r[i][2 * h]), e4m3_lo(r[i][2 * h + 1]),
+                                                           e4m3_hi(r[i][2 * h]), e4m3_hi(r[i][2 * h + 1])};
+#pragma unroll
+                                    for (int t = 0; t < NT; ++t) mma16816<BF>(s[i][t], f, q[t].x, q[t].y);
                                 }
                             }
                         }
                     }
                 }
             } else {
-                const uint32_t at = ku + ((lane & 7) + (lane & 8)) * p.pitch + (lane >> 4) * 16;
 #pragma unroll
                 for (int kk = 0; kk < DP / 16; ++kk) {
                     if (kk < steps) {
-                        uint32_t r[4];
-                        ldsm4(r, at + kk * 32);
+                        uint32_t r[MT][4];
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) ldsm4(r[i], k_at + i * 16 * p.pitch + kk * 32);
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
                             const uint8_t* q = s_q + (8 * t + g) * qpitch + kk * 32 + c * 4;
-                            mma16816<BF>(s[t], r, *reinterpret_cast<const uint32_t*>(q),
-                                         *reinterpret_cast<const uint32_t*>(q + 16));
+                            const uint32_t q0 = *reinterpret_cast<const uint32_t*>(q);
+                            const uint32_t q1 = *reinterpret_cast<const uint32_t*>(q + 16);
+#pragma unroll
+                            for (int i = 0; i < MT; ++i) mma16816<BF>(s[i][t], r[i], q0, q1);
                         }
                     }
                 }
             }
-            // softmax: lane (g, c) holds tokens g, g + 8 of heads 2c, 2c + 1 of each block
-            const bool ok0 = mask >> g & 1u, ok1 = mask >> (g + 8) & 1u;
+            // softmax: lane (g, c) holds tokens g, g + 8 of each 16, heads 2c, 2c + 1 of each block
+            if (mask != kAll) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (!(mask >> (16 * i + g + 8 * (j >> 1)) & 1u)) {
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) s[i][t][j] = -INFINITY;
+                        }
+            }
             float keep[NT][2];
             bool grown = false;
-            uint32_t pb[NT][2];
+            uint32_t pb[MT][NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float x0 = ok0 ? s[t][j] * sc[t][j] : -INFINITY;
-                    const float x1 = ok1 ? s[t][2 + j] * sc[t][j] : -INFINITY;
-                    float top = fmaxf(x0, x1);
+                    float top = fmaxf(s[0][t][j], s[0][t][2 + j]);
+#pragma unroll
+                    for (int i = 1; i < MT; ++i) top = fmaxf(top, fmaxf(s[i][t][j], s[i][t][2 + j]));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                     const float mn = fmaxf(m[t][j], top);
-                    const float ref = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every weight is 0
-                    keep[t][j] = fast_exp2(m[t][j] - ref);
+                    const float ref = mn == -INFINITY ? 0.f : mn * sc[t][j];  // nothing seen yet: every weight is 0
+                    keep[t][j] = m[t][j] == -INFINITY ? 0.f : fast_exp2(fmaf(m[t][j], sc[t][j], -ref));
                     grown |= mn != m[t][j];
                     m[t][j] = mn;
-                    s[t][j] = fast_exp2(x0 - ref);
-                    s[t][2 + j] = fast_exp2(x1 - ref);
-                    l[t][j] = l[t][j] * keep[t][j] + (s[t][j] + s[t][2 + j]);
+                    float sum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        s[i][t][j] = weight(s[i][t][j], sc[t][j], ref);
+                        s[i][t][2 + j] = weight(s[i][t][2 + j], sc[t][j], ref);
+                        sum += s[i][t][j] + s[i][t][2 + j];
+                    }
+                    l[t][j] = fmaf(l[t][j], keep[t][j], sum);
                 }
                 // the weights are rounded to the values' 16-bit type for the tensor cores (bf16 adds
                 // about as much error as the output's own rounding; f16 an eighth of it); their sum is not
-                pb[t][0] = transpose8x8(BF ? pack_bf16(s[t][0], s[t][1]) : pack_f16(s[t][0], s[t][1]));
-                pb[t][1] = transpose8x8(BF ? pack_bf16(s[t][2], s[t][3]) : pack_f16(s[t][2], s[t][3]));
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    pb[i][t][0] = transpose8x8(BF ? pack_bf16(s[i][t][0], s[i][t][1]) : pack_f16(s[i][t][0], s[i][t][1]));
+                    pb[i][t][1] = transpose8x8(BF ? pack_bf16(s[i][t][2], s[i][t][3]) : pack_f16(s[i][t][2], s[i][t][3]));
+                }
             }
             if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
@@ -405,39 +456,49 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
 #pragma unroll
                         for (int j = 0; j < 4; ++j) o[i][t][j] *= keep[t][j & 1];
             }
-            if constexpr (F8) {
-                const uint32_t at = vu + ((lane & 7) + (lane & 8)) * p.pitch + (lane >> 4) * 16;
 #pragma unroll
-                for (int i = 0; i < DP / 16; i += 2) {
-                    if (i < steps) {
-                        uint32_t r[4];
-                        ldsm4_t(r, at + i * 16);
+            for (int k = 0; k < MT; ++k) {
+                if constexpr (F8) {
+                    const uint32_t at = vu + (16 * k + (lane & 7) + (lane & 8)) * p.pitch + (lane >> 4) * 16;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (i + h < steps) {
-                                // bytes (token, dim): (2c, 2g), (2c, 2g+1), (2c+1, 2g), (2c+1, 2g+1)
-                                const uint32_t w0 = __byte_perm(r[2 * h], 0, 0x3120), w1 = __byte_perm(r[2 * h + 1], 0, 0x3120);
-                                const uint32_t f[4] = {e4m3_lo(w0), e4m3_hi(w0), e4m3_lo(w1), e4m3_hi(w1)};
+                    for (int i = 0; i < DP / 16; i += 2) {
+                        if (i < steps) {
+                            uint32_t r[4];
+                            ldsm4_t(r, at + i * 16);
 #pragma unroll
-                                for (int t = 0; t < NT; ++t) mma16816<BF>(o[i + h][t], f, pb[t][0], pb[t][1]);
+                            for (int h = 0; h < 2; ++h) {
+                                if (i + h < steps) {
+                                    // bytes (token, dim): (2c, 2g), (2c, 2g+1), (2c+1, 2g), (2c+1, 2g+1)
+                                    const uint32_t w0 = __byte_perm(r[2 * h], 0, 0x3120);
+                                    const uint32_t w1 = __byte_perm(r[2 * h + 1], 0, 0x3120);
+                                    const uint32_t f[4] = {e4m3_lo(w0), e4m3_hi(w0), e4m3_lo(w1), e4m3_hi(w1)};
+#pragma unroll
+                                    for (int t = 0; t < NT; ++t) mma16816<BF>(o[i + h][t], f, pb[k][t][0], pb[k][t][1]);
+                                }
                             }
                         }
                     }
-                }
-            } else {
-                const uint32_t at = vu + ((lane & 7) + ((lane >> 4) << 3)) * p.pitch + (lane & 8) * 2;
+                } else {
+                    const uint32_t at = vu + (16 * k + (lane & 7) + ((lane >> 4) << 3)) * p.pitch + (lane & 8) * 2;
 #pragma unroll
-                for (int i = 0; i < DP / 16; ++i) {
-                    if (i < steps) {
-                        uint32_t r[4];
-                        ldsm4_t(r, at + i * 32);
+                    for (int i = 0; i < DP / 16; ++i) {
+                        if (i < steps) {
+                            uint32_t r[4];
+                            ldsm4_t(r, at + i * 32);
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) mma16816<BF>(o[i][t], r, pb[t][0], pb[t][1]);
+                            for (int t = 0; t < NT; ++t) mma16816<BF>(o[i][t], r, pb[k][t][0], pb[k][t][1]);
+                        }
                     }
                 }
             }
             __syncwarp();
         }
+        // maxima of scores from here on, in powers of two
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (m[t][j] != -INFINITY) m[t][j] *= sc[t][j];
 
         // ---- join the warps ----
 #pragma unroll
@@ -574,6 +635,10 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
     }
 }
 
+}  // namespace
+int attend_shift(const KvView& kv);
+namespace {
+
 int blocks_of_heads(const KvView& kv) {  // NT
     const int group = kv.q_heads / kv.kv_heads;
     if (group <= 8) return 1;
@@ -584,8 +649,12 @@ int dim_class(const KvView& kv) { return kv.head_dim <= 64 ? 64 : (kv.head_dim <
 
 int ctas_per_sm(const KvView& kv) { return kv.head_dim <= 128 ? 2 : 1; }
 
+int unit_bytes(const KvView& kv, const Plan& p) {
+    return 2 * unit_tokens(dim_class(kv) * type_bytes(kv.type)) * p.pitch;
+}
+
 int smem_of(const KvView& kv, const Plan& p) {
-    return 8 * blocks_of_heads(kv) * (dim_class(kv) * 2 + 16) + kWarps * p.stages * 2 * kUnit * p.pitch + 16;
+    return 8 * blocks_of_heads(kv) * (dim_class(kv) * 2 + 16) + kWarps * p.stages * unit_bytes(kv, p) + 16;
 }
 
 Plan plan_of(const KvView& kv, int sm_count) {
@@ -596,13 +665,14 @@ Plan plan_of(const KvView& kv, int sm_count) {
     p.cpr = kv.head_dim * es / 16;
     p.inv = ((1u << 20) + p.cpr - 1) / p.cpr;
     p.pitch = (p.cpr | 1) * 16;
+    p.shift = attend_shift(kv);
     p.slots = (ctas_per_sm(kv) * sm_count + 1) / 2 * 2;  // even: the sums behind the counters are read in pairs
     // as many units in flight as fit beside the other CTA of the SM; the ring also holds
     // the warp's [hc][head_dim + 4] sums when a piece ends
     const int budget = (ctas_per_sm(kv) == 2 ? 110 : 222) * 1024;
-    const int least = (hc * (kv.head_dim + 4) * 4 + 2 * kUnit * p.pitch - 1) / (2 * kUnit * p.pitch);
+    const int least = (hc * (kv.head_dim + 4) * 4 + unit_bytes(kv, p) - 1) / unit_bytes(kv, p);
     p.stages = kMaxStages;
-    while (p.stages > 3 && p.stages > least && smem_of(kv, p) > budget) --p.stages;
+    while (p.stages > 2 && p.stages > least && smem_of(kv, p) > budget) --p.stages;
     return p;
 }
 
@@ -616,7 +686,8 @@ cudaError_t launch(const AttendArgs& a, const Plan& p, cudaStream_t st) {
     const int64_t per_b = (int64_t)a.kv.kv_heads * p.chunks;
     const int64_t room = room_of(a);
     const int64_t most = a.window > 0 && room > a.window ? a.window : room;
-    const int64_t units = (most + kUnit - 1) / kUnit * per_b * a.B;
+    const int unit = unit_tokens(DP * (T == 2 ? 1 : 2));
+    const int64_t units = (most + unit - 1) / unit * per_b * a.B;
     int64_t grid = (units + kMinUnits - 1) / kMinUnits;
     if (grid > p.slots) grid = p.slots;
     if (grid < 1) grid = 1;
@@ -635,6 +706,20 @@ cudaError_t pick(const AttendArgs& a, const Plan& p, cudaStream_t st) {
 }
 
 }  // namespace
+
+// The unit of the rows' offsets: what page and token stride are both multiples of.
+int attend_shift(const KvView& kv) {
+    const uint64_t bytes = (uint64_t)(kv.page_stride | kv.token_stride) * type_bytes(kv.type);
+    int s = 4;
+    while (s < 30 && !(bytes >> s & 1)) ++s;
+    return s;
+}
+
+bool attend_fits(const KvView& kv) {
+    const uint64_t last = ((uint64_t)(kv.n_pages - 1) * kv.page_stride + (uint64_t)(kv.page_size - 1) * kv.token_stride) *
+                          type_bytes(kv.type);
+    return last >> attend_shift(kv) <= 0xffffffffull;
+}
 
 // A counter a CTA, then two slots of partial sums a CTA: maxima and sums of the block's
 // heads, and their [heads][head_dim] outputs.

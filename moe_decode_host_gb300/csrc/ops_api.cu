@@ -85,6 +85,10 @@ int moe_kv_create(const moe_kv_params* pp, void* k_cache, void* v_cache, const f
     kv->view = KvView{k_cache, v_cache, k_scale, v_scale, p.type, p.n_pages, p.page_size, p.kv_heads, p.q_heads,
                       p.head_dim, p.page_stride, p.token_stride, p.head_stride, nullptr};
     kv->max_batch = p.max_batch;
+    if (!attend_fits(kv->view)) {
+        delete kv;
+        return MOE_ERR_INVALID_ARG;
+    }
     if (sm_count_now(&kv->sm_count) != MOE_OK) {
         delete kv;
         return MOE_ERR_CUDA;
