@@ -27,6 +27,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+// CTAs that share an SM, by the registers that their sums take.
+__host__ __device__ constexpr int ctas_an_sm(int dp, int nt) { return dp > 128 ? 1 : (nt > 2 ? 2 : 3); }
+constexpr int budget_of(int ctas) { return ctas == 3 ? 73 * 1024 : (ctas == 2 ? 111 * 1024 : 222 * 1024); }
+
 // Tokens of a unit, for rows of `bytes` (head_dim rounded up): the wider unit halves the
 // work a token that does not depend on its row (page look-up, the maxima's exchange).
 __host__ __device__ constexpr int unit_tokens(int bytes) { return bytes <= 128 ? 32 : 16; }
@@ -40,10 +44,15 @@ constexpr float kLn2 = 0.69314718f;
 struct Plan {
     int chunk;      // query heads of a segment, at most 8 NT
     int chunks;     // segments of a key head
-    int pitch;      // bytes of a row in the ring: an odd multiple of 16, so ldmatrix meets no bank twice
+    // bytes of a row in the ring.  ldmatrix reads the same 16-byte piece of 8 rows: rows of whole
+    // 128 bytes keep piece i in place i ^ (row % 8) (swizzle 7), others are an odd number of pieces
+    // apart (swizzle 0), so the 8 meet no bank twice
+    int pitch, swizzle;
     int stages;
     int cpr;        // 16-byte pieces of a row
     uint32_t inv;   // 2^20 / cpr rounded up: row of piece i = i * inv >> 20 (i < 512)
+    uint32_t page_mul;  // t / page_size = t * page_mul >> page_shift for t < 2^30
+    int page_shift;
     int shift;      // offsets of rows in the cache are kept in units of 2^shift bytes
     int slots;      // CTAs the workspace has room for
 };
@@ -104,10 +113,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// 2^(s * scale - ref), 0 for a score left out (-inf).
-__device__ __forceinline__ float weight(float s, float scale, float ref) {
-    return s == -INFINITY ? 0.f : fast_exp2(fmaf(s, scale, -ref));
-}
+// What a part with maximum m counts under the joint maximum (a part may have seen nothing).
+__device__ __forceinline__ float part_weight(float m, float top) { return m == -INFINITY ? 0.f : fast_exp2(m - top); }
 
 // Two E4M3 codes (the low or high half of w) as f16x2.
 __device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
@@ -141,7 +148,7 @@ __device__ __forceinline__ int units_of(const Span& s, int unit) { return (s.cou
 // T: 0 bf16, 1 f16, 2 E4M3 (computed in f16).  DP: head_dim rounded up to 64, 128 or
 // 256.  NT: blocks of 8 query heads.
 template <int T, int DP, int NT>
-__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(const AttendArgs a, const Plan p) {
+__global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, NT)) attend_kernel(const AttendArgs a, const Plan p) {
     constexpr bool BF = T == 0, F8 = T == 2;
     constexpr int HC = 8 * NT;
     constexpr int ES = F8 ? 1 : 2;
@@ -249,14 +256,13 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
         auto look_up = [&](int x) {
             const int j = (first_u + warp + kWarps * x) * U + lane;
             if (lane < U && x < n_mine && j < span.count) {
-                const uint32_t t = span.first + j, pg = t / (uint32_t)a.kv.page_size;
+                const uint32_t t = span.first + j, pg = (uint32_t)((uint64_t)t * p.page_mul >> p.page_shift);
                 next_entry = t - pg * a.kv.page_size;
                 next_page = table[pg];
             }
         };
-        auto issue = [&](int x) {  // the unit that look_up last saw, into slot x % stages
+        auto issue = [&](int x, int slot) {  // the unit that look_up last saw
             if (x < n_mine) {
-                const int slot = x % p.stages;
                 const bool in = lane < U && (first_u + warp + kWarps * x) * U + lane < span.count;
                 const bool ok = in && next_page >= 0 && next_page < a.kv.n_pages;
                 if (in && !ok) set_status(a.kv.status, MOE_ERR_BAD_INDEX);
@@ -268,23 +274,28 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
                 constexpr int CPR = DP * ES / 16;
                 if (mask == kAll && p.cpr == CPR) {
                     // lanes cover 32 / CPR whole rows at a time
+                    constexpr int ROWS = 32 / CPR, SW = CPR % 8 ? 0 : 7, PITCH = SW ? CPR * 16 : (CPR | 1) * 16;
                     const int col = lane % CPR * 16, row = lane / CPR;
-                    const uint32_t at = dst + row * p.pitch + col;
+                    const uint8_t *kc = kb + col, *vc = vb + col;
+                    const uint64_t unit = 1ull << p.shift;
 #pragma unroll
-                    for (int i = 0; i < U * CPR / 32; ++i) {
-                        const int64_t o = (int64_t)((uint64_t)__shfl_sync(0xffffffffu, off, i * (32 / CPR) + row) << p.shift) + col;
-                        cp_async16(at + i * (32 / CPR) * p.pitch, kb + o);
-                        cp_async16(at + (U + i * (32 / CPR)) * p.pitch, vb + o);
+                    for (int i = 0; i < U / ROWS; ++i) {
+                        const int r = i * ROWS + row;
+                        const uint64_t o = __shfl_sync(0xffffffffu, off, r) * unit;
+                        const uint32_t at = dst + r * PITCH + (col ^ (r & SW) << 4);
+                        cp_async16(at, kc + o);
+                        cp_async16(at + U * PITCH, vc + o);
                     }
                 } else {
                     for (int i0 = 0; i0 < U * p.cpr; i0 += 32) {
                         const int i = i0 + lane;
                         const int row = (int)((uint32_t)i * p.inv >> 20), col = (i - row * p.cpr) * 16;
-                        const int64_t o = (int64_t)((uint64_t)__shfl_sync(0xffffffffu, off, row & (U - 1)) << p.shift) + col;
+                        const uint64_t o = ((uint64_t)__shfl_sync(0xffffffffu, off, row & (U - 1)) << p.shift) + col;
                         if (row < U) {
                             const uint32_t bytes = (mask >> row & 1u) ? 16u : 0u;  // rows left out are zeros
-                            cp_async16(dst + row * p.pitch + col, kb + o, bytes);
-                            cp_async16(dst + (U + row) * p.pitch + col, vb + o, bytes);
+                            const uint32_t at = dst + row * p.pitch + (col ^ (row & p.swizzle) << 4);
+                            cp_async16(at, kb + o, bytes);
+                            cp_async16(at + U * p.pitch, vb + o, bytes);
                         }
                     }
                 }
@@ -293,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
         };
         look_up(0);
         for (int x = 0; x < p.stages - 1; ++x) {
-            issue(x);
+            issue(x, x);
             look_up(x + 1);
         }
 
@@ -325,7 +336,8 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
                     reinterpret_cast<uint16_t*>(s_q + h * qpitch)[d] =
                         (uint16_t)(BF ? pack_bf16(v[i] * down, 0.f) : pack_f16(v[i] * down, 0.f));
             }
-            if (lane == 0) s_scale[h] = fabsf(a.scale) * kLog2e * (F8 ? a.kv.k_scale[kh] * pow2i(e) : 1.f);
+            // never zero: a score left out (-inf) must stay -inf under it
+            if (lane == 0) s_scale[h] = fmaxf(fabsf(a.scale) * kLog2e * (F8 ? a.kv.k_scale[kh] * pow2i(e) : 1.f), 1e-37f);
         }
         __syncthreads();
 
@@ -344,12 +356,14 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
             }
         }
 
-        for (int x = 0; x < n_mine; ++x) {
-            issue(x + p.stages - 1);
+        // where ldmatrix lanes read: row lane % 16 of a tile of 16 tokens, and for keys (and E4M3 values)
+        // the 16-byte piece lane / 16 further on
+        const int sw = (lane & 7) & p.swizzle;
+        for (int x = 0, slot = 0; x < n_mine; ++x, slot = slot + 1 == p.stages ? 0 : slot + 1) {
+            issue(x + p.stages - 1, slot == 0 ? p.stages - 1 : slot - 1);
             look_up(x + p.stages);
             cp_wait(p.stages - 1);
             __syncwarp();
-            const int slot = x % p.stages;
             const uint32_t ku = ring_u + slot * unit_bytes, vu = ku + U * p.pitch;
             const uint32_t mask = s_mask[warp][slot];
             float s[MT][NT][4];
@@ -358,14 +372,15 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
 #pragma unroll
                 for (int t = 0; t < NT; ++t) s[i][t][0] = s[i][t][1] = s[i][t][2] = s[i][t][3] = 0.f;
             // matrices of a load: token halves of a 16-byte piece of the rows, then of the next piece
-            const uint32_t k_at = ku + ((lane & 7) + (lane & 8)) * p.pitch + (lane >> 4) * 16;
+            const uint32_t k_at = ku + (lane & 15) * p.pitch;
+            const int k_sw = (lane >> 4) ^ sw;  // pieces come in pairs: 2j + lane / 16 is swizzled to 2j ^ k_sw
             if constexpr (F8) {
 #pragma unroll
                 for (int kk = 0; kk < DP / 16; kk += 2) {
                     if (kk < steps) {
                         uint32_t r[MT][4];
 #pragma unroll
-                        for (int i = 0; i < MT; ++i) ldsm4(r[i], k_at + i * 16 * p.pitch + kk * 16);
+                        for (int i = 0; i < MT; ++i) ldsm4(r[i], k_at + i * 16 * p.pitch + ((kk ^ k_sw) << 4));
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             if (kk + h < steps) {
@@ -390,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
                     if (kk < steps) {
                         uint32_t r[MT][4];
 #pragma unroll
-                        for (int i = 0; i < MT; ++i) ldsm4(r[i], k_at + i * 16 * p.pitch + kk * 32);
+                        for (int i = 0; i < MT; ++i) ldsm4(r[i], k_at + i * 16 * p.pitch + (((2 * kk) ^ k_sw) << 4));
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
                             const uint8_t* q = s_q + (8 * t + g) * qpitch + kk * 32 + c * 4;
@@ -428,14 +443,14 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                     const float mn = fmaxf(m[t][j], top);
                     const float ref = mn == -INFINITY ? 0.f : mn * sc[t][j];  // nothing seen yet: every weight is 0
-                    keep[t][j] = m[t][j] == -INFINITY ? 0.f : fast_exp2(fmaf(m[t][j], sc[t][j], -ref));
+                    keep[t][j] = fast_exp2(fmaf(m[t][j], sc[t][j], -ref));
                     grown |= mn != m[t][j];
                     m[t][j] = mn;
                     float sum = 0.f;
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
-                        s[i][t][j] = weight(s[i][t][j], sc[t][j], ref);
-                        s[i][t][2 + j] = weight(s[i][t][2 + j], sc[t][j], ref);
+                        s[i][t][j] = fast_exp2(fmaf(s[i][t][j], sc[t][j], -ref));
+                        s[i][t][2 + j] = fast_exp2(fmaf(s[i][t][2 + j], sc[t][j], -ref));
                         sum += s[i][t][j] + s[i][t][2 + j];
                     }
                     l[t][j] = fmaf(l[t][j], keep[t][j], sum);
@@ -459,12 +474,12 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
 #pragma unroll
             for (int k = 0; k < MT; ++k) {
                 if constexpr (F8) {
-                    const uint32_t at = vu + (16 * k + (lane & 7) + (lane & 8)) * p.pitch + (lane >> 4) * 16;
+                    const uint32_t at = vu + (16 * k + (lane & 15)) * p.pitch;
 #pragma unroll
                     for (int i = 0; i < DP / 16; i += 2) {
                         if (i < steps) {
                             uint32_t r[4];
-                            ldsm4_t(r, at + i * 16);
+                            ldsm4_t(r, at + ((i ^ k_sw) << 4));
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 if (i + h < steps) {
@@ -479,12 +494,13 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
                         }
                     }
                 } else {
-                    const uint32_t at = vu + (16 * k + (lane & 7) + ((lane >> 4) << 3)) * p.pitch + (lane & 8) * 2;
+                    const uint32_t at = vu + (16 * k + (lane & 7) + ((lane >> 4) << 3)) * p.pitch;
+                    const int v_sw = (lane >> 3 & 1) ^ sw;
 #pragma unroll
                     for (int i = 0; i < DP / 16; ++i) {
                         if (i < steps) {
                             uint32_t r[4];
-                            ldsm4_t(r, at + i * 32);
+                            ldsm4_t(r, at + (((2 * i) ^ v_sw) << 4));
 #pragma unroll
                             for (int t = 0; t < NT; ++t) mma16816<BF>(o[i][t], r, pb[k][t][0], pb[k][t][1]);
                         }
@@ -599,34 +615,38 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_kernel(con
                 __threadfence();
                 const float* base = static_cast<const float*>(a.workspace) + p.slots;
                 auto part = [&](int i) { return base + (int64_t)(2 * i + (i == i0 ? 1 : 0)) * HC * (D + 2); };
-                if (tid < nh) {
+                // maxima and sums: a warp a head, a lane a part
+                for (int h = warp; h < nh; h += kWarps) {
                     float top = -INFINITY, sum = 0.f;
-                    for (int i = i0; i <= i1; ++i) top = fmaxf(top, part(i)[tid]);
-                    for (int i = i0; i <= i1; ++i) {
-                        const float mi = part(i)[tid];
-                        sum += mi == -INFINITY ? 0.f : part(i)[HC + tid] * fast_exp2(mi - top);
+                    for (int i = i0 + lane; i <= i1; i += 32) top = fmaxf(top, part(i)[h]);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    for (int i = i0 + lane; i <= i1; i += 32) sum += part_weight(part(i)[h], top) * part(i)[HC + h];
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (lane == 0) {
+                        s_scale[h] = top;
+                        s_inv[h] = sum != 0.f ? (F8 ? a.kv.v_scale[kh] : 1.f) / sum : 0.f;
+                        if (a.lse) a.lse[(int64_t)b * heads + h0 + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
                     }
-                    s_scale[tid] = top;
-                    s_inv[tid] = sum != 0.f ? (F8 ? a.kv.v_scale[kh] : 1.f) / sum : 0.f;
-                    if (a.lse) a.lse[(int64_t)b * heads + h0 + tid] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
                 }
                 __syncthreads();
-                for (int i = tid; i < nh * (D / 2); i += kThreads) {
-                    const int h = i / (D / 2), d = i % (D / 2) * 2;
+                for (int i = tid; i < nh * (D / 4); i += kThreads) {
+                    const int h = i / (D / 4), d = i % (D / 4) * 4;
                     const float top = s_scale[h];
-                    float2 v = make_float2(0.f, 0.f);
-#pragma unroll 4
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
                     for (int k = i0; k <= i1; ++k) {
-                        const float mi = part(k)[h];
-                        const float f = mi == -INFINITY ? 0.f : fast_exp2(mi - top);
-                        const float2 y = *reinterpret_cast<const float2*>(part(k) + 2 * HC + h * D + d);
+                        const float f = part_weight(part(k)[h], top);
+                        const float4 y = *reinterpret_cast<const float4*>(part(k) + 2 * HC + h * D + d);
                         v.x = fmaf(y.x, f, v.x);
                         v.y = fmaf(y.y, f, v.y);
+                        v.z = fmaf(y.z, f, v.z);
+                        v.w = fmaf(y.w, f, v.w);
                     }
                     const float f = s_inv[h];
-                    uint16_t* dst = static_cast<uint16_t*>(a.out) + b * a.out_ts + (h0 + h) * a.out_hs + d;
-                    *reinterpret_cast<uint32_t*>(dst) =
-                        a.q_type == MOE_BF16 ? pack_bf16(v.x * f, v.y * f) : pack_f16(v.x * f, v.y * f);
+                    float r[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
+                    store_run<4>(a.out, b * a.out_ts + (h0 + h) * a.out_hs + d, a.q_type, r);
                 }
             }
         }
@@ -647,7 +667,7 @@ int blocks_of_heads(const KvView& kv) {  // NT
 
 int dim_class(const KvView& kv) { return kv.head_dim <= 64 ? 64 : (kv.head_dim <= 128 ? 128 : 256); }
 
-int ctas_per_sm(const KvView& kv) { return kv.head_dim <= 128 ? 2 : 1; }
+int ctas_per_sm(const KvView& kv) { return ctas_an_sm(dim_class(kv), blocks_of_heads(kv)); }
 
 int unit_bytes(const KvView& kv, const Plan& p) {
     return 2 * unit_tokens(dim_class(kv) * type_bytes(kv.type)) * p.pitch;
@@ -664,12 +684,17 @@ Plan plan_of(const KvView& kv, int sm_count) {
     p.chunk = (group + p.chunks - 1) / p.chunks;
     p.cpr = kv.head_dim * es / 16;
     p.inv = ((1u << 20) + p.cpr - 1) / p.cpr;
-    p.pitch = (p.cpr | 1) * 16;
+    p.swizzle = p.cpr % 8 == 0 ? 7 : 0;
+    p.pitch = p.swizzle ? p.cpr * 16 : (p.cpr | 1) * 16;
+    int lg = 0;
+    while ((1u << lg) < (uint32_t)kv.page_size) ++lg;
+    p.page_shift = 30 + lg;
+    p.page_mul = (uint32_t)(((1ull << p.page_shift) + kv.page_size - 1) / kv.page_size);
     p.shift = attend_shift(kv);
-    p.slots = (ctas_per_sm(kv) * sm_count + 1) / 2 * 2;  // even: the sums behind the counters are read in pairs
+    p.slots = (ctas_per_sm(kv) * sm_count + 3) / 4 * 4;  // the sums behind the counters are read in fours
     // as many units in flight as fit beside the other CTA of the SM; the ring also holds
     // the warp's [hc][head_dim + 4] sums when a piece ends
-    const int budget = (ctas_per_sm(kv) == 2 ? 110 : 222) * 1024;
+    const int budget = budget_of(ctas_per_sm(kv));
     const int least = (hc * (kv.head_dim + 4) * 4 + unit_bytes(kv, p) - 1) / unit_bytes(kv, p);
     p.stages = kMaxStages;
     while (p.stages > 2 && p.stages > least && smem_of(kv, p) > budget) --p.stages;
@@ -681,7 +706,7 @@ cudaError_t launch(const AttendArgs& a, const Plan& p, cudaStream_t st) {
     static std::atomic<uint64_t> configured;
     const int smem = smem_of(a.kv, p);
     // one limit serves every head_dim of the class; the CTAs share the SM's whole memory
-    cudaError_t err = ensure_smem_limit((const void*)attend_kernel<T, DP, NT>, (DP <= 128 ? 113 : 224) * 1024, configured, true);
+    cudaError_t err = ensure_smem_limit((const void*)attend_kernel<T, DP, NT>, budget_of(ctas_an_sm(DP, NT)) + 2048, configured, true);
     if (err != cudaSuccess) return err;
     const int64_t per_b = (int64_t)a.kv.kv_heads * p.chunks;
     const int64_t room = room_of(a);
