@@ -19,6 +19,8 @@
 // same lanes for S and O, so rescaling needs no exchange.  E4M3 keys and values become
 // f16 in registers (exactly): the order of dimensions within a 16-wide step of the
 // contraction is free, so a lane's four consecutive bytes serve as its four elements.
+#include <algorithm>
+
 #include "ptx.cuh"
 #include "vec.cuh"
 
@@ -37,6 +39,7 @@ __host__ __device__ constexpr int unit_tokens(int bytes) { return bytes <= 128 ?
 constexpr int kMaxStages = 8;    // units of a warp's ring
 constexpr int kMinUnits = 4;     // units worth a CTA of its own: one a warp
 constexpr int64_t kMaxTokens = 1 << 30;  // of a sequence: token indexes stay in 32 bits
+constexpr int kBatch = 16;       // parts read at once when a split segment is joined
 constexpr float kLog2e = 1.44269504f;
 constexpr float kLn2 = 0.69314718f;
 
@@ -157,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, NT)) attend_kernel(co
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_m[kWarps][HC], s_l[kWarps][HC], s_scale[HC], s_inv[HC];
     __shared__ uint32_t s_mask[kWarps][kMaxStages];
-    __shared__ long long s_sum[kWarps], s_before;
+    __shared__ long long s_sum[kWarps], s_rest[kWarps], s_before;
     __shared__ int s_b, s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
@@ -172,11 +175,73 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, NT)) attend_kernel(co
     grid_launch_next();
     grid_dep_wait();
 
+    // ---- this CTA's stretch of the line: a scan over the lengths, kThreads at a time ----
+    const int own = blockIdx.x < a.B ? a.lengths[blockIdx.x] : 1;  // its own share of the empty sequences, below
+    const int u0 = tid < a.B ? units_of(span_of(a, tid), U) : 0;
+    long long rest = 0;  // units behind the first kThreads sequences
+    for (int b = kThreads + tid; b < a.B; b += kThreads) rest += units_of(span_of(a, b), U);
+    auto scan = [&](long long x) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        return x;
+    };
+    const long long x0 = scan(u0);
+    if (a.B > kThreads) rest = scan(rest);
+    if (lane == 31) {
+        s_sum[warp] = x0;
+        s_rest[warp] = rest;
+    }
+    __syncthreads();
+    long long ahead = 0, chunk = 0, total = 0;  // units ahead of this warp, of the first kThreads sequences, of all
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) ahead += s_sum[w];
+        chunk += s_sum[w];
+        total += s_rest[w];
+    }
+    total = (total + chunk) * per_b;
+    long long ctas = (total + kMinUnits - 1) / kMinUnits;
+    if (ctas > gridDim.x) ctas = gridDim.x;
+    long long u_begin = 0, u_end = 0;
+    if ((long long)blockIdx.x < ctas) {
+        if (total < 1 << 21) {  // in 32 bits: a grid is below 2^11
+            u_begin = (uint32_t)total * blockIdx.x / (uint32_t)ctas;
+            u_end = (uint32_t)total * (blockIdx.x + 1) / (uint32_t)ctas;
+        } else {
+            u_begin = total * blockIdx.x / ctas;
+            u_end = total * (blockIdx.x + 1) / ctas;
+        }
+        // the sequence that holds unit u_begin
+        const long long lo = (ahead + x0 - u0) * per_b;
+        if (u0 > 0 && u_begin >= lo && u_begin < lo + (long long)u0 * per_b) {
+            s_b = tid;
+            s_before = lo;
+        }
+        for (int b0 = kThreads; chunk * per_b <= u_begin; b0 += kThreads) {
+            const int b = b0 + tid, u = b < a.B ? units_of(span_of(a, b), U) : 0;
+            const long long x = scan(u);
+            __syncthreads();
+            if (lane == 31) s_sum[warp] = x;
+            __syncthreads();
+            long long at = chunk + x - u;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) at += s_sum[w];
+                chunk += s_sum[w];
+            }
+            if (u > 0 && u_begin >= at * per_b && u_begin < (at + u) * per_b) {
+                s_b = b;
+                s_before = at * per_b;
+            }
+        }
+    }
     // ---- sequences without a token, and lengths out of range ----
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const int n = a.lengths[b];
+        const int n = b == (int)blockIdx.x ? own : a.lengths[b];
         if ((n < 0 || n > room_of(a)) && tid == 0) set_status(a.kv.status, MOE_ERR_BAD_INDEX);
-        if (span_of(a, b).count > 0) continue;
+        if (n > 0 && room_of(a) > 0) continue;
         for (int i = tid; i < heads * (D / 2); i += kThreads) {
             const int h = i / (D / 2), d = i % (D / 2) * 2;
             uint16_t* o = static_cast<uint16_t*>(a.out) + b * a.out_ts + h * a.out_hs + d;
@@ -186,48 +251,8 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, NT)) attend_kernel(co
             for (int h = tid; h < heads; h += kThreads) a.lse[(int64_t)b * heads + h] = -INFINITY;
     }
 
-    // ---- this CTA's stretch of the line ----
-    long long mine = 0;
-    for (int b = tid; b < a.B; b += kThreads) mine += units_of(span_of(a, b), U);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) s_sum[warp] = mine;
-    __syncthreads();
-    long long total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += s_sum[w];
-    total *= per_b;
-    long long ctas = (total + kMinUnits - 1) / kMinUnits;
-    if (ctas > gridDim.x) ctas = gridDim.x;
     if ((long long)blockIdx.x >= ctas) return;
-    const long long u_begin = total * blockIdx.x / ctas, u_end = total * (blockIdx.x + 1) / ctas;
-    // the sequence that holds unit u_begin: a scan over the lengths, kThreads at a time
-    {
-        long long before = 0;
-        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-            const int b = b0 + tid;
-            const long long u = b < a.B ? (long long)units_of(span_of(a, b), U) * per_b : 0;
-            long long x = u;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            __syncthreads();
-            if (lane == 31) s_sum[warp] = x;
-            __syncthreads();
-            long long base = before;
-            for (int w = 0; w < warp; ++w) base += s_sum[w];
-            const long long lo = base + x - u;
-            if (u > 0 && u_begin >= lo && u_begin < lo + u) {
-                s_b = b;
-                s_before = lo;
-            }
-            for (int w = 0; w < kWarps; ++w) before += s_sum[w];
-            if (before > u_begin) break;
-        }
-        __syncthreads();
-    }
+    __syncthreads();
     int b = s_b;
     long long before = s_before;  // units ahead of sequence b
     Span span = span_of(a, b);
@@ -302,21 +327,29 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, NT)) attend_kernel(co
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        // queries first, so that they are on their way together with the first units
+        constexpr int HW = HC / kWarps;  // heads a warp brings: warp, warp + kWarps, ...
+        uint16_t raw[HW][DP / 32];
+        const float k_scale = F8 ? a.kv.k_scale[kh] : 1.f, v_scale = F8 ? a.kv.v_scale[kh] : 1.f;
+#pragma unroll
+        for (int x = 0; x < HW; ++x) {
+            const int h = warp + kWarps * x;
+            const uint16_t* src = static_cast<const uint16_t*>(a.q) + b * a.q_ts + (h0 + h) * a.q_hs;
+#pragma unroll
+            for (int i = 0; i < DP / 32; ++i) raw[x][i] = h < nh && lane + 32 * i < D ? src[lane + 32 * i] : (uint16_t)0;
+        }
         look_up(0);
         for (int x = 0; x < p.stages - 1; ++x) {
             issue(x, x);
             look_up(x + 1);
         }
-
-        // ---- queries: 16 bits, row pitch of an odd number of 16-byte pieces ----
-        for (int h = warp; h < HC; h += kWarps) {
-            const uint16_t* src = static_cast<const uint16_t*>(a.q) + b * a.q_ts + (h0 + h) * a.q_hs;
-            float v[DP / 32];
-            float top = 0.f;
+#pragma unroll
+        for (int x = 0; x < HW; ++x) {
+            const int h = warp + kWarps * x;
+            float v[DP / 32], top = 0.f;
 #pragma unroll
             for (int i = 0; i < DP / 32; ++i) {
-                const int d = lane + 32 * i;
-                v[i] = h < nh && d < D ? half_bits_to_f32(src[d], a.q_type) : 0.f;
+                v[i] = half_bits_to_f32(raw[x][i], a.q_type);
                 top = fmaxf(top, fabsf(v[i]));
             }
             int e = 0;
@@ -337,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, NT)) attend_kernel(co
                         (uint16_t)(BF ? pack_bf16(v[i] * down, 0.f) : pack_f16(v[i] * down, 0.f));
             }
             // never zero: a score left out (-inf) must stay -inf under it
-            if (lane == 0) s_scale[h] = fmaxf(fabsf(a.scale) * kLog2e * (F8 ? a.kv.k_scale[kh] * pow2i(e) : 1.f), 1e-37f);
+            if (lane == 0) s_scale[h] = fmaxf(fabsf(a.scale) * kLog2e * k_scale * (F8 ? pow2i(e) : 1.f), 1e-37f);
         }
         __syncthreads();
 
@@ -569,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, NT)) attend_kernel(co
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) sum += s_m[w][tid] == -INFINITY ? 0.f : s_l[w][tid] * fast_exp2(s_m[w][tid] - top);
             if (whole) {
-                s_inv[tid] = (F8 ? a.kv.v_scale[kh] : 1.f) / sum;
+                s_inv[tid] = v_scale / sum;
                 if (!(sum != 0.f)) s_inv[tid] = 0.f;
                 if (a.lse && tid < nh) a.lse[(int64_t)b * heads + h0 + tid] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
             } else {
@@ -615,35 +648,58 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, NT)) attend_kernel(co
                 __threadfence();
                 const float* base = static_cast<const float*>(a.workspace) + p.slots;
                 auto part = [&](int i) { return base + (int64_t)(2 * i + (i == i0 ? 1 : 0)) * HC * (D + 2); };
-                // maxima and sums: a warp a head, a lane a part
+                // a warp a head, a lane a part: maximum and sum in one pass, then every part's weight
+                const int parts = i1 - i0 + 1;
+                float* weights = reinterpret_cast<float*>(smem + HC * (DP * 2 + 16));  // [nh][parts], in the idle ring
                 for (int h = warp; h < nh; h += kWarps) {
                     float top = -INFINITY, sum = 0.f;
-                    for (int i = i0 + lane; i <= i1; i += 32) top = fmaxf(top, part(i)[h]);
+#pragma unroll 4
+                    for (int i = lane; i < parts; i += 32) {
+                        const float mi = part(i0 + i)[h], li = part(i0 + i)[HC + h];
+                        const float mn = fmaxf(top, mi);
+                        sum = sum * part_weight(top, mn) + li * part_weight(mi, mn);
+                        top = mn;
+                        weights[h * parts + i] = mi;
+                    }
+                    float all = top;
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    for (int i = i0 + lane; i <= i1; i += 32) sum += part_weight(part(i)[h], top) * part(i)[HC + h];
+                    for (int o = 16; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+                    sum *= part_weight(top, all);
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    for (int i = lane; i < parts; i += 32) weights[h * parts + i] = part_weight(weights[h * parts + i], all);
                     if (lane == 0) {
-                        s_scale[h] = top;
-                        s_inv[h] = sum != 0.f ? (F8 ? a.kv.v_scale[kh] : 1.f) / sum : 0.f;
-                        if (a.lse) a.lse[(int64_t)b * heads + h0 + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+                        s_inv[h] = sum != 0.f ? v_scale / sum : 0.f;
+                        if (a.lse) a.lse[(int64_t)b * heads + h0 + h] = sum == 0.f ? -INFINITY : (all + log2f(sum)) * kLn2;
                     }
                 }
                 __syncthreads();
                 for (int i = tid; i < nh * (D / 4); i += kThreads) {
                     const int h = i / (D / 4), d = i % (D / 4) * 4;
-                    const float top = s_scale[h];
+                    const float* from = part(i0) + 2 * HC + h * D + d;
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int k = i0; k <= i1; ++k) {
-                        const float f = part_weight(part(k)[h], top);
-                        const float4 y = *reinterpret_cast<const float4*>(part(k) + 2 * HC + h * D + d);
+                    // the first part is in its CTA's second slot, the others in the first ones
+                    auto add = [&](const float4& y, float f) {
                         v.x = fmaf(y.x, f, v.x);
                         v.y = fmaf(y.y, f, v.y);
                         v.z = fmaf(y.z, f, v.z);
                         v.w = fmaf(y.w, f, v.w);
+                    };
+                    add(*reinterpret_cast<const float4*>(from), weights[h * parts]);
+                    from += HC * (D + 2);
+                    int k = 1;
+                    for (; k + kBatch <= parts; k += kBatch) {
+                        float4 y[kBatch];
+#pragma unroll
+                        for (int x = 0; x < kBatch; ++x)
+                            y[x] = *reinterpret_cast<const float4*>(from + (int64_t)2 * x * HC * (D + 2));
+#pragma unroll
+                        for (int x = 0; x < kBatch; ++x) add(y[x], weights[h * parts + k + x]);
+                        from += (int64_t)2 * kBatch * HC * (D + 2);
                     }
+#pragma unroll 4
+                    for (; k < parts; ++k, from += 2 * HC * (D + 2))
+                        add(*reinterpret_cast<const float4*>(from), weights[h * parts + k]);
                     const float f = s_inv[h];
                     float r[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
                     store_run<4>(a.out, b * a.out_ts + (h0 + h) * a.out_hs + d, a.q_type, r);
@@ -685,15 +741,16 @@ Plan plan_of(const KvView& kv, int sm_count) {
     p.cpr = kv.head_dim * es / 16;
     p.inv = ((1u << 20) + p.cpr - 1) / p.cpr;
     p.swizzle = p.cpr % 8 == 0 ? 7 : 0;
-    p.pitch = p.swizzle ? p.cpr * 16 : (p.cpr | 1) * 16;
+    p.pitch = p.swizzle ? p.cpr * 16 : std::max(p.cpr | 1, 3) * 16;
     int lg = 0;
     while ((1u << lg) < (uint32_t)kv.page_size) ++lg;
     p.page_shift = 30 + lg;
     p.page_mul = (uint32_t)(((1ull << p.page_shift) + kv.page_size - 1) / kv.page_size);
     p.shift = attend_shift(kv);
     p.slots = (ctas_per_sm(kv) * sm_count + 3) / 4 * 4;  // the sums behind the counters are read in fours
-    // as many units in flight as fit beside the other CTA of the SM; the ring also holds
-    // the warp's [hc][head_dim + 4] sums when a piece ends
+    // as many units in flight as fit beside the other CTAs of the SM; the ring also holds the
+    // warp's [hc][head_dim + 4] sums when a piece ends, and the parts' weights (hc * slots floats
+    // at most: 38 KB, below the 64 KB of the smallest ring) when a segment is joined
     const int budget = budget_of(ctas_per_sm(kv));
     const int least = (hc * (kv.head_dim + 4) * 4 + unit_bytes(kv, p) - 1) / unit_bytes(kv, p);
     p.stages = kMaxStages;
