@@ -39,7 +39,6 @@ __host__ __device__ constexpr int unit_tokens(int bytes) { return bytes <= 128 ?
 constexpr int kMaxStages = 8;    // units of a warp's ring
 constexpr int kMinUnits = 4;     // units worth a CTA of its own: one a warp
 constexpr int64_t kMaxTokens = 1 << 30;  // of a sequence: token indexes stay in 32 bits
-constexpr int kBatch = 16;       // parts read at once when a split segment is joined
 constexpr float kLog2e = 1.44269504f;
 constexpr float kLn2 = 0.69314718f;
 
@@ -648,9 +647,29 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, NT)) attend_kernel(co
                 __threadfence();
                 const float* base = static_cast<const float*>(a.workspace) + p.slots;
                 auto part = [&](int i) { return base + (int64_t)(2 * i + (i == i0 ? 1 : 0)) * HC * (D + 2); };
-                // a warp a head, a lane a part: maximum and sum in one pass, then every part's weight
-                const int parts = i1 - i0 + 1;
-                float* weights = reinterpret_cast<float*>(smem + HC * (DP * 2 + 16));  // [nh][parts], in the idle ring
+                // the parts' sums come through the idle ring, as many as it holds at once; a thread adds up
+                // what it copied itself.  Meanwhile a warp a head and a lane a part find the joint
+                // maximum and sum, then every part's weight
+                constexpr int IT = (HC * DP / 4 + kThreads - 1) / kThreads;  // 4-wide pieces of a thread
+                const int parts = i1 - i0 + 1, pieces = nh * (D / 4);
+                float* weights = reinterpret_cast<float*>(smem + HC * (DP * 2 + 16));  // [nh][parts]
+                float4* room = reinterpret_cast<float4*>(weights + (nh * parts + 3) / 4 * 4);
+                const int fit = (kWarps * p.stages * unit_bytes / 4 - (nh * parts + 3) / 4 * 4) / (nh * D);
+                const int stride = 2 * HC * (D + 2);  // floats from a CTA's slots to the next one's
+                auto bring = [&](int k0) {
+                    // the first part is in its CTA's second slot, the others in the first ones
+                    const float* from = part(i0 + k0) + 2 * HC + 4 * tid;
+                    uint32_t to = smem_u32(room + tid);
+#pragma unroll 4
+                    for (int k = k0; k < min(parts, k0 + fit); ++k) {
+#pragma unroll
+                        for (int x = 0; x < IT; ++x)
+                            if (tid + x * kThreads < pieces) cp_async16(to + x * kThreads * 16, from + 4 * x * kThreads);
+                        from += k == 0 ? stride / 2 : stride;
+                        to += pieces * 16;
+                    }
+                };
+                bring(0);
                 for (int h = warp; h < nh; h += kWarps) {
                     float top = -INFINITY, sum = 0.f;
 #pragma unroll 4
@@ -674,35 +693,41 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, NT)) attend_kernel(co
                     }
                 }
                 __syncthreads();
-                for (int i = tid; i < nh * (D / 4); i += kThreads) {
-                    const int h = i / (D / 4), d = i % (D / 4) * 4;
-                    const float* from = part(i0) + 2 * HC + h * D + d;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    // the first part is in its CTA's second slot, the others in the first ones
-                    auto add = [&](const float4& y, float f) {
-                        v.x = fmaf(y.x, f, v.x);
-                        v.y = fmaf(y.y, f, v.y);
-                        v.z = fmaf(y.z, f, v.z);
-                        v.w = fmaf(y.w, f, v.w);
-                    };
-                    add(*reinterpret_cast<const float4*>(from), weights[h * parts]);
-                    from += HC * (D + 2);
-                    int k = 1;
-                    for (; k + kBatch <= parts; k += kBatch) {
-                        float4 y[kBatch];
+                float4 v[IT];
+                const float* w[IT];
 #pragma unroll
-                        for (int x = 0; x < kBatch; ++x)
-                            y[x] = *reinterpret_cast<const float4*>(from + (int64_t)2 * x * HC * (D + 2));
-#pragma unroll
-                        for (int x = 0; x < kBatch; ++x) add(y[x], weights[h * parts + k + x]);
-                        from += (int64_t)2 * kBatch * HC * (D + 2);
-                    }
+                for (int x = 0; x < IT; ++x) {
+                    v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    w[x] = weights + min(tid + x * kThreads, pieces - 1) / (D / 4) * parts;
+                }
+                for (int k0 = 0; k0 < parts; k0 += fit) {
+                    if (k0 > 0) bring(k0);
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    const float4* y0 = room + tid;
 #pragma unroll 4
-                    for (; k < parts; ++k, from += 2 * HC * (D + 2))
-                        add(*reinterpret_cast<const float4*>(from), weights[h * parts + k]);
-                    const float f = s_inv[h];
-                    float r[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
-                    store_run<4>(a.out, b * a.out_ts + (h0 + h) * a.out_hs + d, a.q_type, r);
+                    for (int k = k0; k < min(parts, k0 + fit); ++k, y0 += pieces) {
+#pragma unroll
+                        for (int x = 0; x < IT; ++x) {
+                            if (tid + x * kThreads < pieces) {
+                                const float f = w[x][k];
+                                const float4 y = y0[x * kThreads];
+                                v[x].x = fmaf(y.x, f, v[x].x);
+                                v[x].y = fmaf(y.y, f, v[x].y);
+                                v[x].z = fmaf(y.z, f, v[x].z);
+                                v[x].w = fmaf(y.w, f, v[x].w);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < IT; ++x) {
+                    const int i = tid + x * kThreads;
+                    if (i < pieces) {
+                        const int h = i / (D / 4), d = i % (D / 4) * 4;
+                        const float f = s_inv[h];
+                        float r[4] = {v[x].x * f, v[x].y * f, v[x].z * f, v[x].w * f};
+                        store_run<4>(a.out, b * a.out_ts + (h0 + h) * a.out_hs + d, a.q_type, r);
+                    }
                 }
             }
         }
@@ -749,8 +774,9 @@ Plan plan_of(const KvView& kv, int sm_count) {
     p.shift = attend_shift(kv);
     p.slots = (ctas_per_sm(kv) * sm_count + 3) / 4 * 4;  // the sums behind the counters are read in fours
     // as many units in flight as fit beside the other CTAs of the SM; the ring also holds the
-    // warp's [hc][head_dim + 4] sums when a piece ends, and the parts' weights (hc * slots floats
-    // at most: 38 KB, below the 64 KB of the smallest ring) when a segment is joined
+    // warp's [hc][head_dim + 4] sums when a piece ends, and when a segment is joined the parts'
+    // weights (hc * slots floats at most: 29 of 60 KB with three CTAs an SM, 38 of 96 KB with two)
+    // with the sums of one part or more (16 KB at most)
     const int budget = budget_of(ctas_per_sm(kv));
     const int least = (hc * (kv.head_dim + 4) * 4 + unit_bytes(kv, p) - 1) / unit_bytes(kv, p);
     p.stages = kMaxStages;
