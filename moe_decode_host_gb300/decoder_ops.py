@@ -18,26 +18,40 @@ _TYPE = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F3
 _ACT = {None: MOE_ACT_NONE, "none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU}
 
 
+# cudaStream_t of a device's current torch stream, without building a Stream object (3 us)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _refuse(where: str, why: str):
     raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {why}")
 
 
+def _stream(stream, t) -> int:
+    return _raw_stream(t.get_device()) if stream is None else stream_handle(stream)
+
+
 def _type(t, where: str, name: str) -> int:
-    """Type code of a CUDA tensor whose innermost dimension is contiguous."""
+    """Type code of a tensor of one of the four types."""
     code = _TYPE.get(t.dtype, -1)
     if code < 0:
         _refuse(where, f"{name} has type {t.dtype}")
-    if not t.is_cuda:
-        _refuse(where, f"{name} is not on a GPU")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        _refuse(where, f"{name} is not contiguous in its last dimension")
     return code
 
 
-def _vector(t, n: int, dtype, where: str, name: str) -> int:
-    """Pointer of a contiguous CUDA vector of n elements of one type."""
-    if t.dtype != dtype or not t.is_cuda or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        _refuse(where, f"{name} is not a contiguous CUDA vector of {n} {dtype}")
+def _rows(t, shape, where: str, name: str) -> int:
+    """Row stride of a CUDA tensor [rows, n] of that shape with contiguous rows."""
+    if t.shape != shape or not t.is_cuda:
+        _refuse(where, f"{name} is not a CUDA tensor {list(shape)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and shape[1] > 1:
+        _refuse(where, f"{name} is not contiguous in its last dimension")
+    return s0
+
+
+def _vector(t, n: int, where: str, name: str, dtype=None) -> int:
+    """Pointer of a contiguous CUDA vector of n elements (of one type)."""
+    if (dtype is not None and t.dtype != dtype) or not t.is_cuda or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        _refuse(where, f"{name} is not a contiguous CUDA vector of {n} {'elements' if dtype is None else dtype}")
     return t.data_ptr()
 
 
@@ -48,32 +62,25 @@ def moe_add_rms_norm(x, weight, y, residual=None, sum_out=None, scale=None, eps=
     None; y [T, H].  A float8_e4m3fn y holds y / scale[t], scale [T] fp32 being the
     row's largest |y| / 448.  sum_out may be residual or x; y may be x."""
     w = "moe_add_rms_norm"
-    if x.dim() != 2:
-        _refuse(w, "x is not [T, H]")
     shape = x.shape
+    if len(shape) != 2:
+        _refuse(w, "x is not [T, H]")
     T, H = shape
-    xt, yt = _type(x, w, "x"), _type(y, w, "y")
-    if y.shape != shape:
-        _refuse(w, "y has another shape than x")
-    rp = rs = sp = ss = wp = wt = rt = 0
+    xt, xs = _type(x, w, "x"), _rows(x, shape, w, "x")
+    yt, ys = _type(y, w, "y"), _rows(y, shape, w, "y")
+    rp = rs = sp = ss = wp = wt = rt = cp = 0
     if residual is not None:
-        if residual.shape != shape:
-            _refuse(w, "residual has another shape than x")
-        rt, rp, rs = _type(residual, w, "residual"), residual.data_ptr(), residual.stride(0)
+        rt, rs, rp = _type(residual, w, "residual"), _rows(residual, shape, w, "residual"), residual.data_ptr()
     if sum_out is not None:
-        st = _type(sum_out, w, "sum_out")
-        if sum_out.shape != shape or (residual is not None and st != rt):
-            _refuse(w, "sum_out has another shape than x or another type than residual")
-        rt, sp, ss = st, sum_out.data_ptr(), sum_out.stride(0)
+        if residual is not None and sum_out.dtype != residual.dtype:
+            _refuse(w, "sum_out has another type than residual")
+        rt, ss, sp = _type(sum_out, w, "sum_out"), _rows(sum_out, shape, w, "sum_out"), sum_out.data_ptr()
     if weight is not None:
-        wt, wp = _type(weight, w, "weight"), weight.data_ptr()
-        if weight.dim() != 1 or weight.shape[0] != H:
-            _refuse(w, "weight is not [H]")
-    cp = 0
+        wt, wp = _type(weight, w, "weight"), _vector(weight, H, w, "weight")
     if scale is not None:
-        cp = _vector(scale, T, torch.float32, w, "scale")
-    check(lib.moe_add_rms_norm(x.data_ptr(), xt, x.stride(0), rp, rt, rs, wp, wt, eps, T, H, sp, ss, y.data_ptr(), yt,
-                               y.stride(0), cp, stream_handle(stream)), w)
+        cp = _vector(scale, T, w, "scale", torch.float32)
+    check(lib.moe_add_rms_norm(x.data_ptr(), xt, xs, rp, rt, rs, wp, wt, eps, T, H, sp, ss, y.data_ptr(), yt, ys, cp,
+                               _stream(stream, x)), w)
 
 
 class KvCache:
@@ -88,14 +95,16 @@ class KvCache:
         w = "moe_kv_create"
         self.handle = None
         t = _type(k, w, "k")
-        if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride() or _type(v, w, "v") != t:
+        if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride() or v.dtype != k.dtype:
             _refuse(w, "k and v are not [n_pages, page_size, kv_heads, head_dim] of one type and one set of strides")
+        if not k.is_cuda or not v.is_cuda or k.stride(3) != 1:
+            _refuse(w, "k and v are not on a GPU or not contiguous in their last dimension")
         n_pages, page, kv_heads, dim = k.shape
         ks = vs = 0
         if k_scale is not None:
-            ks = _vector(k_scale, kv_heads, torch.float32, w, "k_scale")
+            ks = _vector(k_scale, kv_heads, w, "k_scale", torch.float32)
         if v_scale is not None:
-            vs = _vector(v_scale, kv_heads, torch.float32, w, "v_scale")
+            vs = _vector(v_scale, kv_heads, w, "v_scale", torch.float32)
         p = moe_kv_params(n_pages, page, kv_heads, q_heads, dim, t, max_batch, k.stride(0), k.stride(1), k.stride(2))
         h = ctypes.c_void_p()
         check(lib.moe_kv_create(ctypes.byref(p), k.data_ptr(), v.data_ptr(), ks, vs, ctypes.byref(h)), w)
@@ -124,9 +133,9 @@ class KvCache:
         check(lib.moe_kv_clear_status(self.handle), "moe_kv_clear_status")
 
 
-def _heads(t, shape, code: int, where: str, name: str):
+def _heads(t, shape, dtype, where: str, name: str):
     """(pointer, outer stride, head stride) of a [rows, heads, head_dim] tensor."""
-    if t.shape != shape or _TYPE.get(t.dtype, -1) != code or not t.is_cuda:
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
         _refuse(where, f"{name} is not a CUDA tensor {list(shape)} of the call's type")
     s0, s1, s2 = t.stride()
     if s2 != 1:
@@ -143,25 +152,23 @@ def moe_kv_append(kv: KvCache, q, k, v, positions, slots, cos_sin, q_out, interl
     (cosines, then sines), or None for no rotation.  interleaved pairs (2i, 2i + 1)
     instead of (i, i + rot_dim / 2).  q_out may be q."""
     w = "moe_kv_append"
-    if q.dim() != 3:
-        _refuse(w, "q is not [T, q_heads, head_dim]")
-    T = q.shape[0]
     code = _type(q, w, "q")
+    T, dtype = len(q), q.dtype
     qs, ks = (T, kv.q_heads, kv.head_dim), (T, kv.kv_heads, kv.head_dim)
-    qp, q0, q1 = _heads(q, qs, code, w, "q")
-    kp, k0, k1 = _heads(k, ks, code, w, "k")
-    vp, v0, v1 = _heads(v, ks, code, w, "v")
-    op, o0, o1 = _heads(q_out, qs, code, w, "q_out")
+    qp, q0, q1 = _heads(q, qs, dtype, w, "q")
+    kp, k0, k1 = _heads(k, ks, dtype, w, "k")
+    vp, v0, v1 = _heads(v, ks, dtype, w, "v")
+    op, o0, o1 = _heads(q_out, qs, dtype, w, "q_out")
     pp = tp = n_pos = rot = 0
     if cos_sin is not None:
         if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_cuda or not cos_sin.is_contiguous():
             _refuse(w, "cos_sin is not a contiguous CUDA fp32 [positions, rot_dim]")
         tp = cos_sin.data_ptr()
         n_pos, rot = cos_sin.shape
-        pp = _vector(positions, T, torch.int32, w, "positions")
-    sp = _vector(slots, T, torch.int64, w, "slots")
+        pp = _vector(positions, T, w, "positions", torch.int32)
+    sp = _vector(slots, T, w, "slots", torch.int64)
     check(lib.moe_kv_append(kv.handle, code, qp, q0, q1, kp, k0, k1, vp, v0, v1, pp, sp, tp, n_pos, rot,
-                            1 if interleaved else 0, T, op, o0, o1, stream_handle(stream)), w)
+                            1 if interleaved else 0, T, op, o0, o1, _stream(stream, q)), w)
 
 
 def moe_kv_attend(kv: KvCache, q, page_table, lengths, out, scale=None, window=0, lse=None, stream=None):
@@ -172,19 +179,18 @@ def moe_kv_attend(kv: KvCache, q, page_table, lengths, out, scale=None, window=0
     head_dim ** -0.5; window: only the last `window` tokens count (0: all); lse fp32
     [B, q_heads] receives the log of the softmax sums."""
     w = "moe_kv_attend"
-    if q.dim() != 3:
-        _refuse(w, "q is not [B, q_heads, head_dim]")
-    B = q.shape[0]
-    code = _TYPE.get(q.dtype, -1)
+    code = _type(q, w, "q")
+    B, dtype = len(q), q.dtype
     shape = (B, kv.q_heads, kv.head_dim)
-    qp, q0, q1 = _heads(q, shape, code, w, "q")
-    op, o0, o1 = _heads(out, shape, code, w, "out")
-    if page_table.dtype != torch.int32 or not page_table.is_cuda or page_table.dim() != 2 or page_table.shape[0] != B:
+    qp, q0, q1 = _heads(q, shape, dtype, w, "q")
+    op, o0, o1 = _heads(out, shape, dtype, w, "out")
+    if page_table.dtype != torch.int32 or not page_table.is_cuda or page_table.dim() != 2 or len(page_table) != B:
         _refuse(w, "page_table is not a CUDA int32 [B, max_pages]")
     per = page_table.shape[1]
-    if per > 1 and page_table.stride(1) != 1:
+    t0, t1 = page_table.stride()
+    if per > 1 and t1 != 1:
         _refuse(w, "page_table is not contiguous in its last dimension")
-    lp = _vector(lengths, B, torch.int32, w, "lengths")
+    lp = _vector(lengths, B, w, "lengths", torch.int32)
     zp = 0
     if lse is not None:
         if lse.dtype != torch.float32 or not lse.is_cuda or lse.shape != (B, kv.q_heads) or not lse.is_contiguous():
@@ -192,8 +198,8 @@ def moe_kv_attend(kv: KvCache, q, page_table, lengths, out, scale=None, window=0
         zp = lse.data_ptr()
     if scale is None:
         scale = kv.head_dim ** -0.5
-    check(lib.moe_kv_attend(kv.handle, qp, code, q0, q1, page_table.data_ptr(), page_table.stride(0), per, lp, B,
-                            scale, window, op, o0, o1, zp, stream_handle(stream)), w)
+    check(lib.moe_kv_attend(kv.handle, qp, code, q0, q1, page_table.data_ptr(), t0, per, lp, B, scale, window, op, o0,
+                            o1, zp, _stream(stream, q)), w)
 
 
 def moe_linear(x, w, y, bias=None, act="none", residual=None, x_scale=None, w_scale=None, status=None,
@@ -205,31 +211,27 @@ def moe_linear(x, w, y, bias=None, act="none", residual=None, x_scale=None, w_sc
     bias [N]; residual [T, N] of y's type (may be y); act "none", "relu", "silu" or
     "gelu" (exact); status int32 [1], set to MOE_ERR_TIMEOUT if a device wait ran out."""
     f = "moe_linear"
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+    shape, wide = x.shape, w.shape
+    if len(shape) != 2 or len(wide) != 2 or shape[1] != wide[1]:
         _refuse(f, "x is not [T, K] or w is not [N, K]")
-    T, K = x.shape
-    N = w.shape[0]
+    T, K = shape
+    N = wide[0]
     code, yt = _type(x, f, "x"), _type(y, f, "y")
-    if _type(w, f, "w") != code:
+    if w.dtype != x.dtype:
         _refuse(f, "x and w have different types")
-    if y.shape != (T, N):
-        _refuse(f, "y is not [T, N]")
-    bp = bt = rp = rs = xs = ws = 0
+    xs, ws, ys = _rows(x, shape, f, "x"), _rows(w, wide, f, "w"), _rows(y, (T, N), f, "y")
+    bp = bt = rp = rs = xp = wp = sp = 0
     if bias is not None:
-        bt, bp = _type(bias, f, "bias"), bias.data_ptr()
-        if bias.dim() != 1 or bias.shape[0] != N:
-            _refuse(f, "bias is not [N]")
+        bt, bp = _type(bias, f, "bias"), _vector(bias, N, f, "bias")
     if residual is not None:
-        if residual.shape != y.shape or _type(residual, f, "residual") != yt:
-            _refuse(f, "residual has another shape or type than y")
-        rp, rs = residual.data_ptr(), residual.stride(0)
+        if residual.dtype != y.dtype:
+            _refuse(f, "residual has another type than y")
+        rp, rs = residual.data_ptr(), _rows(residual, (T, N), f, "residual")
     if x_scale is not None:
-        xs = _vector(x_scale, T, torch.float32, f, "x_scale")
+        xp = _vector(x_scale, T, f, "x_scale", torch.float32)
     if w_scale is not None:
-        ws = _vector(w_scale, N, torch.float32, f, "w_scale")
-    sp = 0
+        wp = _vector(w_scale, N, f, "w_scale", torch.float32)
     if status is not None:
-        sp = _vector(status, 1, torch.int32, f, "status")
-    a = _ACT.get(act, -1)
-    check(lib.moe_linear(x.data_ptr(), x.stride(0), w.data_ptr(), w.stride(0), code, T, N, K, xs, ws, bp, bt, a, rp,
-                         rs, y.data_ptr(), yt, y.stride(0), sp, stream_handle(stream)), f)
+        sp = _vector(status, 1, f, "status", torch.int32)
+    check(lib.moe_linear(x.data_ptr(), xs, w.data_ptr(), ws, code, T, N, K, xp, wp, bp, bt, _ACT.get(act, -1), rp, rs,
+                         y.data_ptr(), yt, ys, sp, _stream(stream, x)), f)
