@@ -14,6 +14,8 @@
 //                 tokens x up to 256 outputs (cta_group::2: each CTA stages half of both
 //                 operands), persistent, with two accumulators so that the epilogue of a
 //                 tile runs under the next tile's products.
+#include <algorithm>
+
 #include "ptx.cuh"
 #include "vec.cuh"
 
@@ -29,8 +31,7 @@ constexpr int kMaxStages = 12;
 // sums ([128][128] fp32 at most) fit the smaller ring, so that more clusters run at once.
 __host__ __device__ constexpr int split_ring(int ctas) { return ctas == 2 ? 104 * 1024 : 192 * 1024; }
 constexpr int kSplitMax = 8;           // CTAs of a cluster
-constexpr int kTileStages = 6;
-constexpr int kTileStage = 2 * kABytes;
+constexpr int kTileRing = 192 * 1024;  // bytes of the tiled kernel's ring
 constexpr int kEpiBytes = 32 * 32 * 4;  // staging of an epilogue warp of the tiled kernel: 32 tokens x 32 outputs
 
 struct Head {
@@ -39,7 +40,7 @@ struct Head {
     int abort;
 };
 constexpr int split_smem(int ctas) { return 1024 + split_ring(ctas) + (int)sizeof(Head); }
-constexpr int kTileSmem = 1024 + kTileStages * kTileStage + kEpiWarps * kEpiBytes + (int)sizeof(Head);
+constexpr int kTileSmem = 1024 + kTileRing + kEpiWarps * kEpiBytes + (int)sizeof(Head);
 static_assert(kTileSmem <= 227 * 1024, "shared memory of a CTA");
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -117,24 +118,64 @@ __device__ __forceinline__ uint32_t mma_idesc(int in_type, int m, int n) {
     return (1u << 4) | (f << 7) | (f << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// GELU(v) = v * Phi(v).  Phi(-|v|) = erfc(|v| / sqrt 2) / 2 by Abramowitz and Stegun 7.1.26
-// (t = 1 / (1 + p x), a polynomial in t times exp(-x^2); absolute error of erf 1.5e-7).
-__device__ __forceinline__ float gelu(float v) {
-    const float x = fabsf(v) * 0.70710678f;
-    const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-    float p = fmaf(1.061405429f, t, -1.453152027f);
-    p = fmaf(p, t, 1.421413741f);
-    p = fmaf(p, t, -0.284496736f);
-    p = fmaf(p, t, 0.254829592f);
-    const float tail = 0.5f * p * t * __expf(-x * x);
-    return v * (v > 0.f ? 1.f - tail : tail);
+// Two fp32 operations an instruction.
+struct Pair {
+    uint64_t v;
+};
+__device__ __forceinline__ Pair pair(float a, float b) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(Pair p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v)); }
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// GELU of two values, v Phi(v) = (v + |v|) / 2 - |v| Phi(-|v|), with
+// Phi(-x) = erfc(x / sqrt 2) / 2 by Abramowitz and Stegun 7.1.28: erfc(x) =
+// (1 + a1 x + ... + a6 x^6)^-16, absolute error 3e-7; the powers of 1 / sqrt 2 are in the
+// coefficients.  At 64 the power has long overflowed and the tail is 0; the argument is held
+// there, so that an infinity meets no zero.  (Against 7.1.26, which takes an exponential as
+// well: 8192 x 6144 x 4096 with GELU back to back 264 -> 256 us.)
+__device__ __forceinline__ void gelu2(float& v0, float& v1) {
+    const float x0 = fabsf(v0), x1 = fabsf(v1);
+    const Pair x = pair(fminf(x0, 64.f), fminf(x1, 64.f));
+    auto both = [](float c) { return pair(c, c); };
+    Pair p = fma2(x, both(5.38297491e-6f), both(4.88906371e-5f));
+    p = fma2(p, x, both(3.80035744e-5f));
+    p = fma2(p, x, both(3.27762635e-3f));
+    p = fma2(p, x, both(2.11410057e-2f));
+    p = fma2(p, x, both(4.98673469e-2f));
+    p = fma2(p, x, both(1.f));
+    p = mul2(p, p);
+    p = mul2(p, p);
+    p = mul2(p, p);
+    p = mul2(p, p);
+    float p0, p1;
+    unpair(p, p0, p1);
+    const Pair tail = mul2(x, pair(fast_rcp(p0), fast_rcp(p1)));
+    const Pair pos = fma2(pair(v0, v1), both(0.5f), mul2(pair(x0, x1), both(0.5f)));
+    unpair(fma2(tail, both(-0.5f), pos), v0, v1);
 }
 
 template <int VEC>
 __device__ __forceinline__ void activate(float (&v)[VEC], int act) {
     if (act == MOE_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = gelu(v[i]);
+        for (int i = 0; i < VEC; i += 2) gelu2(v[i], v[i + 1]);
     } else if (act == MOE_ACT_SILU) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = __fdividef(v[i], 1.f + __expf(-v[i]));
@@ -373,6 +414,7 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
 
 struct TileGrid {
     int tm, tn, bn;  // tiles along tokens (of 256) and outputs (of bn)
+    int stages;
 };
 
 // Tile i: bands of 8 token tiles, the outputs' tiles walked within a band, so that the
@@ -390,7 +432,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap xmap, const TileGrid g, bool vec) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t* epi = base + kTileStages * kTileStage;
+    uint8_t* epi = base + kTileRing;
+    const int stage_bytes = kABytes + g.bn / 2 * kRowBytes;
     Head& hd = *reinterpret_cast<Head*>(epi + kEpiWarps * kEpiBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -400,7 +443,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         prefetch_tmap(&wmap);
         prefetch_tmap(&xmap);
         hd.abort = 0;
-        for (int s = 0; s < kTileStages; ++s) {
+        for (int s = 0; s < g.stages; ++s) {
             mbar_init(&hd.full[s], 1);
             mbar_init(&hd.empty[s], 1);
         }
@@ -440,15 +483,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                uint8_t* st = base + (size_t)s * kTileStage;
+                uint8_t* st = base + (size_t)s * stage_bytes;
                 const uint32_t bar = map_rank(smem_u32(&hd.full[s]), 0);
                 if (rank == 0) mbar_arrive_expect_tx_elect(&hd.full[s], bytes);
                 tma_load_pair_elect(st, &xmap, kb * (F8 ? 128 : 64), t0, bar, keep);
                 tma_load_pair_elect(st + kABytes, &wmap, kb * (F8 ? 128 : 64), n0, bar, keep);
-                advance(s, ph, kTileStages);
+                advance(s, ph, g.stages);
             }
         }
-        if (ok) drain(hd, s, ph, kTileStages, (int64_t)nkb * ((tiles - pair + pairs - 1) / pairs));
+        if (ok) drain(hd, s, ph, g.stages, (int64_t)nkb * ((tiles - pair + pairs - 1) / pairs));
     } else if (warp == 1 && rank == 0) {
         const uint32_t idesc = mma_idesc(a.in_type, 256, g.bn);
         int s = 0, buf = 0;
@@ -463,13 +506,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint64_t ad = sw128_desc(smem_u32(base + (size_t)s * kTileStage));
-                const uint64_t bd = sw128_desc(smem_u32(base + (size_t)s * kTileStage + kABytes));
+                const uint64_t ad = sw128_desc(smem_u32(base + (size_t)s * stage_bytes));
+                const uint64_t bd = sw128_desc(smem_u32(base + (size_t)s * stage_bytes + kABytes));
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     mma_elect<F8, 2>(tmem + buf * 256, ad + 2 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
                 commit_pair_elect(&hd.empty[s]);
-                advance(s, ph, kTileStages);
+                advance(s, ph, g.stages);
             }
             if (!ok) break;
             commit_pair_elect(&hd.acc_full[buf]);
@@ -575,6 +618,8 @@ bool encode_rows(CUtensorMap* map, const LinearArgs& a, const void* p, int rows,
 template <int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS) footprint_kernel() {}
 
+int split_stages(int ctas, int bn) { return std::min(kMaxStages, split_ring(ctas) / (kABytes + bn * kRowBytes)); }
+
 template <int CTAS>
 cudaError_t cluster_size(int64_t blocks, int nkb, int* out) {
     static std::atomic<int> known[64][kSplitMax + 1];
@@ -613,20 +658,14 @@ cudaError_t cluster_size(int64_t blocks, int nkb, int* out) {
 }
 
 template <bool F8, int CTAS>
-cudaError_t launch_split(const LinearArgs& a, int bn, bool vec, cudaStream_t st) {
+cudaError_t launch_split(const LinearArgs& a, int bn, int ksplit, bool vec, cudaStream_t st) {
     CUtensorMap wmap, xmap;
     if (!encode_rows(&wmap, a, a.w, a.N, a.w_stride, 128) || !encode_rows(&xmap, a, a.x, a.T, a.x_stride, bn))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> configured;
     cudaError_t err = ensure_smem_limit((const void*)linear_split_kernel<F8, CTAS>, split_smem(CTAS), configured, true);
     if (err != cudaSuccess) return err;
-    const int tz = (a.T + bn - 1) / bn;
-    const int nkb = (int)(((int64_t)a.K * type_bytes(a.in_type) + kRowBytes - 1) / kRowBytes);
-    int ksplit = 1;
-    err = cluster_size<CTAS>((int64_t)((a.N + 127) / 128) * tz, nkb, &ksplit);
-    if (err != cudaSuccess) return err;
-    int stages = split_ring(CTAS) / (kABytes + bn * kRowBytes);
-    if (stages > kMaxStages) stages = kMaxStages;
+    const int tz = (a.T + bn - 1) / bn, stages = split_stages(CTAS, bn);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ksplit, (a.N + 127) / 128, tz);
     cfg.blockDim = dim3(kThreads);
@@ -658,28 +697,44 @@ cudaError_t launch_tiles(const LinearArgs& a, const TileGrid& g, bool vec, cudaS
 
 }  // namespace
 
+// Which kernel, by what each is expected to take in ns (measured on bf16 products of 64 to
+// 8192 tokens, 256 to 8192 outputs and depths of 256 to 8192; a block of K is the 128 bytes of a stage):
+//  tiles  4500 + rounds * blocks of K * max(200, 100 + 0.95 bn); below 200 a stage's latency
+//         over the ring's depth shows.  512 x 4096 x 4096: 18.5 us against 20.4 split.
+//  split  3000 + 20 bn for the join + blocks of K of a CTA * (200 + 0.8 bn).
+//         256 x 1024 x 4096: 11.1 us against 15.6 in tiles.
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
     const bool f8 = a.in_type == MOE_E4M3;
     const bool vec = runs_aligned(a.y, a.y_type, 8, a.y_stride) && (!a.res || runs_aligned(a.res, a.y_type, 8, a.res_stride));
+    const int nkb = (int)(((int64_t)a.K * type_bytes(a.in_type) + kRowBytes - 1) / kRowBytes);
     const int pairs = a.sm_count / 2;
-    // the width of the tiled kernel's tiles that leaves the least work to the last round
-    TileGrid g{(a.T + 255) / 256, 0, 0};
-    int64_t best = INT64_MAX;
-    for (int bn = 256; bn >= 128; bn -= 32) {
+    TileGrid g{(a.T + 255) / 256, 0, 0, 0};
+    int64_t tiles_ns = INT64_MAX;
+    for (int bn = 256; bn >= 64; bn -= 32) {  // the width that leaves the least work to the last round
         const int64_t tn = (a.N + bn - 1) / bn, rounds = (g.tm * tn + pairs - 1) / pairs;
-        const int64_t cost = rounds * (bn + 16);
-        if (cost < best) {
-            best = cost;
+        const int64_t ns = 4500 + rounds * nkb * std::max(200, 100 + bn * 95 / 100);
+        if (ns < tiles_ns) {
+            tiles_ns = ns;
             g.tn = (int)tn;
             g.bn = bn;
+            g.stages = std::min(kMaxStages, kTileRing / (kABytes + bn / 2 * kRowBytes));
         }
     }
-    if ((int64_t)g.tm * g.tn >= pairs) return f8 ? launch_tiles<true>(a, g, vec, st) : launch_tiles<false>(a, g, vec, st);
-    // fewer tiles than pairs: token blocks as even as they come, and K over what is left of the GPU
+    // split: token blocks as even as they come, and K over what is left of the GPU.  Two CTAs an SM
+    // while the smaller ring is as deep as the narrow blocks (or a short pass over K) need
     const int tz = (a.T + 255) / 256, bn = ((a.T + tz - 1) / tz + 15) / 16 * 16;
-    if (bn <= 128) return f8 ? launch_split<true, 2>(a, bn, vec, st) : launch_split<false, 2>(a, bn, vec, st);
-    return f8 ? launch_split<true, 1>(a, bn, vec, st) : launch_split<false, 1>(a, bn, vec, st);
+    const int64_t blocks = (int64_t)((a.N + 127) / 128) * tz;
+    int ksplit = 1;
+    cudaError_t err = bn <= 128 ? cluster_size<2>(blocks, nkb, &ksplit) : cudaSuccess;
+    const bool two = bn <= 32 || (bn <= 128 && (nkb + ksplit - 1) / ksplit <= split_stages(2, bn));
+    if (err == cudaSuccess && !two) err = cluster_size<1>(blocks, nkb, &ksplit);
+    if (err != cudaSuccess) return err;
+    const int64_t at_once = (int64_t)a.sm_count * (two ? 2 : 1), rounds = (blocks * ksplit + at_once - 1) / at_once;
+    const int64_t split_ns = 3000 + 20 * bn + rounds * ((nkb + ksplit - 1) / ksplit) * (200 + bn * 8 / 10);
+    if (a.T > 64 && tiles_ns < split_ns) return f8 ? launch_tiles<true>(a, g, vec, st) : launch_tiles<false>(a, g, vec, st);
+    if (two) return f8 ? launch_split<true, 2>(a, bn, ksplit, vec, st) : launch_split<false, 2>(a, bn, ksplit, vec, st);
+    return f8 ? launch_split<true, 1>(a, bn, ksplit, vec, st) : launch_split<false, 1>(a, bn, ksplit, vec, st);
 }
 
 }  // namespace moe
