@@ -18,6 +18,11 @@ constexpr int budget_of(int ctas) { return ctas == 3 ? 73 * 1024 : (ctas == 2 ? 
 __host__ __device__ constexpr int unit_tokens(int bytes) { return bytes <= 128 ? 32 : 16; }
 constexpr int kMaxStages = 8;    // units of a warp's ring
 constexpr int kMinUnits = 4;     // units worth a CTA of its own: one a warp
+// Units that a CTA could stream in the time that starting and ending a piece takes (about 5
+// us): each segment is that much longer on the line that the CTAs share out, or those with
+// several pieces would end last (0, 6, 10, 16: 172.8, 168.8, 167.8, 168.4 us for 32 ragged
+// sequences, 24.5, 21.1, 20.7, 20.1 us for the windowed batch of 19).
+constexpr int kStart = 12;
 constexpr int64_t kMaxTokens = 1 << 30;  // of a sequence: token indexes stay in 32 bits
 constexpr float kSlack = 8.f;    // weights stay below 2^8: far from f16's range, and as precise
 constexpr float kLog2e = 1.44269504f;

@@ -5,11 +5,12 @@
 // Bound by the cache's bytes, each read once for all query heads of a key head.
 //
 // Split.  The attended tokens of a (sequence, key head, block of query heads) form a
-// segment of units of 16 tokens (32 where a row is at most 128 bytes); the segments of a call are laid end to end and every
-// CTA gets the same number of units of that line, whatever the lengths.  A CTA walks
-// its stretch as pieces of segments.  A segment inside one CTA is finished there; the
-// parts of one that spans CTAs go to a workspace, and the CTA that arrives last joins
-// them, always in the order of the line, so the result does not depend on timing.
+// segment of units of 16 tokens (32 where a row is at most 128 bytes), and a few places more
+// for the cost of starting it; the segments of a call are laid end to end and every CTA gets
+// the same number of places of that line, whatever the lengths.  A CTA walks its stretch as
+// pieces of segments.  A segment inside one CTA is finished there; the parts of one that
+// spans CTAs go to a workspace, and the CTA that arrives last joins them, always in the
+// order of the line, so the result does not depend on timing.
 //
 // A piece.  Each warp takes every fourth unit through a ring of its own (cp.async, no
 // barrier between warps) with its own running maximum and sum; the warps are joined in
@@ -140,7 +141,10 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int b) {
     const int first = a.window > 0 && n > a.window ? (int)n - a.window : 0;
     return {first, (int)n - first};
 }
-__device__ __forceinline__ int units_of(const Span& s, int unit) { return (s.count + unit - 1) / unit; }
+// Places of one of its segments on the line: kStart for what a piece costs, then its units.
+__device__ __forceinline__ int places_of(const Span& s, int unit) {
+    return s.count > 0 ? (s.count + unit - 1) / unit + kStart : 0;
+}
 
 // T: 0 bf16, 1 f16, 2 E4M3 (computed in f16).  DP: head_dim (EXACT) or a bound of it; with
 // the dimension known no step of the products is conditional, and they overlap.  NT: blocks
@@ -176,9 +180,14 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
 
     // ---- this CTA's stretch of the line: a scan over the lengths, kThreads at a time ----
     const int own = blockIdx.x < a.B ? a.lengths[blockIdx.x] : 1;  // its own share of the empty sequences, below
-    const int u0 = tid < a.B ? units_of(span_of(a, tid), U) : 0;
-    long long rest = 0;  // units behind the first kThreads sequences
-    for (int b = kThreads + tid; b < a.B; b += kThreads) rest += units_of(span_of(a, b), U);
+    // sums of places, with the number of sequences that have any above kOne
+    constexpr long long kOne = 1ll << 44;
+    const int u0 = tid < a.B ? places_of(span_of(a, tid), U) : 0;
+    long long rest = 0;  // behind the first kThreads sequences
+    for (int b = kThreads + tid; b < a.B; b += kThreads) {
+        const int u = places_of(span_of(a, b), U);
+        rest += u > 0 ? u + kOne : 0;
+    }
     auto scan = [&](long long x) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -187,22 +196,25 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
         }
         return x;
     };
-    const long long x0 = scan(u0);
+    const long long x0 = scan(u0 > 0 ? u0 + kOne : 0);
     if (a.B > kThreads) rest = scan(rest);
     if (lane == 31) {
         s_sum[warp] = x0;
         s_rest[warp] = rest;
     }
     __syncthreads();
-    long long ahead = 0, chunk = 0, total = 0;  // units ahead of this warp, of the first kThreads sequences, of all
+    long long ahead = 0, chunk = 0, total = 0;  // places ahead of this warp, of the first kThreads sequences, of all
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) ahead += s_sum[w];
         chunk += s_sum[w];
         total += s_rest[w];
     }
-    total = (total + chunk) * per_b;
-    long long ctas = (total + kMinUnits - 1) / kMinUnits;
+    total += chunk;
+    const long long units = ((total & (kOne - 1)) - (total >> 44) * kStart) * per_b;
+    total = (total & (kOne - 1)) * per_b;
+    chunk &= kOne - 1;
+    long long ctas = (units + kMinUnits - 1) / kMinUnits;
     if (ctas > gridDim.x) ctas = gridDim.x;
     long long u_begin = 0, u_end = 0;
     if ((long long)blockIdx.x < ctas) {
@@ -213,14 +225,14 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
             u_begin = total * blockIdx.x / ctas;
             u_end = total * (blockIdx.x + 1) / ctas;
         }
-        // the sequence that holds unit u_begin
-        const long long lo = (ahead + x0 - u0) * per_b;
+        // the sequence that holds place u_begin
+        const long long lo = (((ahead + x0) & (kOne - 1)) - u0) * per_b;
         if (u0 > 0 && u_begin >= lo && u_begin < lo + (long long)u0 * per_b) {
             s_b = tid;
             s_before = lo;
         }
         for (int b0 = kThreads; chunk * per_b <= u_begin; b0 += kThreads) {
-            const int b = b0 + tid, u = b < a.B ? units_of(span_of(a, b), U) : 0;
+            const int b = b0 + tid, u = b < a.B ? places_of(span_of(a, b), U) : 0;
             const long long x = scan(u);
             __syncthreads();
             if (lane == 31) s_sum[warp] = x;
@@ -253,21 +265,23 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
     if ((long long)blockIdx.x >= ctas) return;
     __syncthreads();
     int b = s_b;
-    long long before = s_before;  // units ahead of sequence b
+    long long before = s_before;  // places ahead of sequence b
     Span span = span_of(a, b);
-    int ub = units_of(span, U);
+    int ub = places_of(span, U);
 
     for (long long u = u_begin; u < u_end;) {
         while (u >= before + (long long)ub * per_b) {  // next sequence with a token
             before += (long long)ub * per_b;
             ++b;
             span = span_of(a, b);
-            ub = units_of(span, U);
+            ub = places_of(span, U);
         }
         const int seg = (int)((u - before) / ub);
         const long long seg_begin = before + (long long)seg * ub;
-        const int first_u = (int)(u - seg_begin);
-        const int last_u = (int)((u_end < seg_begin + ub ? u_end : seg_begin + ub) - seg_begin);
+        const int last_place = (int)((u_end < seg_begin + ub ? u_end : seg_begin + ub) - seg_begin);
+        const int first_u = max(0, (int)(u - seg_begin) - kStart), last_u = max(0, last_place - kStart);
+        u = seg_begin + last_place;
+        if (last_u == first_u) continue;  // nothing but the start of a segment
         const int kh = seg / p.chunks, h0 = kh * group + seg % p.chunks * p.chunk;
         const int nh = min(p.chunk, kh * group + group - h0);  // query heads of this segment
 
@@ -582,12 +596,12 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                 }
             }
         __syncthreads();
-        const bool whole = first_u == 0 && last_u == ub;
+        const bool whole = first_u == 0 && last_u == ub - kStart;
         float* slot_base = nullptr;
         int i0 = 0, i1 = 0;
         if (!whole) {
             // CTAs that hold the segment's first and last unit
-            i0 = (int)(((seg_begin + 1) * ctas - 1) / total);
+            i0 = (int)(((seg_begin + kStart + 1) * ctas - 1) / total);
             i1 = (int)(((seg_begin + ub) * ctas - 1) / total);
             const int slot = 2 * blockIdx.x + ((int)blockIdx.x == i0 ? 1 : 0);
             slot_base = static_cast<float*>(a.workspace) + p.slots + (int64_t)slot * HC * (D + 2);
@@ -730,7 +744,6 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
             }
         }
         __syncthreads();  // shared memory is free for the next piece
-        u = seg_begin + last_u;
     }
 }
 
