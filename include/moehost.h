@@ -466,7 +466,9 @@ int moe_kv_attend(moe_kv* kv, const void* q, int q_type, int64_t q_ts, int64_t q
                   int64_t table_stride, int max_pages, const int32_t* lengths, int B, float scale, int window,
                   void* out, int64_t out_ts, int64_t out_hs, float* lse, void* stream);
 
-/* Reads (synchronous; 0 = no error so far) and clears the handle's status word. */
+/* Reads (0 = no error so far) and clears the handle's status word.  Both return when done;
+ * neither waits for work of streams that do not synchronise with the legacy default
+ * stream: synchronise those first. */
 int moe_kv_get_status(moe_kv* kv, int* status);
 int moe_kv_clear_status(moe_kv* kv);
 

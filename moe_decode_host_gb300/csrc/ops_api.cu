@@ -12,8 +12,8 @@ struct moe_kv {
     KvView view;
     int max_batch;
     int sm_count;
+    void* workspace = nullptr;  // one allocation: moe_kv_attend's workspace, then the status word
     int* d_status = nullptr;
-    void* workspace = nullptr;
 };
 
 namespace {
@@ -93,16 +93,16 @@ int moe_kv_create(const moe_kv_params* pp, void* k_cache, void* v_cache, const f
         delete kv;
         return MOE_ERR_CUDA;
     }
-    const size_t ws = attend_workspace(kv->view, kv->sm_count);
-    cudaError_t err = cudaMalloc(&kv->d_status, sizeof(int));
-    err = err ? err : cudaMemset(kv->d_status, 0, sizeof(int));
-    err = err ? err : cudaMalloc(&kv->workspace, ws);
-    err = err ? err : cudaMemset(kv->workspace, 0, ws);
+    const size_t ws = (attend_workspace(kv->view, kv->sm_count) + 15) / 16 * 16;
+    cudaError_t err = cudaMalloc(&kv->workspace, ws + sizeof(int));
+    err = err ? err : cudaMemset(kv->workspace, 0, ws + sizeof(int));
+    err = err ? err : cudaStreamSynchronize(nullptr);  // done before a call on any stream
     if (err != cudaSuccess) {
         cudaGetLastError();
         moe_kv_destroy(kv);
         return err == cudaErrorMemoryAllocation ? MOE_ERR_NOMEM : MOE_ERR_CUDA;
     }
+    kv->d_status = reinterpret_cast<int*>(static_cast<uint8_t*>(kv->workspace) + ws);
     kv->view.status = kv->d_status;
     *out = kv;
     return MOE_OK;
@@ -110,7 +110,6 @@ int moe_kv_create(const moe_kv_params* pp, void* k_cache, void* v_cache, const f
 
 int moe_kv_destroy(moe_kv* kv) {
     if (!kv) return MOE_ERR_INVALID_ARG;
-    cudaFree(kv->d_status);
     cudaFree(kv->workspace);
     delete kv;
     return MOE_OK;
@@ -157,7 +156,8 @@ int moe_kv_get_status(moe_kv* kv, int* status) {
 
 int moe_kv_clear_status(moe_kv* kv) {
     if (!kv) return MOE_ERR_INVALID_ARG;
-    return cuda_status(cudaMemset(kv->d_status, 0, sizeof(int)));
+    cudaError_t err = cudaMemset(kv->d_status, 0, sizeof(int));
+    return cuda_status(err ? err : cudaStreamSynchronize(nullptr));
 }
 
 int moe_linear(const void* x, int64_t x_stride, const void* w, int64_t w_stride, int in_type, int T, int N, int K,
