@@ -37,7 +37,9 @@ __device__ __forceinline__ void cp_wait(int left) {  // until at most `left` gro
 // through the reduction and the stores.  The usual types are template arguments: with the
 // types at run time the conversions made the kernel issue bound (52 instructions an
 // element and 77 us for 8192 x 4096 to E4M3).
-template <int VEC, int NV, int THREADS, int XT, int RT, int WT, int YT>
+// FULL: residual, sum and weights are all there and the runs of a CTA's threads are the row,
+// so that nothing in the loop is conditional.
+template <int VEC, int NV, int THREADS, int XT, int RT, int WT, int YT, bool FULL>
 __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a, int stages) {
     constexpr bool kRing = VEC == 8 && THREADS <= 256;
     constexpr bool kAhead = !kRing && THREADS * NV * VEC <= 8192;  // registers for the next row
@@ -53,27 +55,33 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a, int sta
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int e0 = threadIdx.x * VEC, de = blockDim.x * VEC;
+    const bool has_res = FULL || a.res, has_sum = FULL || a.sum, has_w = FULL || a.w;
+    auto in = [&](int n) { return FULL || e0 + n * de < a.H; };  // run n is in the row
     const int all = blockDim.x * blockDim.y, me = threadIdx.y * blockDim.x + threadIdx.x;
     Raw<VEC, XW> rx[NV];
     Raw<VEC, RW> rr[NV];
     // a thread reads back only what it copied itself: no barrier but its own wait
-    auto copy = [&](int64_t r, int stage) {
+    const uint8_t* gx = static_cast<const uint8_t*>(a.x) + (row * a.x_stride + e0) * type_bytes(xt);
+    const uint8_t* gr = static_cast<const uint8_t*>(a.res) + (row * a.res_stride + e0) * type_bytes(rt);
+    const int64_t gx_step = step * a.x_stride * type_bytes(xt), gr_step = step * a.res_stride * type_bytes(rt);
+    auto copy = [&](int64_t r, int stage) {  // the next row, r, that gx and gr stand at
         if (r < a.T) {
 #pragma unroll
             for (int n = 0; n < NV; ++n)
-                if (e0 + n * de < a.H) {
+                if (in(n)) {
                     uint4* d = ring + (stage * NV + n) * kPlanes * all + me;
-                    const uint8_t* gx = static_cast<const uint8_t*>(a.x) + (r * a.x_stride + e0 + n * de) * type_bytes(xt);
-                    cp_async16(d, gx);
-                    if (XW && xt == MOE_F32) cp_async16(d + all, gx + 16);
-                    if (a.res) {
-                        const uint8_t* gr =
-                            static_cast<const uint8_t*>(a.res) + (r * a.res_stride + e0 + n * de) * type_bytes(rt);
-                        cp_async16(d + (XW ? 2 : 1) * all, gr);
-                        if (RW && rt == MOE_F32) cp_async16(d + (XW ? 3 : 2) * all, gr + 16);
+                    const uint8_t* px = gx + n * de * type_bytes(xt);
+                    cp_async16(d, px);
+                    if (XW && xt == MOE_F32) cp_async16(d + all, px + 16);
+                    if (has_res) {
+                        const uint8_t* pr = gr + n * de * type_bytes(rt);
+                        cp_async16(d + (XW ? 2 : 1) * all, pr);
+                        if (RW && rt == MOE_F32) cp_async16(d + (XW ? 3 : 2) * all, pr + 16);
                     }
                 }
         }
+        gx += gx_step;
+        gr += gr_step;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     auto take = [&](int stage) {
@@ -82,7 +90,7 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a, int sta
             const uint4* d = ring + (stage * NV + n) * kPlanes * all + me;
             if constexpr (VEC == 8) {
                 rx[n].set(d, all);
-                if (a.res) rr[n].set(d + (XW ? 2 : 1) * all, all);
+                if (has_res) rr[n].set(d + (XW ? 2 : 1) * all, all);
             }
         }
     };
@@ -90,19 +98,23 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a, int sta
         if (r >= a.T) return;
 #pragma unroll
         for (int n = 0; n < NV; ++n)
-            if (e0 + n * de < a.H) {
+            if (in(n)) {
                 rx[n].load(a.x, r * a.x_stride + e0 + n * de, xt);
-                if (a.res) rr[n].load(a.res, r * a.res_stride + e0 + n * de, rt);
+                if (has_res) rr[n].load(a.res, r * a.res_stride + e0 + n * de, rt);
             }
     };
     if (kAhead) fetch(row);
     if (kRing)
         for (int i = 0; i < stages - 1; ++i) copy(row + i * step, i);
     int slot = 0;
+    uint8_t* ps = static_cast<uint8_t*>(a.sum) + (row * a.sum_stride + e0) * type_bytes(rt);
+    uint8_t* py = static_cast<uint8_t*>(a.y) + (row * a.y_stride + e0) * type_bytes(yt);
+    const int64_t ps_step = step * a.sum_stride * type_bytes(rt), py_step = step * a.y_stride * type_bytes(yt);
     // every thread of the CTA makes the same number of rounds (their barriers)
     int flip = 0;
-    for (int64_t first = (int64_t)blockIdx.x * blockDim.y; first < a.T; first += step, row += step, flip ^= 1) {
-        const bool live = row < a.T;
+    for (int64_t first = (int64_t)blockIdx.x * blockDim.y; first < a.T;
+         first += step, row += step, ps += ps_step, py += py_step, flip ^= 1) {
+        const bool live = FULL || row < a.T;
         Raw<VEC, WT == kAny || WT == MOE_F32> rw[NV];
         if (kRing) {
             const int next = slot == 0 ? stages - 1 : slot - 1;  // the slot of the row before
@@ -115,16 +127,16 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a, int sta
         }
 #pragma unroll
         for (int n = 0; n < NV; ++n)
-            if (a.w && e0 + n * de < a.H) rw[n].load(a.w, e0 + n * de, wt);
+            if (has_w && in(n)) rw[n].load(a.w, e0 + n * de, wt);
         float s[NV][VEC];
         float ss = 0.f, top = 0.f;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) s[n][i] = 0.f;
-            if (live && e0 + n * de < a.H) {
+            if (live && in(n)) {
                 rx[n].get(xt, s[n]);
-                if (a.res) {
+                if (has_res) {
                     float r[VEC];
                     rr[n].get(rt, r);
 #pragma unroll
@@ -135,11 +147,11 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a, int sta
         if (kAhead) fetch(row + step);
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            if (e0 + n * de < a.H) {
-                if (a.sum && live) store_run<VEC>(a.sum, row * a.sum_stride + e0 + n * de, rt, s[n]);
+            if (in(n)) {
+                if (has_sum && live) store_run<VEC>(ps, n * de, rt, s[n]);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) ss = fmaf(s[n][i], s[n][i], ss);
-                if (a.w) {
+                if (has_w) {
                     float w[VEC];
                     rw[n].get(wt, w);
 #pragma unroll
@@ -160,11 +172,16 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a, int sta
             // two sets of partials: the next round's writes meet no reader of this round's
             if ((threadIdx.x & 31) == 0) part[flip][w0 + (threadIdx.x >> 5)] = make_float2(ss, top);
             __syncthreads();
-            ss = top = 0.f;
-            for (int i = 0; i < warps; ++i) {  // in the same order for every thread: one result a row
-                const float2 v = part[flip][w0 + i];
-                ss += v.x;
-                top = fmaxf(top, v.y);
+            // lane i takes partial i, the rest add nothing: the same tree in every warp, one result a row
+            constexpr int kMost = THREADS / 32 > 16 ? 32 : (THREADS / 32 > 8 ? 16 : 8);
+            const int lane = threadIdx.x & (kMost - 1);
+            const float2 v = lane < warps ? part[flip][w0 + lane] : make_float2(0.f, 0.f);
+            ss = v.x;
+            top = v.y;
+#pragma unroll
+            for (int o = kMost / 2; o > 0; o >>= 1) {
+                ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                if (yt == MOE_E4M3) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             }
         }
         if (!live) continue;
@@ -190,16 +207,20 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a, int sta
             for (int i = 0; i < VEC; ++i) s[n][i] *= f;
 #pragma unroll
         for (int n = 0; n < NV; ++n)
-            if (e0 + n * de < a.H) store_run<VEC>(a.y, row * a.y_stride + e0 + n * de, yt, s[n]);
+            if (in(n)) store_run<VEC>(py, n * de, yt, s[n]);
     }
 }
 
-template <int VEC, int NV, int THREADS, int XT, int RT, int WT, int YT>
+template <int VEC, int NV, int THREADS, int XT, int RT, int WT, int YT, bool FULL = false>
 cudaError_t launch(const NormArgs& a, cudaStream_t st) {
     const int runs = (a.H + VEC - 1) / VEC;
     const int tx = ((runs + NV - 1) / NV + 31) / 32 * 32;
     const int ty = tx >= 128 ? 1 : 128 / tx;
-    const auto kernel = norm_kernel<VEC, NV, THREADS, XT, RT, WT, YT>;
+    if constexpr (!FULL && VEC == 8 && THREADS <= 256 && XT != kAny) {
+        if (a.res && a.sum && a.w && ty == 1 && tx * NV * VEC == a.H)
+            return launch<VEC, NV, THREADS, XT, RT, WT, YT, true>(a, st);
+    }
+    const auto kernel = norm_kernel<VEC, NV, THREADS, XT, RT, WT, YT, FULL>;
     // one round of CTAs: a CTA that had to wait for another to end would walk its rows alone
     static std::atomic<int> resident[THREADS / 32 + 1];  // CTAs an SM holds, by warps
     const int warps = tx * ty / 32;
