@@ -3,6 +3,8 @@
 Translation units compile in parallel into moe_decode_host_gb300/_build/, then
 link into moe_decode_host_gb300/libmoehost.so with the CUDA runtime linked
 statically.  Only nvcc and a host C++ compiler are needed (no torch, no cmake).
+csrc/binding.cc becomes the Python extension _decoder_ops.so (Python's headers, no
+link to the library: it is given the addresses it calls).
 """
 from __future__ import annotations
 
@@ -11,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoehost.so")
+BINDING = os.path.join(PKG, "_decoder_ops.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"),
          "-I", CSRC]
@@ -54,6 +58,14 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
             cmd = [nvcc] + ARCH + FLAGS + (["-Xptxas", "-v"] if ptxas_info else []) + ["-c", src, "-o", obj]
             jobs.append(cmd)
 
+    binding_src = os.path.join(CSRC, "binding.cc")
+    if _stale(BINDING, [binding_src, os.path.join(ROOT, "include", "moehost.h")]):
+        cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+        if not cxx:
+            raise RuntimeError("a host C++ compiler is required to build _decoder_ops.so")
+        jobs.append([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", sysconfig.get_paths()["include"], "-I",
+                     os.path.join(ROOT, "include"), binding_src, "-o", BINDING])
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -64,7 +76,7 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
                 if verbose or ptxas_info or r.returncode != 0:
                     sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
                 if r.returncode != 0:
-                    raise RuntimeError(f"nvcc failed on {cmd[-3]}")
+                    raise RuntimeError(f"the compiler failed on {cmd[-3]}")
     if jobs or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "-o", tmp] + objs
