@@ -309,19 +309,16 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                 const uint32_t mask = __ballot_sync(0xffffffffu, ok);
                 if (lane == 0) s_mask[warp][slot] = mask;
                 const uint32_t dst = ring_u + slot * unit_bytes;
-                if (EXACT && mask == kAll && 32 % CPR == 0) {
-                    // lanes cover 32 / CPR whole rows at a time
-                    constexpr int ROWS = 32 / CPR > 0 ? 32 / CPR : 1;
-                    const int col = lane % CPR * 16, row = lane / CPR;
-                    const uint8_t *kc = kb + col, *vc = vb + col;
+                if (EXACT && mask == kAll) {
+                    static_assert(!EXACT || U * CPR % 32 == 0, "whole rounds of the warp");
                     const uint64_t unit = 1ull << p.shift;
 #pragma unroll
-                    for (int i = 0; i < U / ROWS; ++i) {
-                        const int r = i * ROWS + row;
-                        const uint64_t o = __shfl_sync(0xffffffffu, off, r) * unit;
+                    for (int i0 = 0; i0 < U * CPR; i0 += 32) {
+                        const int r = (i0 + lane) / CPR, col = (i0 + lane) % CPR * 16;
+                        const uint64_t o = __shfl_sync(0xffffffffu, off, r) * unit + col;
                         const uint32_t at = dst + r * pitch + (col ^ (swap_of<F8>(r) & swizzle) << 4);
-                        cp_async16(at, kc + o);
-                        cp_async16(at + U * pitch, vc + o);
+                        cp_async16(at, kb + o);
+                        cp_async16(at + U * pitch, vb + o);
                     }
                 } else {
                     for (int i0 = 0; i0 < U * cpr; i0 += 32) {

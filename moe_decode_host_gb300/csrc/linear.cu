@@ -66,6 +66,12 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ float ld_cluster1(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 // A wait taken by a whole converged warp; false when it ran out.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, unsigned parity, Head& hd, int* status, int where, int slot) {
     return __all_sync(0xffffffffu,
@@ -185,27 +191,40 @@ __device__ __forceinline__ void activate(float (&v)[VEC], int act) {
     }
 }
 
-// Scales and biases of VEC outputs from n on (1 and 0 where there are none).
+// Scales and biases of VEC outputs from n on, `inc` apart (1 and 0 where there are none).
 template <int VEC>
 struct Columns {
     float scale[VEC], bias[VEC];
-    __device__ __forceinline__ void load(const LinearArgs& a, int n) {
+    __device__ __forceinline__ void load(const LinearArgs& a, int n, int inc) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            scale[i] = a.w_scale && n + i < a.N ? a.w_scale[n + i] : 1.f;
+            const int m = n + i * inc;
+            scale[i] = a.w_scale && m < a.N ? a.w_scale[m] : 1.f;
             bias[i] = 0.f;
-            if (a.bias && n + i < a.N)
-                bias[i] = a.bias_type == MOE_F32
-                              ? static_cast<const float*>(a.bias)[n + i]
-                              : half_bits_to_f32(static_cast<const uint16_t*>(a.bias)[n + i], a.bias_type);
+            if (a.bias && m < a.N)
+                bias[i] = a.bias_type == MOE_F32 ? static_cast<const float*>(a.bias)[m]
+                                                 : half_bits_to_f32(static_cast<const uint16_t*>(a.bias)[m], a.bias_type);
         }
     }
 };
 
-// The epilogue of VEC outputs of token t from n on; `whole`: all in range and aligned.
-// res holds the residual's bits when whole, loaded ahead.
+__device__ __forceinline__ void finish_one(const LinearArgs& a, int64_t t, int n, float v) {
+    if (a.res) {
+        Raw<1> r;
+        float f[1];
+        r.load(a.res, t * a.res_stride + n, a.y_type);
+        r.get(a.y_type, f);
+        v += f[0];
+    }
+    const float one[1] = {v};
+    store_run<1>(a.y, t * a.y_stride + n, a.y_type, one);
+}
+
+// The epilogue of VEC outputs of token t from n on, inc apart.  whole: one aligned run in
+// range, with the residual's bits in res; else element by element (with inc = 32 the lanes
+// of a warp still write and read whole lines).
 template <int VEC>
-__device__ __forceinline__ void finish(const LinearArgs& a, int64_t t, int n, float sx, const Columns<VEC>& col,
+__device__ __forceinline__ void finish(const LinearArgs& a, int64_t t, int n, int inc, float sx, const Columns<VEC>& col,
                                        const Raw<VEC>& res, float (&v)[VEC], bool whole) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) v[i] = fmaf(v[i], sx * col.scale[i], col.bias[i]);
@@ -220,19 +239,8 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int64_t t, int n, fl
         store_run<VEC>(a.y, t * a.y_stride + n, a.y_type, v);
     } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            if (n + i < a.N) {
-                float one[1] = {v[i]};
-                if (a.res) {
-                    Raw<1> r;
-                    float f[1];
-                    r.load(a.res, t * a.res_stride + n + i, a.y_type);
-                    r.get(a.y_type, f);
-                    one[0] += f[0];
-                }
-                store_run<1>(a.y, t * a.y_stride + n + i, a.y_type, one);
-            }
-        }
+        for (int i = 0; i < VEC; ++i)
+            if (n + i * inc < a.N) finish_one(a, t, n + i * inc, v[i]);
     }
 }
 
@@ -277,17 +285,17 @@ __global__ void __launch_bounds__(kThreads, CTAS)
     grid_launch_next();
     grid_dep_wait();
     // ---- this rank's tokens are [c0, c1); each epilogue warp finishes every eighth, four
-    // outputs a lane, and has their scales, biases and first residuals in hand before the
-    // sums are ----
+    // outputs a lane (a run where rows are aligned, else 32 apart), and has their scales,
+    // biases and first residuals in hand before the sums are ----
     const int cols = min(bn, a.T - t0);
     const int c0 = cols * rank / S, c1 = cols * (rank + 1) / S;
-    const int mine = n0 + lane * 4;
+    const int inc = vec ? 1 : 32, mine = n0 + (vec ? lane * 4 : lane);
     const bool whole = vec && mine + 4 <= a.N;
     Columns<4> col;
     Raw<4> res[CTAS == 1 ? 2 : 1];
     float sx[2] = {1.f, 1.f};
     if (warp >= 2) {
-        col.load(a, mine);
+        col.load(a, mine, inc);
 #pragma unroll
         for (int k = 0; k < (CTAS == 1 ? 2 : 1); ++k) {
             const int c = c0 + warp - 2 + kEpiWarps * k;
@@ -356,8 +364,16 @@ __global__ void __launch_bounds__(kThreads, CTAS)
             for (int j = 0; j < kSplitMax; ++j)
                 if (j < S) {
 #pragma unroll
-                    for (int h = 0; h < kAhead; ++h)  // a second token past the end rereads the first
-                        p[h][j] = ld_cluster(map_rank(smem_u32(dump + (c + (c + kEpiWarps * h < c1 ? kEpiWarps * h : 0)) * 128 + lane * 4), j));
+                    for (int h = 0; h < kAhead; ++h) {  // a second token past the end rereads the first
+                        const int ch = c + (c + kEpiWarps * h < c1 ? kEpiWarps * h : 0);
+                        const uint32_t at = map_rank(smem_u32(dump + ch * 128 + (vec ? lane * 4 : lane)), j);
+                        if (vec) {
+                            p[h][j] = ld_cluster(at);
+                        } else {
+                            p[h][j] = make_float4(ld_cluster1(at), ld_cluster1(at + 128), ld_cluster1(at + 256),
+                                                  ld_cluster1(at + 384));
+                        }
+                    }
                 }
             if (k > 0 && mine < a.N) {
 #pragma unroll
@@ -381,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, CTAS)
                         v[3] += p[h][j].w;
                     }
                 if (mine < a.N && c + kEpiWarps * h < c1)
-                    finish<4>(a, t0 + c + kEpiWarps * h, mine, sx[h], col, res[h], v, whole);
+                    finish<4>(a, t0 + c + kEpiWarps * h, mine, inc, sx[h], col, res[h], v, whole);
             }
         }
     }
@@ -533,47 +549,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int cols = min(g.bn, a.N - n0);
             // two warps share a quarter of the lanes and take every other 32 outputs
             for (int c = (warp - 2) / 4 * 32; c < cols; c += 64) {
-                // on the way out a lane takes 8 outputs of every eighth token; their scales, biases and
-                // residuals are fetched while the sums go through shared memory
-                const int nn = n0 + c + (lane & 3) * 8;
-                const bool in = nn < n0 + cols, whole = vec && nn + 8 <= a.N;
-                Columns<8> col;
-                Raw<8> res[4];
-                float sx[4];
-                if (in) {
-                    col.load(a, nn);
+                // in: a lane holds a token.  16-byte piece j of its row goes to piece j ^ (row % 8): no side
+                // of the exchange meets a bank twice within 8 lanes
+                auto exchange = [&]() {
+                    float v0[16], v1[16];
+                    const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + buf * 256 + c;
+                    tc_ld16x2(at, at + 16, v0, v1);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int t = t0 + (lane >> 2) + 8 * k;
-                        sx[k] = 1.f;
-                        if (t < a.T) {
-                            if (a.res && whole) res[k].load(a.res, (int64_t)t * a.res_stride + nn, a.y_type);
-                            if (a.x_scale) sx[k] = a.x_scale[t];
+                    for (int j = 0; j < 4; ++j) {
+                        *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                            make_float4(v0[4 * j], v0[4 * j + 1], v0[4 * j + 2], v0[4 * j + 3]);
+                        *reinterpret_cast<float4*>(stage + lane * 128 + (((j + 4) ^ (lane & 7)) << 4)) =
+                            make_float4(v1[4 * j], v1[4 * j + 1], v1[4 * j + 2], v1[4 * j + 3]);
+                    }
+                    __syncwarp();
+                };
+                if (vec) {
+                    // out: a lane takes 8 outputs of every eighth token; their scales, biases and residuals
+                    // are fetched while the sums go through shared memory
+                    const int nn = n0 + c + (lane & 3) * 8;
+                    const bool in = nn < n0 + cols, whole = nn + 8 <= a.N;
+                    Columns<8> col;
+                    Raw<8> res[4];
+                    float sx[4];
+                    if (in) {
+                        col.load(a, nn, 1);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int t = t0 + (lane >> 2) + 8 * k;
+                            sx[k] = 1.f;
+                            if (t < a.T) {
+                                if (a.res && whole) res[k].load(a.res, (int64_t)t * a.res_stride + nn, a.y_type);
+                                if (a.x_scale) sx[k] = a.x_scale[t];
+                            }
                         }
                     }
-                }
-                // in: a lane holds a token.  16-byte piece j of its row goes to piece j ^ (row % 8): neither
-                // side of the exchange meets a bank twice within 8 lanes
-                float v0[16], v1[16];
-                const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + buf * 256 + c;
-                tc_ld16x2(at, at + 16, v0, v1);
+                    exchange();
+                    if (in) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                        make_float4(v0[4 * j], v0[4 * j + 1], v0[4 * j + 2], v0[4 * j + 3]);
-                    *reinterpret_cast<float4*>(stage + lane * 128 + (((j + 4) ^ (lane & 7)) << 4)) =
-                        make_float4(v1[4 * j], v1[4 * j + 1], v1[4 * j + 2], v1[4 * j + 3]);
-                }
-                __syncwarp();
-                if (in) {
+                        for (int k = 0; k < 4; ++k) {
+                            const int r = (lane >> 2) + 8 * k;
+                            const uint8_t* row = stage + r * 128;
+                            const float4 lo = *reinterpret_cast<const float4*>(row + (((2 * (lane & 3)) ^ (r & 7)) << 4));
+                            const float4 hi = *reinterpret_cast<const float4*>(row + (((2 * (lane & 3) + 1) ^ (r & 7)) << 4));
+                            float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                            if (t0 + r < a.T) finish<8>(a, t0 + r, nn, 1, sx[k], col, res[k], v, whole);
+                        }
+                    }
+                } else {
+                    // rows of any alignment: a lane takes one output of every token, so that a warp's
+                    // stores and residuals are consecutive (8087 outputs of 6116 x 1424, fp32 with
+                    // residual: 541 us with 8 outputs a lane, element by element)
+                    const int nn = n0 + c + lane;
+                    const bool in = nn < n0 + cols;
+                    Columns<1> col;
+                    Raw<1> res[32];
+                    if (in) {
+                        col.load(a, nn, 1);
+                        if (a.res) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int r = (lane >> 2) + 8 * k;
-                        const uint8_t* row = stage + r * 128;
-                        const float4 lo = *reinterpret_cast<const float4*>(row + (((2 * (lane & 3)) ^ (r & 7)) << 4));
-                        const float4 hi = *reinterpret_cast<const float4*>(row + (((2 * (lane & 3) + 1) ^ (r & 7)) << 4));
-                        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                        if (t0 + r < a.T) finish<8>(a, t0 + r, nn, sx[k], col, res[k], v, whole);
+                            for (int r = 0; r < 32; ++r)
+                                if (t0 + r < a.T) res[r].load(a.res, (int64_t)(t0 + r) * a.res_stride + nn, a.y_type);
+                        }
+                    }
+                    exchange();
+                    if (in) {
+#pragma unroll
+                        for (int r0 = 0; r0 < 32; r0 += 8) {
+                            float v[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float sum = *reinterpret_cast<const float*>(stage + (r0 + i) * 128 +
+                                                                                  (((lane >> 2) ^ i) << 4) + (lane & 3) * 4);
+                                const float sx = a.x_scale && t0 + r0 + i < a.T ? a.x_scale[t0 + r0 + i] : 1.f;
+                                v[i] = fmaf(sum, sx * col.scale[0], col.bias[0]);
+                            }
+                            activate<8>(v, a.act);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                if (t0 + r0 + i < a.T) {
+                                    float one[1] = {0.f};
+                                    if (a.res) res[r0 + i].get(a.y_type, one);
+                                    one[0] += v[i];
+                                    store_run<1>(a.y, (int64_t)(t0 + r0 + i) * a.y_stride + nn, a.y_type, one);
+                                }
+                            }
+                        }
                     }
                 }
                 __syncwarp();
@@ -707,6 +768,7 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
     const bool f8 = a.in_type == MOE_E4M3;
     const bool vec = runs_aligned(a.y, a.y_type, 8, a.y_stride) && (!a.res || runs_aligned(a.res, a.y_type, 8, a.res_stride));
+    const bool vec4 = runs_aligned(a.y, a.y_type, 4, a.y_stride) && (!a.res || runs_aligned(a.res, a.y_type, 4, a.res_stride));
     const int nkb = (int)(((int64_t)a.K * type_bytes(a.in_type) + kRowBytes - 1) / kRowBytes);
     const int pairs = a.sm_count / 2;
     TileGrid g{(a.T + 255) / 256, 0, 0, 0};
@@ -733,8 +795,8 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st) {
     const int64_t at_once = (int64_t)a.sm_count * (two ? 2 : 1), rounds = (blocks * ksplit + at_once - 1) / at_once;
     const int64_t split_ns = 3000 + 20 * bn + rounds * ((nkb + ksplit - 1) / ksplit) * (200 + bn * 8 / 10);
     if (a.T > 64 && tiles_ns < split_ns) return f8 ? launch_tiles<true>(a, g, vec, st) : launch_tiles<false>(a, g, vec, st);
-    if (two) return f8 ? launch_split<true, 2>(a, bn, ksplit, vec, st) : launch_split<false, 2>(a, bn, ksplit, vec, st);
-    return f8 ? launch_split<true, 1>(a, bn, ksplit, vec, st) : launch_split<false, 1>(a, bn, ksplit, vec, st);
+    if (two) return f8 ? launch_split<true, 2>(a, bn, ksplit, vec4, st) : launch_split<false, 2>(a, bn, ksplit, vec4, st);
+    return f8 ? launch_split<true, 1>(a, bn, ksplit, vec4, st) : launch_split<false, 1>(a, bn, ksplit, vec4, st);
 }
 
 }  // namespace moe
