@@ -14,6 +14,11 @@
 //                 tokens x up to 256 outputs (cta_group::2: each CTA stages half of both
 //                 operands), persistent, with two accumulators so that the epilogue of a
 //                 tile runs under the next tile's products.
+//
+// Measured on a GB300 (launches of a graph): 1 x 4096 x 4096 bf16 with residual 7.3 us (4.6
+// TB/s of weights, launch and fill included), 32 x 6144 x 4096 E4M3 6.5 us, 8192 x 6144 x
+// 4096 bf16 with bias, GELU and residual 230 us (1790 TFLOP/s; 265 us back to back under the
+// power cap), without an epilogue 218 us (cuBLAS 209).
 #include <algorithm>
 
 #include "ptx.cuh"
