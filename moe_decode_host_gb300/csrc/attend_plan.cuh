@@ -23,6 +23,11 @@ constexpr int kMinUnits = 4;     // units worth a CTA of its own: one a warp
 // several pieces would end last (0, 6, 10, 16: 172.8, 168.8, 167.8, 168.4 us for 32 ragged
 // sequences, 24.5, 21.1, 20.7, 20.1 us for the windowed batch of 19).
 constexpr int kStart = 12;
+// Units of a segment that a CTA takes whole, where there is a CTA for each segment: 16 units are
+// done in less time than parts are joined, 24 are not (whole against split, D 128: one sequence of
+// 1 token 4.2 and 10.5 us, of 256 6.4 and 7.6, of 384 7.9 and 7.7; 8 of 100 to 300 7.7 and 8.8, of
+// 10 to 380 9.3 and 8.8).
+constexpr int kWhole = 20;
 constexpr int64_t kMaxTokens = 1 << 30;  // of a sequence: token indexes stay in 32 bits
 constexpr float kSlack = 8.f;    // weights stay below 2^8: far from f16's range, and as precise
 constexpr float kLog2e = 1.44269504f;

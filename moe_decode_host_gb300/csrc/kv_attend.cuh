@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
     __shared__ float s_m[kWarps][HC], s_l[kWarps][HC], s_scale[HC], s_inv[HC];
     __shared__ uint32_t s_mask[kWarps][kMaxStages];
     __shared__ long long s_sum[kWarps], s_rest[kWarps], s_before;
-    __shared__ int s_b, s_last;
+    __shared__ int s_b, s_last, s_longest[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
     constexpr int CPR = DP * ES / 16;
@@ -203,9 +203,11 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
     };
     const long long x0 = scan(u0 > 0 ? u0 + kOne : 0);
     if (a.B > kThreads) rest = scan(rest);
+    const int longest = __reduce_max_sync(0xffffffffu, u0);
     if (lane == 31) {
         s_sum[warp] = x0;
         s_rest[warp] = rest;
+        s_longest[warp] = longest;
     }
     __syncthreads();
     long long ahead = 0, chunk = 0, total = 0;  // places ahead of this warp, of the first kThreads sequences, of all
@@ -216,11 +218,17 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
         total += s_rest[w];
     }
     total += chunk;
+    // short segments, no more than CTAs: a CTA each, which costs less than joining parts.  They all
+    // get the places of the longest such segment
+    bool level = a.B <= kThreads && (total >> 44) * per_b <= gridDim.x;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) level = level && s_longest[w] <= kWhole + kStart;
     const long long units = ((total & (kOne - 1)) - (total >> 44) * kStart) * per_b;
-    total = (total & (kOne - 1)) * per_b;
-    chunk &= kOne - 1;
     long long ctas = (units + kMinUnits - 1) / kMinUnits;
     if (ctas > gridDim.x) ctas = gridDim.x;
+    if (level) ctas = (total >> 44) * per_b;
+    total = level ? ctas * (kWhole + kStart) : (total & (kOne - 1)) * per_b;
+    chunk &= kOne - 1;
     long long u_begin = 0, u_end = 0;
     if ((long long)blockIdx.x < ctas) {
         if (total < 1 << 21) {  // in 32 bits: a grid is below 2^11
@@ -231,12 +239,13 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
             u_end = total * (blockIdx.x + 1) / ctas;
         }
         // the sequence that holds place u_begin
-        const long long lo = (((ahead + x0) & (kOne - 1)) - u0) * per_b;
-        if (u0 > 0 && u_begin >= lo && u_begin < lo + (long long)u0 * per_b) {
+        const int here = level ? kWhole + kStart : u0;
+        const long long lo = (level ? (((ahead + x0) >> 44) - 1) * here : ((ahead + x0) & (kOne - 1)) - here) * per_b;
+        if (u0 > 0 && u_begin >= lo && u_begin < lo + (long long)here * per_b) {
             s_b = tid;
             s_before = lo;
         }
-        for (int b0 = kThreads; chunk * per_b <= u_begin; b0 += kThreads) {
+        for (int b0 = kThreads; !level && chunk * per_b <= u_begin; b0 += kThreads) {
             const int b = b0 + tid, u = b < a.B ? places_of(span_of(a, b), U) : 0;
             const long long x = scan(u);
             __syncthreads();
@@ -272,19 +281,25 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
     int b = s_b;
     long long before = s_before;  // places ahead of sequence b
     Span span = span_of(a, b);
-    int ub = places_of(span, U);
+    int ub = 0, nu = 0;  // its places and its units
+    auto measure = [&]() {
+        ub = places_of(span, U);
+        nu = ub - kStart;
+        if (level && ub > 0) ub = kWhole + kStart;
+    };
+    measure();
 
     for (long long u = u_begin; u < u_end;) {
         while (u >= before + (long long)ub * per_b) {  // next sequence with a token
             before += (long long)ub * per_b;
             ++b;
             span = span_of(a, b);
-            ub = places_of(span, U);
+            measure();
         }
         const int seg = (int)((u - before) / ub);
         const long long seg_begin = before + (long long)seg * ub;
         const int last_place = (int)((u_end < seg_begin + ub ? u_end : seg_begin + ub) - seg_begin);
-        const int first_u = max(0, (int)(u - seg_begin) - kStart), last_u = max(0, last_place - kStart);
+        const int first_u = max(0, (int)(u - seg_begin) - kStart), last_u = min(nu, max(0, last_place - kStart));
         u = seg_begin + last_place;
         if (last_u == first_u) continue;  // nothing but the start of a segment
         const int kh = seg / p.chunks, h0 = kh * group + seg % p.chunks * p.chunk;
@@ -598,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                 }
             }
         __syncthreads();
-        const bool whole = first_u == 0 && last_u == ub - kStart;
+        const bool whole = first_u == 0 && last_u == nu;
         float* slot_base = nullptr;
         int i0 = 0, i1 = 0;
         if (!whole) {
@@ -763,7 +778,7 @@ cudaError_t launch(const AttendArgs& a, const AttendPlan& p, cudaStream_t st) {
     const int64_t most = a.window > 0 && room > a.window ? a.window : room;
     const int unit = unit_tokens(DP * ES);
     const int64_t units = (most + unit - 1) / unit * per_b * a.B;
-    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(p.slots, (units + kMinUnits - 1) / kMinUnits));
+    const int64_t grid = std::min<int64_t>(p.slots, std::max((units + kMinUnits - 1) / kMinUnits, per_b * a.B));
     return launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), p.smem, st, a, p);
 }
 
