@@ -93,34 +93,34 @@ __device__ __forceinline__ void drain(Head& hd, int s, unsigned ph, int stages, 
     __syncwarp();
 }
 
-// One k-step by an elected lane of a converged warp.
+// A stage's four k-steps and the commit that frees it, by an elected lane of a converged warp;
+// with CG == 2 the commit arrives on the barrier at this place in both CTAs.  One election a
+// stage: with one for each instruction the issuing warp took 285 cycles a stage and was what
+// bound products of 64 to 1024 tokens.
+#define MOE_MMA_STAGE(CG, KIND, COMMIT)                                                        \
+    asm volatile(                                                                              \
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b64 x, y;\n\t.reg .b16 m;\n\t"                      \
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 t, %3, %3;\n\t"   \
+        "mov.u16 m, 3;\n\t"                                                                    \
+        "@e tcgen05.mma.cta_group::" CG ".kind::" KIND " [%0], %1, %2, %3, p;\n\t"             \
+        "add.u64 x, %1, 2;\n\tadd.u64 y, %2, 2;\n\t"                                           \
+        "@e tcgen05.mma.cta_group::" CG ".kind::" KIND " [%0], x, y, %3, t;\n\t"               \
+        "add.u64 x, %1, 4;\n\tadd.u64 y, %2, 4;\n\t"                                           \
+        "@e tcgen05.mma.cta_group::" CG ".kind::" KIND " [%0], x, y, %3, t;\n\t"               \
+        "add.u64 x, %1, 6;\n\tadd.u64 y, %2, 6;\n\t"                                           \
+        "@e tcgen05.mma.cta_group::" CG ".kind::" KIND " [%0], x, y, %3, t;\n\t"               \
+        "@e tcgen05.commit.cta_group::" CG ".mbarrier::arrive::one.shared::cluster." COMMIT    \
+        ";\n\t}" ::"r"(d),                                                                     \
+        "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(smem_u32(bar))                             \
+        : "memory")
 template <bool F8, int CG>
-__device__ __forceinline__ void mma_elect(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
-    if constexpr (F8 && CG == 1)
-        asm volatile(
-            "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
-            : "memory");
-    else if constexpr (F8)
-        asm volatile(
-            "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
-            : "memory");
-    else if constexpr (CG == 1)
-        asm volatile(
-            "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
-            : "memory");
+__device__ __forceinline__ void mma_stage(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc, uint64_t* bar) {
+    if constexpr (F8 && CG == 1) MOE_MMA_STAGE("1", "f8f6f4", "b64 [%5]");
+    else if constexpr (F8) MOE_MMA_STAGE("2", "f8f6f4", "multicast::cluster.b64 [%5], m");
+    else if constexpr (CG == 1) MOE_MMA_STAGE("1", "f16", "b64 [%5]");
+    else MOE_MMA_STAGE("2", "f16", "multicast::cluster.b64 [%5], m");
 }
+#undef MOE_MMA_STAGE
 
 // Instruction descriptor: fp32 sums, operand formats (f16 and E4M3 are 0, bf16 is 1),
 // M rows and N columns.
@@ -184,6 +184,7 @@ __device__ __forceinline__ void gelu2(float& v0, float& v1) {
 
 template <int VEC>
 __device__ __forceinline__ void activate(float (&v)[VEC], int act) {
+    if (act == MOE_ACT_NONE) return;
     if (act == MOE_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < VEC; i += 2) gelu2(v[i], v[i + 1]);
@@ -200,15 +201,27 @@ __device__ __forceinline__ void activate(float (&v)[VEC], int act) {
 template <int VEC>
 struct Columns {
     float scale[VEC], bias[VEC];
-    __device__ __forceinline__ void load(const LinearArgs& a, int n, int inc) {
+    __device__ __forceinline__ void load(const LinearArgs& a, int n, int inc) {  // past N: the last one's
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            const int m = n + i * inc;
-            scale[i] = a.w_scale && m < a.N ? a.w_scale[m] : 1.f;
+            scale[i] = 1.f;
             bias[i] = 0.f;
-            if (a.bias && m < a.N)
-                bias[i] = a.bias_type == MOE_F32 ? static_cast<const float*>(a.bias)[m]
-                                                 : half_bits_to_f32(static_cast<const uint16_t*>(a.bias)[m], a.bias_type);
+        }
+        if (a.w_scale) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) scale[i] = a.w_scale[min(n + i * inc, a.N - 1)];
+        }
+        if (a.bias) {
+            if (a.bias_type == MOE_F32) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) bias[i] = static_cast<const float*>(a.bias)[min(n + i * inc, a.N - 1)];
+            } else {
+                uint16_t h[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) h[i] = static_cast<const uint16_t*>(a.bias)[min(n + i * inc, a.N - 1)];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) bias[i] = half_bits_to_f32(h[i], a.bias_type);
+            }
         }
     }
 };
@@ -247,6 +260,20 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int64_t t, int n, in
         for (int i = 0; i < VEC; ++i)
             if (n + i * inc < a.N) finish_one(a, t, n + i * inc, v[i]);
     }
+}
+
+// A stage's two copies by an elected lane of a converged warp.
+__device__ __forceinline__ void load_stage(uint64_t* bar, uint32_t bytes, uint32_t dw, const CUtensorMap* wmap, uint32_t dx,
+                                           const CUtensorMap* xmap, int k, int n, int t, uint64_t wpolicy, uint64_t xpolicy) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%2], [%3, {%6, %7}], [%0], %9;\n\t"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%4], [%5, {%6, %8}], [%0], %10;\n\t}" ::"r"(smem_u32(bar)),
+        "r"(bytes), "r"(dw), "l"(wmap), "r"(dx), "l"(xmap), "r"(k), "r"(n), "r"(t), "l"(wpolicy), "l"(xpolicy)
+        : "memory");
 }
 
 // ---- split kernel ------------------------------------------------------------
@@ -316,10 +343,8 @@ __global__ void __launch_bounds__(kThreads, CTAS)
         unsigned ph = 0;
         for (int kb = kb0; kb < kb1; ++kb) {
             if (!wait_warp(&hd.empty[s], ph ^ 1u, hd, a.status, 2, s)) break;
-            uint8_t* st = base + (size_t)s * stage_bytes;
-            mbar_arrive_expect_tx_elect(&hd.full[s], stage_bytes);
-            tma_load_2d_hint_elect(st, &wmap, kb * (F8 ? 128 : 64), n0, &hd.full[s], first);
-            tma_load_2d_hint_elect(st + kABytes, &xmap, kb * (F8 ? 128 : 64), t0, &hd.full[s], last);
+            const uint32_t st = smem_u32(base) + (uint32_t)(s * stage_bytes);
+            load_stage(&hd.full[s], stage_bytes, st, &wmap, st + kABytes, &xmap, kb * (F8 ? 128 : 64), n0, t0, first, last);
             advance(s, ph, stages);
         }
         drain(hd, s, ph, stages, kb1 - kb0);
@@ -332,9 +357,7 @@ __global__ void __launch_bounds__(kThreads, CTAS)
             tc_fence_after();
             const uint64_t ad = sw128_desc(smem_u32(base + (size_t)s * stage_bytes));
             const uint64_t bd = sw128_desc(smem_u32(base + (size_t)s * stage_bytes + kABytes));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_elect<F8, 1>(tmem, ad + 2 * k, bd + 2 * k, idesc, kb > kb0 || k > 0);
-            tc_commit_elect(&hd.empty[s]);
+            mma_stage<F8, 1>(tmem, ad, bd, idesc, kb > kb0, &hd.empty[s]);
             advance(s, ph, stages);
         }
         tc_commit_elect(&hd.acc_full[0]);
@@ -412,13 +435,19 @@ __global__ void __launch_bounds__(kThreads, CTAS)
 
 // ---- tiled kernel --------------------------------------------------------------
 
-__device__ __forceinline__ void tma_load_pair_elect(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar,
-                                                    uint64_t policy) {
+// A stage's two copies by an elected lane of a converged warp; they arrive on `bar`, which may
+// be the peer's.  The leader first announces the bytes of both CTAs on its own barrier.
+__device__ __forceinline__ void load_pair_stage(uint64_t* own, bool leader, uint32_t bytes, uint32_t bar, uint32_t dx,
+                                                const CUtensorMap* xmap, uint32_t dw, const CUtensorMap* wmap, int k, int t,
+                                                int n, uint64_t policy) {
     asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "{\n\t.reg .pred e, f;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.and.u32 f, %1, 0, e;\n\t"
+        "@f mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %2;\n\t"
         "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-        "[%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy)
+        "[%4], [%5, {%8, %9}], [%3], %11;\n\t"
+        "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%6], [%7, {%8, %10}], [%3], %11;\n\t}" ::"r"(smem_u32(own)),
+        "r"((uint32_t)leader), "r"(bytes), "r"(bar), "r"(dx), "l"(xmap), "r"(dw), "l"(wmap), "r"(k), "r"(t), "r"(n), "l"(policy)
         : "memory");
 }
 // Arrives on the barrier at this place in both CTAs when the MMAs issued so far are done.
@@ -504,11 +533,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                uint8_t* st = base + (size_t)s * stage_bytes;
-                const uint32_t bar = map_rank(smem_u32(&hd.full[s]), 0);
-                if (rank == 0) mbar_arrive_expect_tx_elect(&hd.full[s], bytes);
-                tma_load_pair_elect(st, &xmap, kb * (F8 ? 128 : 64), t0, bar, keep);
-                tma_load_pair_elect(st + kABytes, &wmap, kb * (F8 ? 128 : 64), n0, bar, keep);
+                const uint32_t st = smem_u32(base) + (uint32_t)(s * stage_bytes);
+                load_pair_stage(&hd.full[s], rank == 0, bytes, map_rank(smem_u32(&hd.full[s]), 0), st, &xmap, st + kABytes,
+                                &wmap, kb * (F8 ? 128 : 64), t0, n0, keep);
                 advance(s, ph, g.stages);
             }
         }
@@ -529,10 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint64_t ad = sw128_desc(smem_u32(base + (size_t)s * stage_bytes));
                 const uint64_t bd = sw128_desc(smem_u32(base + (size_t)s * stage_bytes + kABytes));
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_elect<F8, 2>(tmem + buf * 256, ad + 2 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
-                commit_pair_elect(&hd.empty[s]);
+                mma_stage<F8, 2>(tmem + buf * 256, ad, bd, idesc, kb > 0, &hd.empty[s]);
                 advance(s, ph, g.stages);
             }
             if (!ok) break;
@@ -591,14 +615,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     exchange();
                     if (in) {
+                        float v[32];  // all four runs at once: a branch on flags and types for 32 values
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int r = (lane >> 2) + 8 * k;
                             const uint8_t* row = stage + r * 128;
                             const float4 lo = *reinterpret_cast<const float4*>(row + (((2 * (lane & 3)) ^ (r & 7)) << 4));
                             const float4 hi = *reinterpret_cast<const float4*>(row + (((2 * (lane & 3) + 1) ^ (r & 7)) << 4));
-                            float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                            if (t0 + r < a.T) finish<8>(a, t0 + r, nn, 1, sx[k], col, res[k], v, whole);
+                            const float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[8 * k + i] = fmaf(w[i], sx[k] * col.scale[i], col.bias[i]);
+                        }
+                        activate<32>(v, a.act);
+                        if (!whole) {  // the run that N ends in: through this lane's own places, one by one
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int r = (lane >> 2) + 8 * k;
+                                uint8_t* row = stage + r * 128;
+                                *reinterpret_cast<float4*>(row + (((2 * (lane & 3)) ^ (r & 7)) << 4)) =
+                                    make_float4(v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3]);
+                                *reinterpret_cast<float4*>(row + (((2 * (lane & 3) + 1) ^ (r & 7)) << 4)) =
+                                    make_float4(v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]);
+                            }
+#pragma unroll 1
+                            for (int j = 0; j < 32; ++j) {
+                                const int r = (lane >> 2) + 8 * (j >> 3), i = j & 7;
+                                if (t0 + r < a.T && nn + i < a.N)
+                                    finish_one(a, t0 + r, nn + i,
+                                               *reinterpret_cast<const float*>(
+                                                   stage + r * 128 + (((2 * (lane & 3) + (i >> 2)) ^ (r & 7)) << 4) + (i & 3) * 4));
+                            }
+                        } else {
+                            auto out = [&](int type) {
+                                if (a.res) {
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        float f[8];
+                                        res[k].get(type, f);
+#pragma unroll
+                                        for (int i = 0; i < 8; ++i) v[8 * k + i] += f[i];
+                                    }
+                                }
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const int t = t0 + (lane >> 2) + 8 * k;
+                                    const float(&w)[8] = *reinterpret_cast<const float(*)[8]>(v + 8 * k);
+                                    if (t < a.T) store_run<8>(a.y, (int64_t)t * a.y_stride + nn, type, w);
+                                }
+                            };
+                            if (a.y_type == MOE_BF16) out(MOE_BF16);
+                            else if (a.y_type == MOE_F16) out(MOE_F16);
+                            else out(MOE_F32);
                         }
                     }
                 } else {
