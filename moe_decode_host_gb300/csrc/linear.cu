@@ -62,18 +62,25 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+// From a CTA of the cluster where `on`, else zeros: no branch for the parts that there are not.
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, bool on) {
     float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.f32 %0, 0f00000000;\n\tmov.f32 %1, 0f00000000;\n\t"
+        "mov.f32 %2, 0f00000000;\n\tmov.f32 %3, 0f00000000;\n\t@p ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "=&f"(v.x), "=&f"(v.y), "=&f"(v.z), "=&f"(v.w)
+        : "r"(addr), "r"((uint32_t)on)
+        : "memory");
     return v;
 }
 
-__device__ __forceinline__ float ld_cluster1(uint32_t addr) {
+__device__ __forceinline__ float ld_cluster1(uint32_t addr, bool on) {
     float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t@p ld.shared::cluster.f32 %0, [%1];\n\t}"
+        : "=&f"(v)
+        : "r"(addr), "r"((uint32_t)on)
+        : "memory");
     return v;
 }
 
@@ -95,8 +102,7 @@ __device__ __forceinline__ void drain(Head& hd, int s, unsigned ph, int stages, 
 
 // A stage's four k-steps and the commit that frees it, by an elected lane of a converged warp;
 // with CG == 2 the commit arrives on the barrier at this place in both CTAs.  One election a
-// stage: with one for each instruction the issuing warp took 285 cycles a stage and was what
-// bound products of 64 to 1024 tokens.
+// stage takes the issuing warp 250 cycles beside its wait, one for each instruction 285.
 #define MOE_MMA_STAGE(CG, KIND, COMMIT)                                                        \
     asm volatile(                                                                              \
         "{\n\t.reg .pred e, p, t;\n\t.reg .b64 x, y;\n\t.reg .b16 m;\n\t"                      \
@@ -238,30 +244,6 @@ __device__ __forceinline__ void finish_one(const LinearArgs& a, int64_t t, int n
     store_run<1>(a.y, t * a.y_stride + n, a.y_type, one);
 }
 
-// The epilogue of VEC outputs of token t from n on, inc apart.  whole: one aligned run in
-// range, with the residual's bits in res; else element by element (with inc = 32 the lanes
-// of a warp still write and read whole lines).
-template <int VEC>
-__device__ __forceinline__ void finish(const LinearArgs& a, int64_t t, int n, int inc, float sx, const Columns<VEC>& col,
-                                       const Raw<VEC>& res, float (&v)[VEC], bool whole) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = fmaf(v[i], sx * col.scale[i], col.bias[i]);
-    activate<VEC>(v, a.act);
-    if (whole) {
-        if (a.res) {
-            float f[VEC];
-            res.get(a.y_type, f);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] += f[i];
-        }
-        store_run<VEC>(a.y, t * a.y_stride + n, a.y_type, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            if (n + i * inc < a.N) finish_one(a, t, n + i * inc, v[i]);
-    }
-}
-
 // A stage's two copies by an elected lane of a converged warp.
 __device__ __forceinline__ void load_stage(uint64_t* bar, uint32_t bytes, uint32_t dw, const CUtensorMap* wmap, uint32_t dx,
                                            const CUtensorMap* xmap, int k, int n, int t, uint64_t wpolicy, uint64_t xpolicy) {
@@ -326,7 +308,10 @@ __global__ void __launch_bounds__(kThreads, CTAS)
     Columns<4> col;
     Raw<4> res[CTAS == 1 ? 2 : 1];
     float sx[2] = {1.f, 1.f};
+    uint32_t peer[kSplitMax];  // this lane's first output of the block's first token, in each rank's sums
     if (warp >= 2) {
+#pragma unroll
+        for (int j = 0; j < kSplitMax; ++j) peer[j] = map_rank(smem_u32(base) + lane * (vec ? 16 : 4), min(j, S - 1));
         col.load(a, mine, inc);
 #pragma unroll
         for (int k = 0; k < (CTAS == 1 ? 2 : 1); ++k) {
@@ -368,11 +353,19 @@ __global__ void __launch_bounds__(kThreads, CTAS)
         const int q = warp & 3;
         wait_warp(&hd.acc_full[0], 0, hd, a.status, 3, 0);
         tc_fence_after();
-        for (int c = (warp - 2) / 4 * 16; c < cols; c += 32) {  // two warps share a quarter of the lanes
-            float v[16];
-            tc_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, v);
+        for (int c = (warp - 2) / 4 * 16; c < cols; c += 64) {  // two warps share a quarter of the lanes
+            const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + c;
+            float v[16], w[16];
+            float* to = dump + c * 128 + q * 32 + lane;
+            if (c + 32 < cols) {
+                tc_ld16x2(at, at + 32, v, w);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) dump[(c + i) * 128 + q * 32 + lane] = v[i];
+                for (int i = 0; i < 16; ++i) to[(32 + i) * 128] = w[i];
+            } else {
+                tc_ld16(at, v);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) to[i * 128] = v[i];
         }
         tc_fence_before();
     }
@@ -382,50 +375,86 @@ __global__ void __launch_bounds__(kThreads, CTAS)
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tcols) : "memory");
     }
-    // ---- the parts in rank order, then the epilogue ----
+    // ---- the parts in rank order, then the epilogue; branches are taken for all the tokens in
+    // hand at once (one a part, a flag and a run: 2350 cycles an iteration, 128 x 4096 x 4096
+    // JOINFIG) ----
     if (warp >= 2) {
         // two tokens at a time where there are registers for the parts of both on their way together
         constexpr int kAhead = CTAS == 1 ? 2 : 1;
-        for (int c = c0 + warp - 2, k = 0; c < c1; c += kAhead * kEpiWarps, ++k) {
+        for (int c = c0 + warp - 2, k = 0; c < c1 && mine < a.N; c += kAhead * kEpiWarps, ++k) {
             float4 p[kAhead][kSplitMax];
-#pragma unroll
-            for (int j = 0; j < kSplitMax; ++j)
-                if (j < S) {
-#pragma unroll
-                    for (int h = 0; h < kAhead; ++h) {  // a second token past the end rereads the first
-                        const int ch = c + (c + kEpiWarps * h < c1 ? kEpiWarps * h : 0);
-                        const uint32_t at = map_rank(smem_u32(dump + ch * 128 + (vec ? lane * 4 : lane)), j);
-                        if (vec) {
-                            p[h][j] = ld_cluster(at);
-                        } else {
-                            p[h][j] = make_float4(ld_cluster1(at), ld_cluster1(at + 128), ld_cluster1(at + 256),
-                                                  ld_cluster1(at + 384));
-                        }
-                    }
-                }
-            if (k > 0 && mine < a.N) {
-#pragma unroll
-                for (int h = 0; h < kAhead; ++h) {
-                    const int t = t0 + c + kEpiWarps * h;
-                    if (c + kEpiWarps * h < c1) {
-                        if (a.res && whole) res[h].load(a.res, (int64_t)t * a.res_stride + mine, a.y_type);
-                        if (a.x_scale) sx[h] = a.x_scale[t];
-                    }
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < kAhead; ++h) {
-                float v[4] = {0.f, 0.f, 0.f, 0.f};
+            const bool there[2] = {true, c + kEpiWarps < c1};
+            if (vec) {
 #pragma unroll
                 for (int j = 0; j < kSplitMax; ++j)
-                    if (j < S) {
-                        v[0] += p[h][j].x;
-                        v[1] += p[h][j].y;
-                        v[2] += p[h][j].z;
-                        v[3] += p[h][j].w;
+#pragma unroll
+                    for (int h = 0; h < kAhead; ++h) p[h][j] = ld_cluster(peer[j] + (c + kEpiWarps * h) * 512, j < S && there[h]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kSplitMax; ++j)
+#pragma unroll
+                    for (int h = 0; h < kAhead; ++h) {
+                        const uint32_t at = peer[j] + (c + kEpiWarps * h) * 512;
+                        const bool on = j < S && there[h];
+                        p[h][j] = make_float4(ld_cluster1(at, on), ld_cluster1(at + 128, on), ld_cluster1(at + 256, on),
+                                              ld_cluster1(at + 384, on));
                     }
-                if (mine < a.N && c + kEpiWarps * h < c1)
-                    finish<4>(a, t0 + c + kEpiWarps * h, mine, inc, sx[h], col, res[h], v, whole);
+            }
+            if (k > 0) {
+                if (a.x_scale) {
+#pragma unroll
+                    for (int h = 0; h < kAhead; ++h)
+                        if (there[h]) sx[h] = a.x_scale[t0 + c + kEpiWarps * h];
+                }
+                if (a.res && whole) {
+#pragma unroll
+                    for (int h = 0; h < kAhead; ++h)
+                        if (there[h])
+                            res[h].load(a.res, (int64_t)(t0 + c + kEpiWarps * h) * a.res_stride + mine, a.y_type);
+                }
+            }
+            float v[4 * kAhead];
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h) {
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < kSplitMax; ++j) {
+                    sum[0] += p[h][j].x;
+                    sum[1] += p[h][j].y;
+                    sum[2] += p[h][j].z;
+                    sum[3] += p[h][j].w;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 * h + i] = fmaf(sum[i], sx[h] * col.scale[i], col.bias[i]);
+            }
+            activate<4 * kAhead>(v, a.act);
+            if (!whole) {  // element by element; with inc = 32 a warp still writes and reads whole lines
+#pragma unroll
+                for (int h = 0; h < kAhead; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (there[h] && mine + i * inc < a.N)
+                            finish_one(a, t0 + c + kEpiWarps * h, mine + i * inc, v[4 * h + i]);
+            } else {
+                auto out = [&](int type) {
+                    if (a.res) {
+#pragma unroll
+                        for (int h = 0; h < kAhead; ++h) {
+                            float f[4];
+                            res[h].get(type, f);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[4 * h + i] += f[i];
+                        }
+                    }
+#pragma unroll
+                    for (int h = 0; h < kAhead; ++h) {
+                        const float w[4] = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+                        if (there[h]) store_run<4>(a.y, (int64_t)(t0 + c + kEpiWarps * h) * a.y_stride + mine, type, w);
+                    }
+                };
+                if (a.y_type == MOE_BF16) out(MOE_BF16);
+                else if (a.y_type == MOE_F16) out(MOE_F16);
+                else out(MOE_F32);
             }
         }
     }
@@ -603,14 +632,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     float sx[4];
                     if (in) {
                         col.load(a, nn, 1);
+                        const int r0 = t0 + (lane >> 2);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int t = t0 + (lane >> 2) + 8 * k;
-                            sx[k] = 1.f;
-                            if (t < a.T) {
-                                if (a.res && whole) res[k].load(a.res, (int64_t)t * a.res_stride + nn, a.y_type);
-                                if (a.x_scale) sx[k] = a.x_scale[t];
-                            }
+                        for (int k = 0; k < 4; ++k) sx[k] = 1.f;
+                        if (a.x_scale) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) sx[k] = a.x_scale[min(r0 + 8 * k, a.T - 1)];
+                        }
+                        if (a.res && whole) {
+                            auto fetch = [&](int type) {  // past T: the last token's
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    res[k].load(a.res, (int64_t)min(r0 + 8 * k, a.T - 1) * a.res_stride + nn, type);
+                            };
+                            if (a.y_type == MOE_F32) fetch(MOE_F32);
+                            else fetch(MOE_BF16);  // 16 bits either way
                         }
                     }
                     exchange();
