@@ -37,6 +37,10 @@ constexpr int kMaxStages = 12;
 __host__ __device__ constexpr int split_ring(int ctas) { return ctas == 2 ? 104 * 1024 : 192 * 1024; }
 constexpr int kSplitMax = 8;           // CTAs of a cluster
 constexpr int kTileRing = 192 * 1024;  // bytes of the tiled kernel's ring
+// Outputs of a tile up to which a stage holds two blocks of K: the loading and the issuing warp
+// take about 170 ns a stage, more than the products of narrow tiles (one and two blocks: 256 x
+// 1024 x 4096 14.5 and 11.5 us with 64 outputs a tile; 1024 x 4096 x 4096 23.9 and 24.7 with 256).
+constexpr int kTwoBlocks = 128;
 constexpr int kEpiBytes = 32 * 32 * 4;  // staging of an epilogue warp of the tiled kernel: 32 tokens x 32 outputs
 
 struct Head {
@@ -115,17 +119,22 @@ __device__ __forceinline__ void drain(Head& hd, int s, unsigned ph, int stages, 
         "@e tcgen05.mma.cta_group::" CG ".kind::" KIND " [%0], x, y, %3, t;\n\t"               \
         "add.u64 x, %1, 6;\n\tadd.u64 y, %2, 6;\n\t"                                           \
         "@e tcgen05.mma.cta_group::" CG ".kind::" KIND " [%0], x, y, %3, t;\n\t"               \
-        "@e tcgen05.commit.cta_group::" CG ".mbarrier::arrive::one.shared::cluster." COMMIT    \
-        ";\n\t}" ::"r"(d),                                                                     \
+        COMMIT "\n\t}" ::"r"(d),                                                               \
         "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(smem_u32(bar))                             \
         : "memory")
-template <bool F8, int CG>
+#define MOE_COMMIT_ONE "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];"
+#define MOE_COMMIT_PAIR "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], m;"
+template <bool F8, int CG, bool COMMIT = true>
 __device__ __forceinline__ void mma_stage(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc, uint64_t* bar) {
-    if constexpr (F8 && CG == 1) MOE_MMA_STAGE("1", "f8f6f4", "b64 [%5]");
-    else if constexpr (F8) MOE_MMA_STAGE("2", "f8f6f4", "multicast::cluster.b64 [%5], m");
-    else if constexpr (CG == 1) MOE_MMA_STAGE("1", "f16", "b64 [%5]");
-    else MOE_MMA_STAGE("2", "f16", "multicast::cluster.b64 [%5], m");
+    if constexpr (F8 && CG == 1) MOE_MMA_STAGE("1", "f8f6f4", MOE_COMMIT_ONE);
+    else if constexpr (CG == 1) MOE_MMA_STAGE("1", "f16", MOE_COMMIT_ONE);
+    else if constexpr (F8 && COMMIT) MOE_MMA_STAGE("2", "f8f6f4", MOE_COMMIT_PAIR);
+    else if constexpr (F8) MOE_MMA_STAGE("2", "f8f6f4", "");
+    else if constexpr (COMMIT) MOE_MMA_STAGE("2", "f16", MOE_COMMIT_PAIR);
+    else MOE_MMA_STAGE("2", "f16", "");
 }
+#undef MOE_COMMIT_ONE
+#undef MOE_COMMIT_PAIR
 #undef MOE_MMA_STAGE
 
 // Instruction descriptor: fp32 sums, operand formats (f16 and E4M3 are 0, bf16 is 1),
@@ -375,9 +384,8 @@ __global__ void __launch_bounds__(kThreads, CTAS)
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tcols) : "memory");
     }
-    // ---- the parts in rank order, then the epilogue; branches are taken for all the tokens in
-    // hand at once (one a part, a flag and a run: 2350 cycles an iteration, 128 x 4096 x 4096
-    // JOINFIG) ----
+    // ---- the parts in rank order, then the epilogue; branches are taken once for all the tokens
+    // in hand (256 x 1024 x 4096 bf16 10.4 us; with one for each part, flag and run 11.7) ----
     if (warp >= 2) {
         // two tokens at a time where there are registers for the parts of both on their way together
         constexpr int kAhead = CTAS == 1 ? 2 : 1;
@@ -464,9 +472,10 @@ __global__ void __launch_bounds__(kThreads, CTAS)
 
 // ---- tiled kernel --------------------------------------------------------------
 
-// A stage's two copies by an elected lane of a converged warp; they arrive on `bar`, which may
-// be the peer's.  The leader first announces the bytes of both CTAs on its own barrier.
-__device__ __forceinline__ void load_pair_stage(uint64_t* own, bool leader, uint32_t bytes, uint32_t bar, uint32_t dx,
+// The two copies of a block of K by an elected lane of a converged warp; they arrive on `bar`,
+// which may be the peer's.  With `announce` (the leader, at a stage's first block) the bytes of
+// both CTAs are first announced on its own barrier.
+__device__ __forceinline__ void load_pair_block(uint64_t* own, bool announce, uint32_t bytes, uint32_t bar, uint32_t dx,
                                                 const CUtensorMap* xmap, uint32_t dw, const CUtensorMap* wmap, int k, int t,
                                                 int n, uint64_t policy) {
     asm volatile(
@@ -476,7 +485,7 @@ __device__ __forceinline__ void load_pair_stage(uint64_t* own, bool leader, uint
         "[%4], [%5, {%8, %9}], [%3], %11;\n\t"
         "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
         "[%6], [%7, {%8, %10}], [%3], %11;\n\t}" ::"r"(smem_u32(own)),
-        "r"((uint32_t)leader), "r"(bytes), "r"(bar), "r"(dx), "l"(xmap), "r"(dw), "l"(wmap), "r"(k), "r"(t), "r"(n), "l"(policy)
+        "r"((uint32_t)announce), "r"(bytes), "r"(bar), "r"(dx), "l"(xmap), "r"(dw), "l"(wmap), "r"(k), "r"(t), "r"(n), "l"(policy)
         : "memory");
 }
 // Arrives on the barrier at this place in both CTAs when the MMAs issued so far are done.
@@ -505,14 +514,14 @@ __device__ __forceinline__ void tile_at(const TileGrid& g, int i, int& m, int& n
     m = 8 * b + r - n * rows;
 }
 
-template <bool F8>
+template <bool F8, int SUB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_tile_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap wmap,
                        const __grid_constant__ CUtensorMap xmap, const TileGrid g, bool vec) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* epi = base + kTileRing;
-    const int stage_bytes = kABytes + g.bn / 2 * kRowBytes;
+    const int w_bytes = g.bn / 2 * kRowBytes, stage_bytes = SUB * (kABytes + w_bytes);
     Head& hd = *reinterpret_cast<Head*>(epi + kEpiWarps * kEpiBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -550,25 +559,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // each CTA stages its half: 128 tokens and bn / 2 outputs; the leader's barrier counts both
         const uint64_t keep = l2_policy_evict_last();
         const int half = g.bn / 2;
-        const unsigned bytes = 2u * (unsigned)(kABytes + half * kRowBytes);
+        const unsigned bytes = 2u * (unsigned)stage_bytes;
         int s = 0;
         unsigned ph = 0;
         for (int i = pair; i < tiles && ok; i += pairs) {
             int m, n;
             tile_at(g, i, m, n);
             const int t0 = m * 256 + (int)rank * 128, n0 = n * g.bn + (int)rank * half;
-            for (int kb = 0; kb < nkb; ++kb) {
+            for (int kb = 0; kb < nkb; kb += SUB) {
                 if (!wait_warp(&hd.empty[s], ph ^ 1u, hd, a.status, 2, s)) {
                     ok = false;
                     break;
                 }
                 const uint32_t st = smem_u32(base) + (uint32_t)(s * stage_bytes);
-                load_pair_stage(&hd.full[s], rank == 0, bytes, map_rank(smem_u32(&hd.full[s]), 0), st, &xmap, st + kABytes,
-                                &wmap, kb * (F8 ? 128 : 64), t0, n0, keep);
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)  // a block past the last is zeros
+                    load_pair_block(&hd.full[s], rank == 0 && u == 0, bytes, map_rank(smem_u32(&hd.full[s]), 0),
+                                    st + u * kABytes, &xmap, st + SUB * kABytes + u * w_bytes, &wmap,
+                                    (kb + u) * (F8 ? 128 : 64), t0, n0, keep);
                 advance(s, ph, g.stages);
             }
         }
-        if (ok) drain(hd, s, ph, g.stages, (int64_t)nkb * ((tiles - pair + pairs - 1) / pairs));
+        if (ok) drain(hd, s, ph, g.stages, (int64_t)((nkb + SUB - 1) / SUB) * ((tiles - pair + pairs - 1) / pairs));
     } else if (warp == 1 && rank == 0) {
         const uint32_t idesc = mma_idesc(a.in_type, 256, g.bn);
         int s = 0, buf = 0;
@@ -577,15 +589,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!wait_warp(&hd.acc_empty[buf], ((accph >> buf) & 1u) ^ 1u, hd, a.status, 4, buf)) break;
             accph ^= 1u << buf;
             tc_fence_after();
-            for (int kb = 0; kb < nkb; ++kb) {
+            for (int kb = 0; kb < nkb; kb += SUB) {
                 if (!wait_warp(&hd.full[s], ph, hd, a.status, 1, s)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t ad = sw128_desc(smem_u32(base + (size_t)s * stage_bytes));
-                const uint64_t bd = sw128_desc(smem_u32(base + (size_t)s * stage_bytes + kABytes));
-                mma_stage<F8, 2>(tmem + buf * 256, ad, bd, idesc, kb > 0, &hd.empty[s]);
+                const uint64_t ad = sw128_desc(smem_u32(base) + s * stage_bytes);
+                const uint64_t bd = sw128_desc(smem_u32(base) + s * stage_bytes + SUB * kABytes);
+                if constexpr (SUB == 2)
+                    mma_stage<F8, 2, false>(tmem + buf * 256, ad, bd, idesc, kb > 0, &hd.empty[s]);
+                mma_stage<F8, 2>(tmem + buf * 256, ad + (SUB - 1) * (kABytes >> 4), bd + (SUB - 1) * (w_bytes >> 4), idesc,
+                                 SUB == 2 || kb > 0, &hd.empty[s]);
                 advance(s, ph, g.stages);
             }
             if (!ok) break;
@@ -852,26 +867,30 @@ cudaError_t launch_split(const LinearArgs& a, int bn, int ksplit, bool vec, cuda
     return cudaLaunchKernelEx(&cfg, linear_split_kernel<F8, CTAS>, a, wmap, xmap, bn, stages, vec);
 }
 
-template <bool F8>
-cudaError_t launch_tiles(const LinearArgs& a, const TileGrid& g, bool vec, cudaStream_t st) {
+template <bool F8, int SUB>
+cudaError_t launch_tiles(const LinearArgs& a, TileGrid g, bool vec, cudaStream_t st) {
     CUtensorMap wmap, xmap;
     if (!encode_rows(&wmap, a, a.w, a.N, a.w_stride, g.bn / 2) || !encode_rows(&xmap, a, a.x, a.T, a.x_stride, 128))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> configured;
-    cudaError_t err = ensure_smem_limit((const void*)linear_tile_kernel<F8>, kTileSmem, configured);
+    cudaError_t err = ensure_smem_limit((const void*)linear_tile_kernel<F8, SUB>, kTileSmem, configured);
     if (err != cudaSuccess) return err;
     const int pairs = min(a.sm_count / 2, g.tm * g.tn);
-    return launch_pdl(linear_tile_kernel<F8>, dim3(2 * pairs), dim3(kThreads), kTileSmem, st, a, wmap, xmap, g, vec);
+    g.stages = std::min(kMaxStages, kTileRing / (SUB * (kABytes + g.bn / 2 * kRowBytes)));
+    return launch_pdl(linear_tile_kernel<F8, SUB>, dim3(2 * pairs), dim3(kThreads), kTileSmem, st, a, wmap, xmap, g, vec);
 }
 
 }  // namespace
 
 // Which kernel, by what each is expected to take in ns (measured on bf16 products of 64 to
 // 8192 tokens, 256 to 8192 outputs and depths of 256 to 8192; a block of K is the 128 bytes of a stage):
-//  tiles  4500 + rounds * blocks of K * max(200, 100 + 0.95 bn); below 200 a stage's latency
-//         over the ring's depth shows.  512 x 4096 x 4096: 18.5 us against 20.4 split.
-//  split  3000 + 20 bn for the join + blocks of K of a CTA * (200 + 0.8 bn).
-//         256 x 1024 x 4096: 11.1 us against 15.6 in tiles.
+//  tiles  1600 + blocks of K * step + (rounds - 1) * max(blocks of K * step, epilogue) + epilogue,
+//         for an epilogue is hidden under the next tile's products but for the last.  Epilogue:
+//         1000 + 14 bn.  Step, the most of: 50 + 1.15 bn to 128 outputs and 0.62 for each beyond
+//         them (the issuing warps, then the tensor cores); the stage of all CTAs at the 17 TB/s
+//         that L2 gives.  512 x 4096 x 4096: 16.7 us against 20.3 split.
+//  split  2500 + rounds * (20 bn for the join + blocks of K of a CTA * (200 + 0.8 bn)).
+//         128 x 4096 x 4096: 10.7 us against 13.8 in tiles.
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
     const bool f8 = a.in_type == MOE_E4M3;
@@ -883,12 +902,14 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st) {
     int64_t tiles_ns = INT64_MAX;
     for (int bn = 256; bn >= 64; bn -= 32) {  // the width that leaves the least work to the last round
         const int64_t tn = (a.N + bn - 1) / bn, rounds = (g.tm * tn + pairs - 1) / pairs;
-        const int64_t ns = 4500 + rounds * nkb * std::max(200, 100 + bn * 95 / 100);
+        const int64_t ctas = 2 * std::min<int64_t>(pairs, g.tm * tn);
+        const int64_t l2 = ctas * (kABytes + bn / 2 * kRowBytes) / 17000, epi = 1000 + 14 * bn;
+        const int64_t pass = nkb * std::max<int64_t>(l2, bn <= 128 ? 50 + bn * 115 / 100 : 197 + (bn - 128) * 62 / 100);
+        const int64_t ns = 1600 + pass + (rounds - 1) * std::max(pass, epi) + epi;
         if (ns < tiles_ns) {
             tiles_ns = ns;
             g.tn = (int)tn;
             g.bn = bn;
-            g.stages = std::min(kMaxStages, kTileRing / (kABytes + bn / 2 * kRowBytes));
         }
     }
     // split: token blocks as even as they come, and K over what is left of the GPU.  Two CTAs an SM
@@ -901,8 +922,11 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st) {
     if (err == cudaSuccess && !two) err = cluster_size<1>(blocks, nkb, &ksplit);
     if (err != cudaSuccess) return err;
     const int64_t at_once = (int64_t)a.sm_count * (two ? 2 : 1), rounds = (blocks * ksplit + at_once - 1) / at_once;
-    const int64_t split_ns = 3000 + 20 * bn + rounds * ((nkb + ksplit - 1) / ksplit) * (200 + bn * 8 / 10);
-    if (a.T > 64 && tiles_ns < split_ns) return f8 ? launch_tiles<true>(a, g, vec, st) : launch_tiles<false>(a, g, vec, st);
+    const int64_t split_ns = 2500 + rounds * (20 * bn + ((nkb + ksplit - 1) / ksplit) * (200 + bn * 8 / 10));
+    if (a.T > 64 && tiles_ns < split_ns) {
+        if (g.bn <= kTwoBlocks) return f8 ? launch_tiles<true, 2>(a, g, vec, st) : launch_tiles<false, 2>(a, g, vec, st);
+        return f8 ? launch_tiles<true, 1>(a, g, vec, st) : launch_tiles<false, 1>(a, g, vec, st);
+    }
     if (two) return f8 ? launch_split<true, 2>(a, bn, ksplit, vec4, st) : launch_split<false, 2>(a, bn, ksplit, vec4, st);
     return f8 ? launch_split<true, 1>(a, bn, ksplit, vec4, st) : launch_split<false, 1>(a, bn, ksplit, vec4, st);
 }
