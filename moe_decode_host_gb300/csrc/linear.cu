@@ -16,9 +16,10 @@
 //                 tile runs under the next tile's products.
 //
 // Measured on a GB300 (launches of a graph): 1 x 4096 x 4096 bf16 with residual 7.3 us (4.6
-// TB/s of weights, launch and fill included), 32 x 6144 x 4096 E4M3 6.5 us, 8192 x 6144 x
-// 4096 bf16 with bias, GELU and residual 230 us (1790 TFLOP/s; 265 us back to back under the
-// power cap), without an epilogue 218 us (cuBLAS 209).
+// TB/s of weights, launch and fill included), 32 x 6144 x 4096 E4M3 6.4 us, 8192 x 6144 x
+// 4096 bf16 with bias, GELU and residual 231 us (1780 TFLOP/s; 263 us back to back under the
+// power cap), without an epilogue 217 us (cuBLAS 231 in the same bursts of 30).  Between them
+// 128 x 4096 x 4096 10.8 us (cuBLAS 7.6), 512 16.7 (11.6), 1024 23.4 (19.8).
 #include <algorithm>
 
 #include "ptx.cuh"
