@@ -356,6 +356,14 @@ def test_attend_batches(m, lens, ct):
     check_attend(m, gen(len(lens)), lens, 8, 2, 128, 16, BF16, ct)
 
 
+@pytest.mark.parametrize("lens", [[320], [321], [319, 0, 1, 320], [640, 641, 639], [0, 17, 0, 0, 300], [320] * 76, [16] * 128,
+                                  [16] * 129])
+@pytest.mark.parametrize("hq,hkv,D,ct", [(8, 2, 128, BF16), (32, 2, 64, E4M3), (3, 1, 256, F16)])
+def test_attend_short_sequences(m, lens, hq, hkv, D, ct):
+    """Lengths about the most that one block takes whole, and batches about the most it does so for."""
+    check_attend(m, gen(len(lens) + D), lens, hq, hkv, D, 16, F16 if ct == F16 else BF16, ct)
+
+
 def test_attend_sharp_and_flat_scores(m):
     """Scores far apart (one key takes all), negative scale, and scale zero (a mean)."""
     check_attend(m, gen(1), [300, 50], 8, 2, 64, 16, BF16, BF16, scale=8.0, gain=4.0)
@@ -555,6 +563,24 @@ def test_linear(m, T, N, K, xt, yt):
                                             (E4M3, BF16, F32, True), (E4M3, F32, None, True), (F16, BF16, None, False)])
 def test_linear_epilogue(m, T, act, xt, yt, bias, res):
     check_linear(m, gen(T), T, 333, 256, xt, yt, act, bias, res, ragged=True)
+
+
+@pytest.mark.parametrize("K", [16, 64, 80, 128, 192, 1040])  # blocks of K in odd and even numbers, the last one short
+@pytest.mark.parametrize("T,N", [(257, 1023), (300, 72), (513, 2050), (1000, 8100)])
+@pytest.mark.parametrize("yt", [BF16, F16, F32])
+def test_linear_tiles_end_inside_a_run(m, T, N, K, yt):
+    """Aligned rows whose last run of outputs is cut short, with residual, in tiles of several widths."""
+    g = gen(T + N + K)
+    x, w = randn(g, T, K).to(BF16), (randn(g, N, K) / math.sqrt(K)).to(BF16)
+    wide = torch.full((T, (N + 15) // 8 * 8), float("nan"), dtype=yt, device="cuda")
+    y = wide[:, :N]
+    r = randn(g, T, wide.shape[1]).to(yt)[:, :N]
+    m.moe_linear(x, w, y, residual=r)
+    sums, size = x.double() @ w.double().t(), x.double().abs() @ w.double().abs().t()
+    want = sums + r.double()
+    tol = size * (K / 16 + 4) * 2.0 ** -22 + sums.abs() * 2.0 ** -20 + want.abs() * 2.0 ** -23 + 1e-6
+    within(y, want, tol + want.abs() * U[yt] + SUB[yt])
+    assert wide[:, N:].isnan().all()
 
 
 def test_linear_residual_in_place_and_special_values(m):
