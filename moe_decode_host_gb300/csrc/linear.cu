@@ -438,12 +438,30 @@ __global__ void __launch_bounds__(kThreads, CTAS)
             }
             activate<4 * kAhead>(v, a.act);
             if (!whole) {  // element by element; with inc = 32 a warp still writes and reads whole lines
+                auto out = [&](int type) {
+                    if (a.res) {
+                        Raw<1> r[4 * kAhead];
 #pragma unroll
-                for (int h = 0; h < kAhead; ++h)
+                        for (int i = 0; i < 4 * kAhead; ++i)
+                            if (there[i / 4] && mine + i % 4 * inc < a.N)
+                                r[i].load(a.res, (int64_t)(t0 + c + kEpiWarps * (i / 4)) * a.res_stride + mine + i % 4 * inc, type);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (there[h] && mine + i * inc < a.N)
-                            finish_one(a, t0 + c + kEpiWarps * h, mine + i * inc, v[4 * h + i]);
+                        for (int i = 0; i < 4 * kAhead; ++i) {
+                            float f[1];
+                            r[i].get(type, f);
+                            v[i] += f[0];
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4 * kAhead; ++i) {
+                        const float one[1] = {v[i]};
+                        if (there[i / 4] && mine + i % 4 * inc < a.N)
+                            store_run<1>(a.y, (int64_t)(t0 + c + kEpiWarps * (i / 4)) * a.y_stride + mine + i % 4 * inc, type, one);
+                    }
+                };
+                if (a.y_type == MOE_BF16) out(MOE_BF16);
+                else if (a.y_type == MOE_F16) out(MOE_F16);
+                else out(MOE_F32);
             } else {
                 auto out = [&](int type) {
                     if (a.res) {
@@ -723,7 +741,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 } else {
                     // rows of any alignment: a lane takes one output of every token, so that a warp's
                     // stores and residuals are consecutive (8087 outputs of 6116 x 1424, fp32 with
-                    // residual: 541 us with 8 outputs a lane, element by element)
+                    // residual: 180 us; with a branch on types and flags for each output 278, with 8
+                    // outputs a lane, element by element, 541)
                     const int nn = n0 + c + lane;
                     const bool in = nn < n0 + cols;
                     Columns<1> col;
@@ -731,33 +750,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (in) {
                         col.load(a, nn, 1);
                         if (a.res) {
+                            auto fetch = [&](int type) {  // past T: the last token's
 #pragma unroll
-                            for (int r = 0; r < 32; ++r)
-                                if (t0 + r < a.T) res[r].load(a.res, (int64_t)(t0 + r) * a.res_stride + nn, a.y_type);
+                                for (int r = 0; r < 32; ++r)
+                                    res[r].load(a.res, (int64_t)min(t0 + r, a.T - 1) * a.res_stride + nn, type);
+                            };
+                            if (a.y_type == MOE_F32) fetch(MOE_F32);
+                            else fetch(MOE_BF16);  // 16 bits either way
                         }
                     }
                     exchange();
                     if (in) {
 #pragma unroll
                         for (int r0 = 0; r0 < 32; r0 += 8) {
-                            float v[8];
+                            float v[8], sx[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) sx[i] = 1.f;
+                            if (a.x_scale) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) sx[i] = a.x_scale[min(t0 + r0 + i, a.T - 1)];
+                            }
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const float sum = *reinterpret_cast<const float*>(stage + (r0 + i) * 128 +
                                                                                   (((lane >> 2) ^ i) << 4) + (lane & 3) * 4);
-                                const float sx = a.x_scale && t0 + r0 + i < a.T ? a.x_scale[t0 + r0 + i] : 1.f;
-                                v[i] = fmaf(sum, sx * col.scale[0], col.bias[0]);
+                                v[i] = fmaf(sum, sx[i] * col.scale[0], col.bias[0]);
                             }
                             activate<8>(v, a.act);
+                            auto out = [&](int type) {
+                                if (a.res) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                if (t0 + r0 + i < a.T) {
-                                    float one[1] = {0.f};
-                                    if (a.res) res[r0 + i].get(a.y_type, one);
-                                    one[0] += v[i];
-                                    store_run<1>(a.y, (int64_t)(t0 + r0 + i) * a.y_stride + nn, a.y_type, one);
+                                    for (int i = 0; i < 8; ++i) {
+                                        float one[1];
+                                        res[r0 + i].get(type, one);
+                                        v[i] += one[0];
+                                    }
                                 }
-                            }
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const float one[1] = {v[i]};
+                                    if (t0 + r0 + i < a.T)
+                                        store_run<1>(a.y, (int64_t)(t0 + r0 + i) * a.y_stride + nn, type, one);
+                                }
+                            };
+                            if (a.y_type == MOE_BF16) out(MOE_BF16);
+                            else if (a.y_type == MOE_F16) out(MOE_F16);
+                            else out(MOE_F32);
                         }
                     }
                 }
