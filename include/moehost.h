@@ -370,7 +370,9 @@ int moe_quant_mxfp4(const void* x_bf16, int rows, int K, uint8_t* nib, uint8_t* 
  * norm, position rotation with the append to a paged key-value cache, attention of
  * one new token per sequence over that cache, and the dense products between them.
  * All strides are in elements, the innermost dimension is contiguous, and no call
- * allocates device memory or synchronises, so all can be captured in a graph.  Sums,
+ * allocates device memory or synchronises, so all can be captured in a graph.  Every call
+ * runs on the calling thread's current device, which has to be the one that its buffers,
+ * its stream and its cache handle belong to (the Python binding refuses others).  Sums,
  * statistics and accumulators are fp32; each output is rounded once. */
 
 /* Residual addition and root-mean-square norm:

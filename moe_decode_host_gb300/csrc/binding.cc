@@ -17,6 +17,7 @@ namespace {
 
 PyObject* g_error = nullptr;       // MoeError(code, where)
 PyObject* g_raw_stream = nullptr;  // torch: device index -> cudaStream_t of the current stream
+PyObject* g_current = nullptr;     // torch: index of the current device
 enum { kBf16, kF16, kF32, kE4m3, kI32, kI64, kTypes };
 PyObject* g_types[kTypes];  // torch dtypes in that order; the first four are moehost.h's codes
 
@@ -25,7 +26,7 @@ decltype(&moe_kv_append) f_append = nullptr;
 decltype(&moe_kv_attend) f_attend = nullptr;
 decltype(&moe_linear) f_linear = nullptr;
 
-PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_is_cuda, *s_get_device, *s_cuda_stream, *s_call;
+PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device, *s_device_index, *s_cuda_stream, *s_call;
 
 // ---- errors ---------------------------------------------------------------------
 
@@ -39,8 +40,15 @@ void raise(int code, const char* where, const char* what, const char* why) {
         Py_DECREF(e);
     }
 }
-bool refuse(const char* where, const char* what, const char* why) {
-    raise(MOE_ERR_INVALID_ARG, where, what, why);
+// One call of an entry point: its name, and the GPU that its tensors are on (-1 before the first).
+// The library launches on the current device, whatever memory it is given, so that this GPU has
+// to be the current one and every tensor's: anything else is refused before the launch.
+struct Call {
+    const char* name;
+    int device = -1;
+};
+bool refuse(const Call& c, const char* what, const char* why) {
+    raise(MOE_ERR_INVALID_ARG, c.name, what, why);
     return false;
 }
 PyObject* finish(int code, const char* where) {
@@ -75,20 +83,35 @@ bool read_sizes(PyObject* seq, int64_t (&out)[kDims], int& n) {
     return (ok || n > kDims) && !PyErr_Occurred();
 }
 
+// An integer that a call of torch's gave (and which is let go of here); false with an exception set.
+bool small_int(PyObject* o, int& v) {
+    if (!o) return false;
+    v = (int)PyLong_AsLong(o);
+    Py_DECREF(o);
+    return !PyErr_Occurred();
+}
+
+bool on_device(Call& c, int device, const char* name) {
+    if (device < 0) return refuse(c, name, "is not on a GPU");
+    if (c.device < 0) {
+        int now = -1;
+        if (!small_int(PyObject_CallNoArgs(g_current), now)) return false;
+        if (device != now) return refuse(c, name, "is not on the current GPU");
+        c.device = device;
+    }
+    return device == c.device || refuse(c, name, "is on another GPU than the call's other tensors");
+}
+
 // Fills t from a CUDA tensor of one of the known types; false with an exception set.
-bool read(PyObject* o, Tensor& t, const char* where, const char* name) {
+bool read(PyObject* o, Tensor& t, Call& where, const char* name) {
     PyObject* d = PyObject_GetAttr(o, s_dtype);
     if (!d) return false;
     for (int i = 0; i < kTypes; ++i)
         if (d == g_types[i]) t.type = i;
     Py_DECREF(d);
     if (t.type < 0) return refuse(where, name, "has a type that the call does not take");
-    PyObject* c = PyObject_GetAttr(o, s_is_cuda);
-    if (!c) return false;
-    const bool cuda = c == Py_True;
-    Py_DECREF(c);
-    if (!cuda) return refuse(where, name, "is not on a GPU");
-    int n = 0;
+    int n = 0, device = -1;  // -1: a CPU tensor
+    if (!small_int(PyObject_CallMethodNoArgs(o, s_get_device), device) || !on_device(where, device, name)) return false;
     if (!read_sizes(PyObject_GetAttr(o, s_shape), t.shape, t.dims) ||
         !read_sizes(PyObject_CallMethodNoArgs(o, s_stride), t.stride, n))
         return false;
@@ -102,7 +125,7 @@ bool read(PyObject* o, Tensor& t, const char* where, const char* name) {
 bool given(PyObject* o) { return o && o != Py_None; }
 
 // A matrix [rows, cols] of any of the element types with contiguous rows.
-bool matrix(PyObject* o, Tensor& t, int64_t rows, int64_t cols, const char* where, const char* name) {
+bool matrix(PyObject* o, Tensor& t, int64_t rows, int64_t cols, Call& where, const char* name) {
     if (!read(o, t, where, name)) return false;
     if (t.type > kE4m3) return refuse(where, name, "has a type that the call does not take");
     if (t.dims != 2 || (rows >= 0 && (t.shape[0] != rows || t.shape[1] != cols)))
@@ -112,7 +135,7 @@ bool matrix(PyObject* o, Tensor& t, int64_t rows, int64_t cols, const char* wher
 }
 
 // A contiguous vector of n elements; type < 0: any of the element types.
-bool vector(PyObject* o, Tensor& t, int64_t n, int type, const char* where, const char* name) {
+bool vector(PyObject* o, Tensor& t, int64_t n, int type, Call& where, const char* name) {
     if (!read(o, t, where, name)) return false;
     if (type >= 0 ? t.type != type : t.type > kE4m3) return refuse(where, name, "has a type that the call does not take");
     if (t.dims != 1 || t.shape[0] != n || (n > 1 && t.stride[0] != 1))
@@ -121,7 +144,7 @@ bool vector(PyObject* o, Tensor& t, int64_t n, int type, const char* where, cons
 }
 
 // [rows, heads, dim] of one type, contiguous in its last dimension.
-bool heads(PyObject* o, Tensor& t, int64_t rows, int64_t n, int64_t dim, int type, const char* where, const char* name) {
+bool heads(PyObject* o, Tensor& t, int64_t rows, int64_t n, int64_t dim, int type, Call& where, const char* name) {
     if (!read(o, t, where, name)) return false;
     if (t.type > kE4m3 || (type >= 0 && t.type != type)) return refuse(where, name, "has a type that the call does not take");
     if (t.dims != 3 || (rows >= 0 && t.shape[0] != rows) || t.shape[1] != n || t.shape[2] != dim)
@@ -132,17 +155,20 @@ bool heads(PyObject* o, Tensor& t, int64_t rows, int64_t n, int64_t dim, int typ
 
 // ---- other arguments --------------------------------------------------------------
 
-// cudaStream_t: a torch stream, an integer, or None for torch's current stream of `on`'s device.
-bool stream_of(PyObject* o, PyObject* on, void*& out) {
+// cudaStream_t: a torch stream of the call's device, an integer, or None for torch's current
+// stream of that device.
+bool stream_of(PyObject* o, Call& c, void*& out) {
     PyObject* r;
     if (!given(o)) {
-        PyObject* d = PyObject_CallMethodNoArgs(on, s_get_device);
+        PyObject* d = PyLong_FromLong(c.device);
         if (!d) return false;
         r = PyObject_CallOneArg(g_raw_stream, d);
         Py_DECREF(d);
     } else if (PyLong_Check(o)) {
         r = Py_NewRef(o);
     } else {
+        int device = -1;
+        if (!small_int(PyObject_GetAttr(o, s_device_index), device) || !on_device(c, device, "stream")) return false;
         r = PyObject_GetAttr(o, s_cuda_stream);
     }
     if (!r) return false;
@@ -195,33 +221,35 @@ bool integer(PyObject* o, int& v) {
     return true;
 }
 
-// handle, q_heads, kv_heads, head_dim of a KvCache
+// handle, q_heads, kv_heads, head_dim and device of a KvCache
 struct Cache {
     moe_kv* kv = nullptr;
     int64_t q_heads = 0, kv_heads = 0, dim = 0;
 };
-bool cache_of(PyObject* o, Cache& c, const char* where) {
+bool cache_of(PyObject* o, Cache& c, Call& where) {
     PyObject* t = PyObject_GetAttr(o, s_call);
     if (!t) return false;
-    const bool ok = PyTuple_Check(t) && PyTuple_GET_SIZE(t) == 4;
+    const bool ok = PyTuple_Check(t) && PyTuple_GET_SIZE(t) == 5;
+    int device = -1;
     if (ok) {
         c.kv = static_cast<moe_kv*>(PyLong_AsVoidPtr(PyTuple_GET_ITEM(t, 0)));
         c.q_heads = PyLong_AsLongLong(PyTuple_GET_ITEM(t, 1));
         c.kv_heads = PyLong_AsLongLong(PyTuple_GET_ITEM(t, 2));
         c.dim = PyLong_AsLongLong(PyTuple_GET_ITEM(t, 3));
+        device = (int)PyLong_AsLong(PyTuple_GET_ITEM(t, 4));
     }
     Py_DECREF(t);
     if (!ok) return refuse(where, "the cache", "is closed");
-    return !PyErr_Occurred();
+    return !PyErr_Occurred() && on_device(where, device, "the cache");
 }
 
 // ---- the operators ------------------------------------------------------------------
 
 PyObject* n_norm[8];
 PyObject* py_norm(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
-    const char* w = "moe_add_rms_norm";
+    Call w{"moe_add_rms_norm"};
     PyObject* v[8];  // x, weight, y, residual, sum_out, scale, eps, stream
-    if (!arguments(args, n, kw, w, n_norm, 3, v)) return nullptr;
+    if (!arguments(args, n, kw, w.name, n_norm, 3, v)) return nullptr;
     Tensor x, y, wt, r, s, sc;
     double eps = 1e-6;
     void* st = nullptr;
@@ -233,19 +261,19 @@ PyObject* py_norm(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) 
     if (given(v[4]) && !matrix(v[4], s, T, H, w, "sum_out")) return nullptr;
     if (given(v[3]) && given(v[4]) && r.type != s.type) return refuse(w, "sum_out", "has another type than residual"), nullptr;
     if (given(v[5]) && !vector(v[5], sc, T, kF32, w, "scale")) return nullptr;
-    if (!number(v[6], eps) || !stream_of(v[7], v[0], st)) return nullptr;
+    if (!number(v[6], eps) || !stream_of(v[7], w, st)) return nullptr;
     if (T > INT32_MAX || H > INT32_MAX) return refuse(w, "x", "is too large"), nullptr;
     return finish(f_norm(x.ptr, x.type, x.stride[0], r.ptr, given(v[3]) ? r.type : s.type, r.stride[0], wt.ptr, wt.type,
                          (float)eps, (int)T, (int)H, s.ptr, s.stride[0], y.ptr, y.type, y.stride[0],
                          static_cast<float*>(sc.ptr), st),
-                  w);
+                  w.name);
 }
 
 PyObject* n_append[10];
 PyObject* py_append(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
-    const char* w = "moe_kv_append";
+    Call w{"moe_kv_append"};
     PyObject* v[10];  // kv, q, k, v, positions, slots, cos_sin, q_out, interleaved, stream
-    if (!arguments(args, n, kw, w, n_append, 8, v)) return nullptr;
+    if (!arguments(args, n, kw, w.name, n_append, 8, v)) return nullptr;
     Cache c;
     Tensor q, k, x, o, pos, slots, cs;
     void* st = nullptr;
@@ -261,20 +289,20 @@ PyObject* py_append(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw
         if (!vector(v[4], pos, T, kI32, w, "positions")) return nullptr;
     }
     const int turn = given(v[8]) ? PyObject_IsTrue(v[8]) : 0;
-    if (turn < 0 || !stream_of(v[9], v[1], st)) return nullptr;
+    if (turn < 0 || !stream_of(v[9], w, st)) return nullptr;
     if (T > INT32_MAX || cs.shape[1] > 1024) return refuse(w, "q or cos_sin", "is too large"), nullptr;
     return finish(f_append(c.kv, q.type, q.ptr, q.stride[0], q.stride[1], k.ptr, k.stride[0], k.stride[1], x.ptr,
                            x.stride[0], x.stride[1], static_cast<int32_t*>(pos.ptr), static_cast<int64_t*>(slots.ptr),
                            static_cast<float*>(cs.ptr), (int)cs.shape[0], (int)cs.shape[1], turn, (int)T, o.ptr,
                            o.stride[0], o.stride[1], st),
-                  w);
+                  w.name);
 }
 
 PyObject* n_attend[9];
 PyObject* py_attend(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
-    const char* w = "moe_kv_attend";
+    Call w{"moe_kv_attend"};
     PyObject* v[9];  // kv, q, page_table, lengths, out, scale, window, lse, stream
-    if (!arguments(args, n, kw, w, n_attend, 5, v)) return nullptr;
+    if (!arguments(args, n, kw, w.name, n_attend, 5, v)) return nullptr;
     Cache c;
     Tensor q, o, table, len, lse;
     int window = 0;
@@ -299,20 +327,20 @@ PyObject* py_attend(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw
     } else {
         scale = 1.0 / __builtin_sqrt((double)c.dim);
     }
-    if (!integer(v[6], window) || !stream_of(v[8], v[1], st)) return nullptr;
+    if (!integer(v[6], window) || !stream_of(v[8], w, st)) return nullptr;
     if (B > INT32_MAX) return refuse(w, "q", "is too large"), nullptr;
     return finish(f_attend(c.kv, q.ptr, q.type, q.stride[0], q.stride[1], static_cast<int32_t*>(table.ptr),
                            table.stride[0], (int)table.shape[1], static_cast<int32_t*>(len.ptr), (int)B, (float)scale,
                            window, o.ptr, o.stride[0], o.stride[1], static_cast<float*>(lse.ptr), st),
-                  w);
+                  w.name);
 }
 
 PyObject* n_linear[10];
 PyObject* g_acts[4];  // "none", "relu", "silu", "gelu"
 PyObject* py_linear(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
-    const char* f = "moe_linear";
+    Call f{"moe_linear"};
     PyObject* v[10];  // x, w, y, bias, act, residual, x_scale, w_scale, status, stream
-    if (!arguments(args, n, kw, f, n_linear, 3, v)) return nullptr;
+    if (!arguments(args, n, kw, f.name, n_linear, 3, v)) return nullptr;
     Tensor x, w, y, b, r, xs, ws, status;
     void* st = nullptr;
     if (!matrix(v[0], x, -1, 0, f, "x") || !matrix(v[1], w, -1, 0, f, "w")) return nullptr;
@@ -334,18 +362,19 @@ PyObject* py_linear(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw
     if (given(v[6]) && !vector(v[6], xs, T, kF32, f, "x_scale")) return nullptr;
     if (given(v[7]) && !vector(v[7], ws, N, kF32, f, "w_scale")) return nullptr;
     if (given(v[8]) && !vector(v[8], status, 1, kI32, f, "status")) return nullptr;
-    if (!stream_of(v[9], v[0], st)) return nullptr;
+    if (!stream_of(v[9], f, st)) return nullptr;
     if (T > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return refuse(f, "x or w", "is too large"), nullptr;
     return finish(f_linear(x.ptr, x.stride[0], w.ptr, w.stride[0], x.type, (int)T, (int)N, (int)K,
                            static_cast<float*>(xs.ptr), static_cast<float*>(ws.ptr), b.ptr, b.type, act, r.ptr,
                            r.stride[0], y.ptr, y.type, y.stride[0], static_cast<int*>(status.ptr), st),
-                  f);
+                  f.name);
 }
 
-// bind(MoeError, raw_stream, (six dtypes), (four addresses))
+// bind(MoeError, raw_stream, current_device, (six dtypes), (four addresses))
 PyObject* py_bind(PyObject*, PyObject* args) {
-    PyObject *error, *raw, *types, *addr;
-    if (!PyArg_ParseTuple(args, "OOO!O!", &error, &raw, &PyTuple_Type, &types, &PyTuple_Type, &addr)) return nullptr;
+    PyObject *error, *raw, *current, *types, *addr;
+    if (!PyArg_ParseTuple(args, "OOOO!O!", &error, &raw, &current, &PyTuple_Type, &types, &PyTuple_Type, &addr))
+        return nullptr;
     if (PyTuple_GET_SIZE(types) != kTypes || PyTuple_GET_SIZE(addr) != 4) {
         PyErr_SetString(PyExc_ValueError, "six types and four addresses");
         return nullptr;
@@ -355,6 +384,7 @@ PyObject* py_bind(PyObject*, PyObject* args) {
     if (PyErr_Occurred()) return nullptr;
     g_error = Py_NewRef(error);
     g_raw_stream = Py_NewRef(raw);
+    g_current = Py_NewRef(current);
     for (int i = 0; i < kTypes; ++i) g_types[i] = Py_NewRef(PyTuple_GET_ITEM(types, i));
     f_norm = reinterpret_cast<decltype(f_norm)>(p[0]);
     f_append = reinterpret_cast<decltype(f_append)>(p[1]);
@@ -412,7 +442,7 @@ bool intern(PyObject* (&out)[N], const char* const (&names)[N]) {
 
 PyMODINIT_FUNC PyInit__decoder_ops() {
     PyObject* attr[8];
-    if (!intern(attr, {"dtype", "shape", "stride", "data_ptr", "is_cuda", "get_device", "cuda_stream", "_call"}) ||
+    if (!intern(attr, {"dtype", "shape", "stride", "data_ptr", "get_device", "device_index", "cuda_stream", "_call"}) ||
         !intern(n_norm, {"x", "weight", "y", "residual", "sum_out", "scale", "eps", "stream"}) ||
         !intern(n_append, {"kv", "q", "k", "v", "positions", "slots", "cos_sin", "q_out", "interleaved", "stream"}) ||
         !intern(n_attend, {"kv", "q", "page_table", "lengths", "out", "scale", "window", "lse", "stream"}) ||
@@ -420,6 +450,6 @@ PyMODINIT_FUNC PyInit__decoder_ops() {
         !intern(g_acts, {"none", "relu", "silu", "gelu"}))
         return nullptr;
     s_dtype = attr[0], s_shape = attr[1], s_stride = attr[2], s_data_ptr = attr[3];
-    s_is_cuda = attr[4], s_get_device = attr[5], s_cuda_stream = attr[6], s_call = attr[7];
+    s_get_device = attr[4], s_device_index = attr[5], s_cuda_stream = attr[6], s_call = attr[7];
     return PyModule_Create(&module);
 }

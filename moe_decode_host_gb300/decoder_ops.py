@@ -22,9 +22,16 @@ from ._lib import MOE_ERR_INVALID_ARG, MoeError, check, lib, moe_kv_params
 
 _TYPES = (torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn)  # MOE_BF16 .. MOE_E4M3
 
-_decoder_ops.bind(MoeError, torch._C._cuda_getCurrentRawStream, _TYPES + (torch.int32, torch.int64),
-                  tuple(ctypes.cast(f, ctypes.c_void_p).value
-                        for f in (lib.moe_add_rms_norm, lib.moe_kv_append, lib.moe_kv_attend, lib.moe_linear)))
+# the C entry points that the binding calls
+_CALLS = tuple(ctypes.cast(f, ctypes.c_void_p).value
+               for f in (lib.moe_add_rms_norm, lib.moe_kv_append, lib.moe_kv_attend, lib.moe_linear))
+
+
+def _bind(raw_stream=torch._C._cuda_getCurrentRawStream, current_device=torch._C._cuda_getDevice, calls=_CALLS):
+    _decoder_ops.bind(MoeError, raw_stream, current_device, _TYPES + (torch.int32, torch.int64), calls)
+
+
+_bind()
 
 moe_add_rms_norm = _decoder_ops.moe_add_rms_norm
 moe_kv_append = _decoder_ops.moe_kv_append
@@ -53,6 +60,12 @@ class KvCache:
             refuse("k and v are not [n_pages, page_size, kv_heads, head_dim] with one set of strides")
         if not k.is_cuda or not v.is_cuda or k.stride(3) != 1:
             refuse("k and v are not on a GPU or not contiguous in their last dimension")
+        # the handle's workspace is on the current device, and its calls run there
+        device = k.get_device()
+        if device != torch._C._cuda_getDevice():
+            refuse("k is not on the current GPU")
+        if any(t is not None and t.get_device() != device for t in (v, k_scale, v_scale)):
+            refuse("its tensors are not on one GPU")
         n_pages, page, kv_heads, dim = k.shape
         for s in (k_scale, v_scale):
             if s is not None and (s.dtype != torch.float32 or not s.is_cuda or s.shape != (kv_heads,)
@@ -65,7 +78,7 @@ class KvCache:
                                 0 if k_scale is None else k_scale.data_ptr(),
                                 0 if v_scale is None else v_scale.data_ptr(), ctypes.byref(h)), w)
         self.handle = h
-        self._call = (h.value, q_heads, kv_heads, dim)  # what the calls read
+        self._call = (h.value, q_heads, kv_heads, dim, device)  # what the calls read
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, dim
         self.page_size, self.n_pages, self.max_batch = page, n_pages, max_batch
