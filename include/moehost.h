@@ -386,7 +386,9 @@ int moe_quant_mxfp4(const void* x_bf16, int rows, int K, uint8_t* nib, uint8_t* 
  *            residual or x themselves (same rows, type and stride).
  *  y         device [T][H] of y_type, rows y_stride apart; may be x itself likewise.
  *            MOE_E4M3: y holds y / y_scale[t] with y_scale[t] = max(max_j |y_tj| / 448,
- *            2^-126); a row with a NaN or an infinite square gets a NaN scale.
+ *            2^-126); a row with a NaN in s * weight, or with a sum of squares past fp32's
+ *            range, gets a NaN scale and NaN codes.  In the other types such a sum (elements
+ *            from about 2^64 / sqrt(H) up) leaves zeros, and NaN where s is infinite.
  *  y_scale   device fp32 [T], MOE_E4M3 only (else NULL).
  * 1 <= H <= 32768, eps finite and >= 0; T = 0 is valid.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */

@@ -35,6 +35,13 @@ __device__ __forceinline__ void cp_wait(int left) {  // until at most `left` gro
     }
 }
 
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // A row is handled by blockDim.x threads (whole warps) with NV runs of VEC elements each,
 // blockDim.y rows a CTA at a time.  A CTA walks rows gridDim.x * blockDim.y apart; the next
 // row's loads are issued before the current row is reduced, so that reads stay in flight
@@ -163,14 +170,14 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a, int sta
                 }
                 if (yt == MOE_E4M3) {
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) top = fmaxf(top, fabsf(s[n][i]));
+                    for (int i = 0; i < VEC; ++i) top = max_nan(top, fabsf(s[n][i]));
                 }
             }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (yt == MOE_E4M3) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (yt == MOE_E4M3) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
         }
         if (warps > 1) {
             // two sets of partials: the next round's writes meet no reader of this round's
@@ -185,17 +192,20 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a, int sta
 #pragma unroll
             for (int o = kMost / 2; o > 0; o >>= 1) {
                 ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                if (yt == MOE_E4M3) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                if (yt == MOE_E4M3) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
             }
         }
         if (!live) continue;
-        float f = rsqrtf(fmaf(ss, a.inv_h, a.eps));
+        const float square = fmaf(ss, a.inv_h, a.eps);
+        float f = rsqrtf(square);
         if (yt == MOE_E4M3) {
-            // a row with a NaN or an infinity gets a NaN scale (fmaxf alone would hide it)
-            const float m = top * f;
-            const float scale = m == m && f == f ? fmaxf(m * (1.f / kE4M3Max), 1.17549435e-38f) : __uint_as_float(0x7fc00000u);
+            // a NaN anywhere, or a square past fp32 (f would be 0): a NaN scale and NaN codes
+            const float m = square < INFINITY ? top * f : __uint_as_float(0x7fc00000u);
+            const float scale = m == m ? fmaxf(m * (1.f / kE4M3Max), 1.17549435e-38f) : m;
             if (threadIdx.x == 0) a.scale[row] = scale;
-            if (top > 1e-30f) {
+            if (m != m) {
+                f = m;
+            } else if (top > 1e-30f) {
                 f = kE4M3Max / top;  // = f / scale
             } else {  // f / scale could overflow: the row is multiplied by both
                 const float inv = 1.f / scale;  // finite, as scale >= 2^-126

@@ -1,0 +1,54 @@
+"""The decoder-layer operators at the ends of their ranges, against plain 64-bit forms.
+
+Bounds are derived as in test_gpu_decoder_ops.py, whose helpers are used here."""
+import math
+
+import pytest
+import torch
+
+from test_gpu_decoder_ops import (BF16, E4M3, F16, F32, SUB, U, attend64, e4m3_tol, gen, m, make_cache,  # noqa: F401
+                                  norm64, randn, within)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- norm ---------------------------------------------------------------------
+
+
+def norm8(m, x, w, eps=1e-6):
+    y, sc = torch.empty(x.shape, dtype=E4M3, device="cuda"), torch.empty(x.shape[0], device="cuda")
+    m.moe_add_rms_norm(x, w, y, scale=sc, eps=eps)
+    return y.float(), sc
+
+
+@pytest.mark.parametrize("H", [64, 200, 4096, 4097])
+@pytest.mark.parametrize("xt", [F32, BF16])
+def test_norm_square_past_fp32(m, H, xt):
+    """A finite row whose squares overflow: a NaN scale in E4M3, zeros in the other types, and no
+    other row touched."""
+    x = randn(gen(H), 5, H).to(xt)
+    clean8, cleans = norm8(m, x, None)
+    clean = torch.empty_like(x)
+    m.moe_add_rms_norm(x, None, clean)
+    x[1] = 1e20  # every square overflows
+    x[3, H // 2] = 3e19  # one does
+    y8, sc = norm8(m, x, None)
+    assert sc[1].isnan() and sc[3].isnan() and y8[1].isnan().all() and y8[3].isnan().all()
+    assert torch.equal(sc[[0, 2, 4]], cleans[[0, 2, 4]]) and torch.equal(y8[[0, 2, 4]], clean8[[0, 2, 4]])
+    y = torch.empty_like(x)
+    m.moe_add_rms_norm(x, None, y)
+    assert (y[[1, 3]] == 0).all() and torch.equal(y[[0, 2, 4]], clean[[0, 2, 4]])
+
+
+@pytest.mark.parametrize("H", [64, 200, 4096, 4097])
+def test_norm_nan_of_a_weight(m, H):
+    """A NaN that the weights bring, or an infinity times a zero weight, reaches the scale of every
+    row that it is in."""
+    x, w = randn(gen(H), 3, H), torch.ones(H, device="cuda")
+    w[H - 1] = float("nan")
+    y8, sc = norm8(m, x, w)
+    assert sc.isnan().all() and y8.isnan().all()
+    w[H - 1] = 0.0
+    x[1, H - 1] = float("inf")
+    y8, sc = norm8(m, x, w)
+    assert sc[1].isnan() and y8[1].isnan().all() and sc[[0, 2]].isfinite().all() and (y8[[0, 2], H - 1] == 0).all()
