@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a, int sta
         }
         if (!live) continue;
         const float square = fmaf(ss, a.inv_h, a.eps);
-        float f = rsqrtf(square);
+        float f = rsqrtf(square), after = 1.f;
         if (yt == MOE_E4M3) {
             // a NaN anywhere, or a square past fp32 (f would be 0): a NaN scale and NaN codes
             const float m = square < INFINITY ? top * f : __uint_as_float(0x7fc00000u);
@@ -205,20 +205,22 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a, int sta
             if (threadIdx.x == 0) a.scale[row] = scale;
             if (m != m) {
                 f = m;
-            } else if (top > 1e-30f) {
-                f = kE4M3Max / top;  // = f / scale
-            } else {  // f / scale could overflow: the row is multiplied by both
-                const float inv = 1.f / scale;  // finite, as scale >= 2^-126
-#pragma unroll
-                for (int n = 0; n < NV; ++n)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) s[n][i] *= inv;
+            } else if (top > 1e-30f && scale > 1.17549435e-38f) {
+                f = kE4M3Max / top;  // = f / scale: one factor
+            } else {
+                after = 1.f / scale;  // finite, as scale >= 2^-126
             }
         }
 #pragma unroll
         for (int n = 0; n < NV; ++n)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) s[n][i] *= f;
+        if (yt == MOE_E4M3 && after != 1.f) {  // f / scale may be past fp32: y first, then over the scale
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) s[n][i] *= after;
+        }
 #pragma unroll
         for (int n = 0; n < NV; ++n)
             if (in(n)) store_run<VEC>(py, n * de, yt, s[n]);

@@ -52,3 +52,18 @@ def test_norm_nan_of_a_weight(m, H):
     x[1, H - 1] = float("inf")
     y8, sc = norm8(m, x, w)
     assert sc[1].isnan() and y8[1].isnan().all() and sc[[0, 2]].isfinite().all() and (y8[[0, 2], H - 1] == 0).all()
+
+
+@pytest.mark.parametrize("H", [64, 200, 4096, 4097])
+@pytest.mark.parametrize("xt", [F32, BF16])
+@pytest.mark.parametrize("size,weight,eps", [(1e8, 1e-37, 1e-6), (1.0, 1e-22, 1e30), (1.0, 1e-34, 1e-6), (1e-31, 1.0, 1e12)])
+def test_norm_scale_held_at_its_least(m, H, xt, size, weight, eps):
+    """Rows whose largest |y| / 448 is below 2^-126: the scale stays there and the codes are y over
+    that scale (y stays normal or loses less than E4M3 does: 2^-149 against half of 2^-9 2^-126)."""
+    x = (size * (0.5 + torch.rand(4, H, generator=gen(H), device="cuda"))).to(xt)
+    w = (weight * (0.1 + torch.rand(H, generator=gen(H + 1), device="cuda"))).to(xt)
+    y64 = norm64(x, None, w, eps)[1]
+    s = (y64.abs().amax(1) / 448).clamp(min=2.0 ** -126)
+    y8, sc = norm8(m, x, w, eps)
+    within(sc, s, s * 8e-6, "scale")
+    within(y8, y64 / s[:, None], e4m3_tol(y64 / s[:, None]) + 2.0 ** -22, "codes")
