@@ -627,8 +627,9 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
             float top = -INFINITY, sum = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][tid]);
+            // a warp with no maximum has seen nothing (sum 0) or NaN alone (sum NaN, which has to stay)
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) sum += s_m[w][tid] == -INFINITY ? 0.f : s_l[w][tid] * fast_exp2(s_m[w][tid] - top);
+            for (int w = 0; w < kWarps; ++w) sum += s_l[w][tid] * part_weight(s_m[w][tid], top);
             if (whole) {
                 s_inv[tid] = v_scale / sum;
                 if (!(sum != 0.f)) s_inv[tid] = 0.f;

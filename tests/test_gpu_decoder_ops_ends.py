@@ -67,3 +67,38 @@ def test_norm_scale_held_at_its_least(m, H, xt, size, weight, eps):
     y8, sc = norm8(m, x, w, eps)
     within(sc, s, s * 8e-6, "scale")
     within(y8, y64 / s[:, None], e4m3_tol(y64 / s[:, None]) + 2.0 ** -22, "codes")
+
+
+# ---- attend -------------------------------------------------------------------
+
+
+def attend(m, q, k, v, ks, vs, pages, lens, **kw):
+    kv = m.KvCache(k, v, q_heads=q.shape[1], max_batch=len(lens), k_scale=ks, v_scale=vs)
+    o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    m.moe_kv_attend(kv, q, pages, torch.tensor(lens, dtype=torch.int32, device="cuda"), o, lse=lse, **kw)
+    assert kv.status() == 0
+    return o, lse
+
+
+@pytest.mark.parametrize("ct", [BF16, F16, E4M3])
+@pytest.mark.parametrize("lens,where", [([1, 5], 0), ([40, 7], 20), ([300, 300], 299), ([300, 20], 70), ([6000, 100], 4321)])
+def test_attend_nan_keys_reach_the_log_sum(m, ct, lens, where):
+    """One NaN among the keys of a head: that head's outputs and log-sums are NaN, wherever the token
+    lies in the split; a NaN query likewise.  The others stay as they were."""
+    g = gen(32)
+    qt = F16 if ct == F16 else BF16
+    k, v, ks, vs, pages = make_cache(g, lens, 16, 2, 64, ct)
+    q = randn(g, 2, 6, 64).to(qt)
+    o, lse = attend(m, q, k, v, ks, vs, pages, lens)
+    page, e = int(pages[0, where // 16]), where % 16
+    kb = k.float()
+    kb[page, e, 1, 7] = float("nan")
+    o2, lse2 = attend(m, q, kb.to(ct), v, ks, vs, pages, lens)
+    assert o2[0, 3:].isnan().all() and lse2[0, 3:].isnan().all()
+    assert torch.equal(o2[0, :3], o[0, :3]) and torch.equal(lse2[0, :3], lse[0, :3])
+    assert torch.equal(o2[1], o[1]) and torch.equal(lse2[1], lse[1])
+    q[0, 2, 63] = float("nan")
+    o3, lse3 = attend(m, q, k, v, ks, vs, pages, lens)
+    assert o3[0, 2].isnan().all() and lse3[0, 2].isnan()
+    rest = [0, 1, 3, 4, 5]
+    assert torch.equal(o3[0, rest], o[0, rest]) and torch.equal(lse3[0, rest], lse[0, rest])
