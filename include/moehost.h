@@ -401,7 +401,7 @@ int moe_add_rms_norm(const void* x, int x_type, int64_t x_stride, const void* re
  *   k_cache[(s / page_size) * page_stride + (s % page_size) * token_stride + h * head_stride + d]
  * and of v_cache likewise, so both orders of tokens and heads within a page fit.
  *  type       MOE_BF16, MOE_F16, or MOE_E4M3 with one fp32 scale per key head (value =
- *             scale * code).
+ *             scale * code; the scale may have either sign).
  *  q_heads    a multiple of kv_heads; query head h reads key head
  *             h / (q_heads / kv_heads).
  *  head_dim   a multiple of 16, at most 256.

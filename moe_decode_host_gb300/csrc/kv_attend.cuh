@@ -389,8 +389,10 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                 for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 e = prescale_exp(top);
             }
-            // a negative scale is folded into q, so that the largest raw score is the largest score
-            const float down = copysignf(F8 ? pow2i(-e) : 1.f, a.scale);
+            // the sign of the scores' factor is folded into q, so that the largest raw score is the
+            // largest score
+            const float factor = a.scale * kLog2e * k_scale;
+            const float down = copysignf(F8 ? pow2i(-e) : 1.f, factor);
 #pragma unroll
             for (int i = 0; i < DP / 32; ++i) {
                 const int d = lane + 32 * i;
@@ -398,8 +400,9 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                     reinterpret_cast<uint16_t*>(s_q + h * qpitch)[d] =
                         (uint16_t)(BF ? pack_bf16(v[i] * down, 0.f) : pack_f16(v[i] * down, 0.f));
             }
-            // never zero: a score left out (-inf) must stay -inf under it
-            if (lane == 0) s_scale[h] = fmaxf(fabsf(a.scale) * kLog2e * k_scale * (F8 ? pow2i(e) : 1.f), 1e-37f);
+            // never zero: a score left out (-inf) must stay -inf under it.  NaN stays NaN
+            const float up = fabsf(factor) * (F8 ? pow2i(e) : 1.f);
+            if (lane == 0) s_scale[h] = up < 1e-37f ? 1e-37f : up;
         }
         __syncthreads();
 

@@ -80,6 +80,28 @@ def attend(m, q, k, v, ks, vs, pages, lens, **kw):
     return o, lse
 
 
+@pytest.mark.parametrize("qt", [BF16, F16])
+@pytest.mark.parametrize("scale", [0.125, -0.25])
+def test_attend_signed_scales(m, qt, scale):
+    """A cache's value is scale * code whatever the scale's sign, and a NaN scale spoils its heads."""
+    g = gen(31)
+    lens = [1, 40, 0, 700, 3000]
+    k, v, ks, vs, pages = make_cache(g, lens, 16, 4, 64, E4M3)
+    ks[1], vs[2] = -ks[1], -vs[2]
+    ks[3], vs[3] = -ks[3], -vs[3]
+    q = randn(g, len(lens), 12, 64).to(qt)
+    o, lse = attend(m, q, k, v, ks, vs, pages, lens, scale=scale)
+    o64, l64, ot, lt = attend64(q, k, v, ks, vs, pages, lens, scale, 0)
+    within(o, o64, ot, "out")
+    within(lse, l64, lt, "lse")
+    ks[1] = float("nan")
+    o2, lse2 = attend(m, q, k, v, ks, vs, pages, lens, scale=scale)
+    some = torch.tensor([n > 0 for n in lens], device="cuda")
+    assert o2[some, 3:6].isnan().all() and lse2[some, 3:6].isnan().all()
+    keep = [0, 1, 2, 6, 7, 8, 9, 10, 11]
+    assert torch.equal(o2[:, keep], o[:, keep]) and torch.equal(lse2[:, keep], lse[:, keep])
+
+
 @pytest.mark.parametrize("ct", [BF16, F16, E4M3])
 @pytest.mark.parametrize("lens,where", [([1, 5], 0), ([40, 7], 20), ([300, 300], 299), ([300, 20], 70), ([6000, 100], 4321)])
 def test_attend_nan_keys_reach_the_log_sum(m, ct, lens, where):
