@@ -29,7 +29,10 @@ constexpr int kStart = 12;
 // 10 to 380 9.3 and 8.8).
 constexpr int kWhole = 20;
 constexpr int64_t kMaxTokens = 1 << 30;  // of a sequence: token indexes stay in 32 bits
-constexpr float kSlack = 8.f;    // weights stay below 2^8: far from f16's range, and as precise
+constexpr float kSlack = 8.f;    // of the maximum over its reference, in powers of two
+// f16 weights are kept 2^kLift larger than the softmax has them, up to 2^14: what f16 can no longer
+// hold is then below 2^-31 of the largest.  (Unlifted, 2^18 weights of 2^-25 beside one of 1 vanish.)
+constexpr float kLift = 6.f;
 constexpr float kLog2e = 1.44269504f;
 constexpr float kLn2 = 0.69314718f;
 

@@ -158,6 +158,7 @@ template <int T, int DP, int NT, bool EXACT>
 __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
     attend_kernel(const AttendArgs a, const AttendPlan p) {
     constexpr bool BF = T == 0, F8 = T == 2;
+    constexpr float lift = BF ? 0.f : kLift;
     constexpr int HC = 8 * NT;
     constexpr int ES = F8 ? 1 : 2;
     constexpr int U = unit_tokens(DP * ES), MT = U / 16;  // tokens of a unit, in tiles of 16
@@ -508,12 +509,12 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    // the reference moves only when weights would pass 2^kSlack: any reference near the
+                    // the reference moves only when weights would pass 2^(kSlack + lift): any reference near the
                     // maximum does, and moving it costs a pass over the sums
                     const bool move = (top - m[t][j]) * sc[t][j] > kSlack;  // false where nothing was seen yet
                     const float mn = move ? top : m[t][j];
-                    const float ref = mn == -INFINITY ? 0.f : mn * sc[t][j];  // then every weight is 0
-                    keep[t][j] = move ? fast_exp2(fmaf(m[t][j], sc[t][j], -ref)) : 1.f;
+                    const float ref = mn == -INFINITY ? 0.f : fmaf(mn, sc[t][j], -lift);  // then every weight is 0
+                    keep[t][j] = move ? fast_exp2(fmaf(m[t][j], sc[t][j], -ref) - lift) : 1.f;
                     grown |= move;
                     m[t][j] = mn;
                     float sum = 0.f;
@@ -574,12 +575,12 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
             }
             __syncwarp();
         }
-        // maxima of scores from here on, in powers of two
+        // maxima of scores from here on, in powers of two, less the lift
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                if (m[t][j] != -INFINITY) m[t][j] *= sc[t][j];
+                if (m[t][j] != -INFINITY) m[t][j] = fmaf(m[t][j], sc[t][j], -lift);
 
         // ---- join the warps ----
 #pragma unroll

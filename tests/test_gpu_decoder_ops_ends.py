@@ -124,3 +124,27 @@ def test_attend_nan_keys_reach_the_log_sum(m, ct, lens, where):
     assert o3[0, 2].isnan().all() and lse3[0, 2].isnan()
     rest = [0, 1, 3, 4, 5]
     assert torch.equal(o3[0, rest], o[0, rest]) and torch.equal(lse3[0, rest], lse[0, rest])
+
+
+@pytest.mark.parametrize("ct,qt", [(F16, F16), (E4M3, F16), (BF16, BF16)])
+def test_attend_many_small_weights(m, ct, qt):
+    """One key outweighs each of the others by e^17.5 = 2^25.3, and there are 2^18 others, whose
+    values alone are not zero: together they are 0.6% of the weight and all of the output."""
+    n, B = (1 << 18) + 1, 512  # more sequences than blocks: a block walks a whole sequence
+    page = 4096
+    n_pages = -(-n // page)
+    k = torch.zeros(n_pages, page, 1, 64, device="cuda")
+    v = torch.ones_like(k)
+    k[0, 0, 0, 0], v[0, 0] = 17.5, 0.0
+    ks = vs = torch.ones(1, device="cuda") if ct == E4M3 else None
+    if ct == E4M3:
+        k[0, 0, 0, 0] = 16.0
+        k[0, 0, 0, 1] = 1.5
+    q = torch.zeros(1, 1, 64, device="cuda")
+    q[..., :2] = 1.0
+    pages = torch.arange(n_pages, dtype=torch.int32, device="cuda")[None]
+    k, v, q = k.to(ct), v.to(ct), q.to(qt)
+    o, lse = attend(m, q.expand(B, 1, 64).contiguous(), k, v, ks, vs, pages.expand(B, -1), [n] * B, scale=1.0)
+    o64, l64, ot, lt = attend64(q, k, v, ks, vs, pages, [n], 1.0, 0)
+    within(o, o64.expand(B, 1, 64), ot.expand(B, 1, 64), "out")
+    within(lse, l64.expand(B, 1), lt.expand(B, 1), "lse")
