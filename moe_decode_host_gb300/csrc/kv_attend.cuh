@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
             }
             float keep[NT][2];
             bool grown = false;
-            uint32_t pb[MT][NT][2];
+            uint32_t pb[MT][NT][2][2];  // two terms
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -526,13 +526,21 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                     }
                     l[t][j] = fmaf(l[t][j], keep[t][j], sum);
                 }
-                // the weights are rounded to the values' 16-bit type for the tensor cores (bf16 adds
-                // about as much error as the output's own rounding; f16 an eighth of it); their sum is not
+                // a weight goes to the tensor cores as two terms of the values' 16-bit type, the nearest and
+                // its remainder (2^-16 of the weight are lost with bf16, 2^-22 with f16): one term alone added
+                // as much error as the output's rounding and, where one key outweighs the rest, took its own
+                // rounding into every output (32 ragged 172.6 us with one term, 173.5 with two)
+                auto pack = [](float x, float y) { return BF ? pack_bf16(x, y) : pack_f16(x, y); };
+                auto low = [](uint32_t p) { return half_bits_to_f32(p & 0xffffu, BF ? MOE_BF16 : MOE_F16); };
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    pb[i][t][0] = transpose8x8(BF ? pack_bf16(s[i][t][0], s[i][t][1]) : pack_f16(s[i][t][0], s[i][t][1]));
-                    pb[i][t][1] = transpose8x8(BF ? pack_bf16(s[i][t][2], s[i][t][3]) : pack_f16(s[i][t][2], s[i][t][3]));
-                }
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float x = s[i][t][2 * j], y = s[i][t][2 * j + 1];
+                        const uint32_t p = pack(x, y);
+                        pb[i][t][0][j] = transpose8x8(p);
+                        pb[i][t][1][j] = transpose8x8(pack(x - low(p), y - low(p >> 16)));
+                    }
             }
             if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
@@ -556,7 +564,9 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                                     const uint32_t f[4] = {e4m3_lo(r[2 * h]), e4m3_lo(r[2 * h + 1]), e4m3_hi(r[2 * h]),
                                                            e4m3_hi(r[2 * h + 1])};
 #pragma unroll
-                                    for (int t = 0; t < NT; ++t) mma16816<BF>(o[i + h][t], f, pb[k][t][0], pb[k][t][1]);
+                                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                        for (int j = 0; j < 2; ++j) mma16816<BF>(o[i + h][t], f, pb[k][t][j][0], pb[k][t][j][1]);
                                 }
                             }
                         }
@@ -568,7 +578,9 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                             uint32_t r[4];
                             ldsm4_t(r, v_at + 16 * k * pitch + (((2 * i) ^ v_x) << 4));
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) mma16816<BF>(o[i][t], r, pb[k][t][0], pb[k][t][1]);
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) mma16816<BF>(o[i][t], r, pb[k][t][j][0], pb[k][t][j][1]);
                         }
                     }
                 }

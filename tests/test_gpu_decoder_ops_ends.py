@@ -148,3 +148,40 @@ def test_attend_many_small_weights(m, ct, qt):
     o64, l64, ot, lt = attend64(q, k, v, ks, vs, pages, [n], 1.0, 0)
     within(o, o64.expand(B, 1, 64), ot.expand(B, 1, 64), "out")
     within(lse, l64.expand(B, 1), lt.expand(B, 1), "lse")
+
+
+@pytest.mark.parametrize("ct,qt", [(BF16, BF16), (F16, F16), (E4M3, BF16), (E4M3, F16)])
+def test_attend_dominant_key_after_the_first(m, ct, qt):
+    """Two keys in one warp's hands, the later one e^c times the earlier one's weight, the rest below
+    e^-24; values of one.  The outputs are one: what is left of the weights' two terms (2^-16) and
+    of fp32 sums is below half of the type's spacing under one (2^-9 for bf16; 2^-12 for f16, whose
+    weights lose 2^-22)."""
+    c = torch.linspace(3.0, 5.4, 48, device="cuda")  # below 2^8, where the softmax's reference stays
+    k, v = torch.zeros(1, 256, 1, 128, device="cuda"), torch.ones(1, 256, 1, 128, device="cuda")
+    k[0, :, 0, 0] = -8.0
+    k[0, 0], k[0, 128, 0, 0] = 0.0, 1.0
+    q = torch.zeros(48, 1, 128, device="cuda")
+    q[:, 0, 0] = c
+    one = torch.ones(1, device="cuda") if ct == E4M3 else None
+    pages = torch.zeros(48, 1, dtype=torch.int32, device="cuda")
+    o, _ = attend(m, q.to(qt), k.to(ct), v.to(ct), one, one, pages, [129] * 48, scale=1.0)
+    assert (o == 1).all(), float((o.double() - 1).abs().max())
+
+
+@pytest.mark.parametrize("ct,qt", [(BF16, BF16), (F16, F16), (E4M3, BF16), (E4M3, F16)])
+@pytest.mark.parametrize("hq,hkv,D", [(8, 2, 128), (16, 1, 64), (32, 1, 96), (2, 2, 256)])
+def test_attend_adds_little_to_the_outputs_rounding(m, ct, qt, hq, hkv, D):
+    """The bound of attend64 with the weights' two 16-bit terms in the place of one: 2^-16 of a weight
+    for bf16 caches and 2^-22 for the others."""
+    g = gen(34)
+    lens = [5000, 33, 2000, 320]
+    k, v, ks, vs, pages = make_cache(g, lens, 16, hkv, D, ct)
+    q = randn(g, len(lens), hq, D).to(qt)
+    o, _ = attend(m, q, k, v, ks, vs, pages, lens)
+    o64, _, tol, _ = attend64(q, k, v, ks, vs, pages, lens, D ** -0.5, 0)
+    own = o64.abs() * U[qt] * 1.01 + SUB[qt]
+    size = attend64(q, k, v.float().abs().to(ct), ks, vs, pages, lens, D ** -0.5, 0)[0]
+    one = U[BF16] if ct == BF16 else U[F16]
+    tol = tol - size * (one - one * one)
+    assert (tol >= own).all()
+    within(o, o64, tol)
