@@ -74,12 +74,13 @@ __device__ __forceinline__ Slot slot_of(const AppendArgs& a, int64_t slot, bool 
     return s;
 }
 
-// What head h's values are multiplied by on their way into an E4M3 cache.
-__device__ __forceinline__ float inverse_scale(const AppendArgs& a, int h) {
+// The scale of head h's values in an E4M3 cache, and what they are multiplied by on their way there.
+__device__ __forceinline__ float scale_of(const AppendArgs& a, int h) {
     int n;
     const int kind = kind_of(a, h, n);
-    return kind == 0 || a.kv.type != MOE_E4M3 ? 1.f : 1.f / (kind == 1 ? a.kv.k_scale : a.kv.v_scale)[n];
+    return kind == 0 || a.kv.type != MOE_E4M3 ? 1.f : (kind == 1 ? a.kv.k_scale : a.kv.v_scale)[n];
 }
+__device__ __forceinline__ float inverse_scale(const AppendArgs& a, int h) { return 1.f / scale_of(a, h); }
 
 // Rotates an item of head h (raw runs in r0, r1) and writes it where it belongs.
 template <int VEC, class R>
@@ -123,10 +124,19 @@ __device__ __forceinline__ void finish(const AppendArgs& a, int64_t t, int h, co
         store_run<VEC>(a.q_out, t * a.qo_ts + n * a.qo_hs + it.e1, xt, x1);
     } else {
         if (ct == MOE_E4M3) {
+            if (fabsf(inv) == INFINITY) {  // a scale below 2^-128: its inverse is past fp32, the quotients need not be
+                const float scale = scale_of(a, h);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                x0[i] *= inv;
-                x1[i] *= inv;
+                for (int i = 0; i < VEC; ++i) {
+                    x0[i] /= scale;
+                    x1[i] /= scale;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    x0[i] *= inv;
+                    x1[i] *= inv;
+                }
             }
         }
         void* cache = kind == 1 ? a.kv.k : a.kv.v;

@@ -69,6 +69,27 @@ def test_norm_scale_held_at_its_least(m, H, xt, size, weight, eps):
     within(y8, y64 / s[:, None], e4m3_tol(y64 / s[:, None]) + 2.0 ** -22, "codes")
 
 
+# ---- append -------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("D", [64, 80])  # runs of 8 through the ring, and the kernel for any rows
+def test_append_over_subnormal_scales(m, D):
+    """Scales whose inverse is past fp32: zeros stay zeros, and values are divided all the same."""
+    ks = torch.tensor([2.0 ** -130, 2.0 ** -126, 0.5], device="cuda")
+    vs = torch.tensor([2.0 ** -149, -(2.0 ** -129), 1.0], device="cuda")
+    kc, vc = (torch.ones(2, 4, 3, D, device="cuda").to(E4M3) for _ in range(2))
+    kv = m.KvCache(kc, vc, q_heads=3, max_batch=1, k_scale=ks, v_scale=vs)
+    x = torch.zeros(5, 3, D, device="cuda").to(BF16)
+    x[:, :, 1], x[:, :, 2], x[:, :, 3] = 2.0 ** -126, 3 * 2.0 ** -129, -7 * 2.0 ** -131
+    x[:, :, 4], x[:, :, 5] = 1.0, -3.0
+    raw = x if D == 64 else torch.cat([x.flatten()[:1], x.flatten()])[1:].view_as(x)  # at an odd address
+    slots = torch.arange(5, device="cuda")
+    m.moe_kv_append(kv, raw, raw, raw, None, slots, None, torch.empty_like(x))
+    for cache, scale in ((kc, ks), (vc, vs)):
+        want = (x.double() / scale.double()[:, None]).clamp(-448, 448)
+        assert torch.equal(cache.view(8, 3, D)[:5].float(), want.float().to(E4M3).float())
+
+
 # ---- attend -------------------------------------------------------------------
 
 
