@@ -206,3 +206,30 @@ def test_attend_adds_little_to_the_outputs_rounding(m, ct, qt, hq, hkv, D):
     tol = tol - size * (one - one * one)
     assert (tol >= own).all()
     within(o, o64, tol)
+
+
+# ---- linear -------------------------------------------------------------------
+
+
+def activation_points():
+    v = torch.cat([torch.linspace(-14, 14, 40001), torch.linspace(-0.01, 0.01, 4001), torch.linspace(-90, 90, 18001),
+                   torch.tensor([0.0, 1e-30, -1e-30, 1e30, -1e30, 3e38, -3e38])]).cuda()
+    return v[: v.numel() // 8 * 8]
+
+
+def as_stored(want, yt):
+    """Infinite where the output type's nearest value is."""
+    top = torch.finfo(yt).max * (1 + U[yt] / 2)
+    return torch.where(want.abs() >= top, want.sign() * math.inf, want)
+
+
+@pytest.mark.parametrize("T", [1, 300])  # the split kernel and the tiled one
+@pytest.mark.parametrize("yt", [F32, F16, BF16])
+def test_linear_gelu_everywhere(m, T, yt):
+    """v Phi(v) of the bias alone, to 2^-18 of its value in fp32 and below 2^-126 absolutely (header)."""
+    v = activation_points()
+    x, w = torch.zeros(T, 16, device="cuda").to(BF16), torch.zeros(v.numel(), 16, device="cuda").to(BF16)
+    y = torch.empty(T, v.numel(), dtype=yt, device="cuda")
+    m.moe_linear(x, w, y, bias=v, act="gelu")
+    want = (0.5 * v.double() * torch.special.erfc(-v.double() / math.sqrt(2.0))).expand(T, -1)
+    within(y, as_stored(want, yt), want.abs() * (2.0 ** -18 + U[yt]) + 2.0 ** -126 + SUB[yt])
