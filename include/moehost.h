@@ -80,8 +80,8 @@ extern "C" {
 #define MOE_F32 2
 #define MOE_E4M3 3
 
-/* Activations of moe_linear.  GELU is the exact form, v * Phi(v), computed in fp32 to 2^-18 of
- * its value (where that is a normal number) before the output is rounded. */
+/* Activations of moe_linear.  GELU is the exact form, v * Phi(v).  It is computed to 2^-18 of its
+ * value and SiLU to 2^-20 (where that is a normal fp32 number) before the output is rounded. */
 #define MOE_ACT_NONE 0
 #define MOE_ACT_RELU 1
 #define MOE_ACT_SILU 2

@@ -210,6 +210,25 @@ __device__ __forceinline__ void gelu2(float& v0, float& v1) {
     unpair(fma2(mul2(x, both(-1.f)), tail, pos), v0, v1);
 }
 
+// SiLU of two values, v / (1 + exp(-v)), by the exponential that cannot overflow: v / (1 + e) above 0
+// and v e / (1 + e) below, e = exp(-|v|) = 2^z with what z loses to rounding brought back as a
+// factor.  2^-20 of the value at most.  At 256 e has long vanished, and no infinity meets another.
+__device__ __forceinline__ void silu2(float& v0, float& v1) {
+    constexpr float kL = 1.4426950216293335f, kRest = 1.925963033500011e-08f;  // log2(e) and the rest of it
+    auto both = [](float c) { return pair(c, c); };
+    const float x0 = fminf(fabsf(v0), 256.f), x1 = fminf(fabsf(v1), 256.f);
+    const Pair down = pair(-x0, -x1), z = mul2(down, both(kL)), minus_z = mul2(pair(x0, x1), both(kL));
+    const Pair rest = fma2(down, both(kRest), fma2(down, both(kL), minus_z));
+    float z0, z1, d0, d1, e0, e1;
+    unpair(z, z0, z1);
+    Pair e = pair(fast_exp2(z0), fast_exp2(z1));
+    e = fma2(e, mul2(rest, both(0.693147181f)), e);
+    unpair(fma2(e, both(1.f), both(1.f)), d0, d1);
+    unpair(e, e0, e1);
+    const Pair up = mul2(pair(v0, v1), pair(v0 > 0.f ? 1.f : e0, v1 > 0.f ? 1.f : e1));
+    unpair(mul2(up, pair(fast_rcp(d0), fast_rcp(d1))), v0, v1);
+}
+
 template <int VEC>
 __device__ __forceinline__ void activate(float (&v)[VEC], int act) {
     if (act == MOE_ACT_NONE) return;
@@ -218,7 +237,7 @@ __device__ __forceinline__ void activate(float (&v)[VEC], int act) {
         for (int i = 0; i < VEC; i += 2) gelu2(v[i], v[i + 1]);
     } else if (act == MOE_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = __fdividef(v[i], 1.f + __expf(-v[i]));
+        for (int i = 0; i < VEC; i += 2) silu2(v[i], v[i + 1]);
     } else if (act == MOE_ACT_RELU) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];

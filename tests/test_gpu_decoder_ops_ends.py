@@ -233,3 +233,17 @@ def test_linear_gelu_everywhere(m, T, yt):
     m.moe_linear(x, w, y, bias=v, act="gelu")
     want = (0.5 * v.double() * torch.special.erfc(-v.double() / math.sqrt(2.0))).expand(T, -1)
     within(y, as_stored(want, yt), want.abs() * (2.0 ** -18 + U[yt]) + 2.0 ** -126 + SUB[yt])
+
+
+@pytest.mark.parametrize("T", [1, 300])
+@pytest.mark.parametrize("yt", [F32, F16, BF16])
+def test_linear_silu_everywhere(m, T, yt):
+    """v / (1 + exp(-v)) of the bias alone, to 2^-20 of its value in fp32 and below 2^-126 absolutely:
+    an exponential good to 2^-22 and its factor, a sum, a reciprocal of 1 unit and two products (2^-24,
+    2^-24, 2^-23, 2^-23): 2.5 2^-22 in all."""
+    v = activation_points()
+    x, w = torch.zeros(T, 16, device="cuda").to(BF16), torch.zeros(v.numel(), 16, device="cuda").to(BF16)
+    y = torch.empty(T, v.numel(), dtype=yt, device="cuda")
+    m.moe_linear(x, w, y, bias=v, act="silu")
+    want = (v.double() * torch.sigmoid(v.double())).expand(T, -1)
+    within(y, as_stored(want, yt), want.abs() * (2.0 ** -20 + U[yt]) + 2.0 ** -126 + SUB[yt])
