@@ -211,6 +211,23 @@ def test_attend_adds_little_to_the_outputs_rounding(m, ct, qt, hq, hkv, D):
 # ---- linear -------------------------------------------------------------------
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 64, 4096), (3, 1000, 8192), (32, 512, 4096), (128, 256, 4096), (300, 520, 2048),
+                                   (600, 1023, 1040), (1024, 2048, 512)])
+@pytest.mark.parametrize("xt", [BF16, F16, E4M3])
+def test_linear_of_whole_numbers_is_exact(m, T, N, K, xt):
+    """Whole numbers up to 8 (their sums below 2^24): fp32 holds every partial sum, so that nothing may
+    be rounded on the way, in whatever parts the product is made and joined."""
+    g = gen(T + K)
+    x = torch.randint(-8, 9, (T, K), generator=g, device="cuda").to(xt)
+    w = torch.randint(-8, 9, (N, K), generator=g, device="cuda").to(xt)
+    one = (lambda n: torch.ones(n, device="cuda")) if xt == E4M3 else (lambda n: None)
+    r = torch.randint(-1000, 1000, (T, N), generator=g, device="cuda").float()
+    b = torch.randint(-1000, 1000, (N,), generator=g, device="cuda").float()
+    y = torch.empty(T, N, device="cuda")
+    m.moe_linear(x, w, y, bias=b, residual=r, x_scale=one(T), w_scale=one(N))
+    assert torch.equal(y.double(), x.double() @ w.double().t() + b.double() + r.double())
+
+
 def activation_points():
     v = torch.cat([torch.linspace(-14, 14, 40001), torch.linspace(-0.01, 0.01, 4001), torch.linspace(-90, 90, 18001),
                    torch.tensor([0.0, 1e-30, -1e-30, 1e30, -1e30, 3e38, -3e38])]).cuda()
