@@ -455,7 +455,8 @@ int moe_kv_append(moe_kv* kv, int type, const void* q, int64_t q_ts, int64_t q_h
  * h / (q_heads / kv_heads) at slot page_table[b][j / page_size] * page_size + j % page_size.
  *  q, out  device [B][q_heads][head_dim] of type q_type: MOE_BF16 or MOE_F16, the
  *          cache's own type unless the cache is MOE_E4M3; strides *_ts per sequence and
- *          *_hs per head; 16-byte aligned, strides whole 16-byte units.
+ *          *_hs per head; 16-byte aligned, strides whole 16-byte units.  out must not share
+ *          elements with q (out = q is refused): parts of a sequence read its query at any time.
  *  page_table device int32 [B][max_pages], rows table_stride apart (0: one row for all);
  *          entries past a sequence's last page (or wholly before its window) are not read.
  *  lengths device int32 [B].  A sequence of length 0 gets zeros and a log-sum of -inf.

@@ -414,7 +414,7 @@ PyMethodDef methods[] = {
     {"moe_kv_attend", FAST(py_attend),
      "moe_kv_attend(kv, q, page_table, lengths, out, scale=None, window=0, lse=None, stream=None)\n--\n\n"
      "Attention of one query token per sequence over the cache.\n\n"
-     "q, out [B, q_heads, head_dim] bfloat16 or float16; page_table int32 [B, max_pages]\n"
+     "q, out [B, q_heads, head_dim] bfloat16 or float16, not the same memory; page_table int32 [B, max_pages]\n"
      "(an expanded single row fits); lengths int32 [B]; scale defaults to\n"
      "head_dim ** -0.5; window: only the last `window` tokens count (0: all); lse fp32\n"
      "[B, q_heads] receives the log of the softmax sums."},

@@ -141,6 +141,7 @@ int moe_kv_attend(moe_kv* kv, const void* q, int q_type, int64_t q_ts, int64_t q
     if (!std::isfinite(scale)) return MOE_ERR_INVALID_ARG;
     if (B == 0) return MOE_OK;
     if (!q || !lengths || !out || (max_pages > 0 && !page_table)) return MOE_ERR_INVALID_ARG;
+    if (q == out) return MOE_ERR_INVALID_ARG;  // several CTAs read a query whose output one of them writes
     if (B == 1) q_ts = out_ts = table_stride = 0;  // of no meaning for one sequence, or one head
     if (kv->view.q_heads == 1) q_hs = out_hs = 0;
     if (!whole16(q, q_type, q_ts, q_hs) || !whole16(out, q_type, out_ts, out_hs)) return MOE_ERR_INVALID_ARG;

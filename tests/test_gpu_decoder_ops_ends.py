@@ -208,6 +208,23 @@ def test_attend_adds_little_to_the_outputs_rounding(m, ct, qt, hq, hkv, D):
     within(o, o64, tol)
 
 
+def test_attend_refuses_the_query_as_output(m):
+    """Parts of a sequence read its query while another's join may have written the output."""
+    g = gen(35)
+    k, v, _, _, pages = make_cache(g, [40], 16, 1, 64, BF16)
+    kv = m.KvCache(k, v, q_heads=4, max_batch=1)
+    q = randn(g, 1, 4, 64).to(BF16)
+    keep, n = q.clone(), torch.tensor([40], dtype=torch.int32, device="cuda")
+    with pytest.raises(m.MoeError) as e:
+        m.moe_kv_attend(kv, q, pages, n, q)
+    assert e.value.code == m.MOE_ERR_INVALID_ARG and torch.equal(q, keep) and kv.status() == 0
+    both = torch.cat([q, torch.zeros_like(q)], 1)  # one tensor's heads, apart from one another
+    o = torch.empty_like(q)
+    m.moe_kv_attend(kv, q, pages, n, o)
+    m.moe_kv_attend(kv, both[:, :4], pages, n, both[:, 4:])
+    assert torch.equal(both[:, 4:], o) and torch.equal(both[:, :4], keep)
+
+
 # ---- linear -------------------------------------------------------------------
 
 
