@@ -16,7 +16,7 @@ import torch
 try:
     from . import _decoder_ops
 except ImportError as e:  # as for the library itself: there is no other path
-    raise ImportError("moe_decode_host_gb300/_decoder_ops.so is missing or does not load: build the library first "
+    raise ImportError("the extension moe_decode_host_gb300/_decoder_ops is missing or does not load: build the library first "
                       "(python moe_decode_host_gb300/build.py, or __graft_entry__.build())") from e
 from ._lib import MOE_ERR_INVALID_ARG, MoeError, check, lib, moe_kv_params
 
