@@ -8,6 +8,7 @@ status codes out as MoeError.  PyTorch is used for device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 
 import numpy as np
 
@@ -19,8 +20,7 @@ __all__ = ["LIB_PATH", "MoeError", "Scratch", "Layer", "StepBuffers", "expert_by
            "moe_grouped_ffn", "moe_combine", "residency_update", "moe_gather_join", "link_probe", "debug_e2m1_pairs", "debug_e2m1_round", "run_step",
            "MOE_OK", "MOE_ERR_INVALID_ARG", "MOE_ERR_CUDA", "MOE_ERR_NONFINITE", "MOE_ERR_BAD_EXPERT",
            "MOE_ERR_TIMEOUT", "MOE_ERR_NOMEM", "MOE_ERR_INJECTED", "MOE_ERR_SCRATCH_TOO_SMALL",
-           "moe_grouped_ffn_noalloc", "residency_plan", "quant_mxfp4", "mxf4_peak_probe", "MOE_ERR_BAD_INDEX",
-           "KvCache", "moe_add_rms_norm", "moe_kv_append", "moe_kv_attend", "moe_linear"]
+           "moe_grouped_ffn_noalloc", "residency_plan", "quant_mxfp4", "mxf4_peak_probe", "MOE_ERR_BAD_INDEX"]
 
 
 def expert_bytes(H: int, I: int) -> int:
@@ -270,6 +270,8 @@ def run_step(layer: Layer, buf: StepBuffers, logits, x, stream=None, residency=T
 
 
 _DECODER_OPS = ("KvCache", "moe_add_rms_norm", "moe_kv_append", "moe_kv_attend", "moe_linear")
+if importlib.util.find_spec("torch") is not None:  # without torch "import *" brings the rest
+    __all__ += _DECODER_OPS
 
 
 def __getattr__(name):
