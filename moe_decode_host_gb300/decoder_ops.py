@@ -71,6 +71,8 @@ class KvCache:
             if s is not None and (s.dtype != torch.float32 or not s.is_cuda or s.shape != (kv_heads,)
                                   or (kv_heads > 1 and s.stride(0) != 1)):
                 refuse("a scale is not a contiguous CUDA fp32 [kv_heads]")
+        if any(not 0 <= n < 1 << 31 for n in (n_pages, page, kv_heads, q_heads, dim, max_batch)):
+            refuse("a size is out of range")  # the structure below would take its low 32 bits
         p = moe_kv_params(n_pages, page, kv_heads, q_heads, dim, _TYPES.index(k.dtype), max_batch, k.stride(0),
                           k.stride(1), k.stride(2))
         h = ctypes.c_void_p()
