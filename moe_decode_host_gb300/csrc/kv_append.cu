@@ -180,9 +180,6 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
     }
 }
 
-__device__ __forceinline__ void cp_async16(uint4* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async16_l1(uint4* dst, const void* src) {  // read by the whole CTA: through L1
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }

@@ -52,30 +52,13 @@ __device__ __forceinline__ int token_of(int r) {
     return F8 ? (r >> 1 & 3) * 4 + (r & 1) + (r >> 3) * 2 : r;
 }
 
-__device__ __forceinline__ float fast_exp2(float x) {
-    float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+// 16 bytes of a row of the cache, or zeros where `bytes` is 0.  Rows are read whole: 128 bytes at a time from L2.
+__device__ __forceinline__ void cp_row16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+__device__ __forceinline__ void cp_row16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void cp_wait(int left) {  // until at most `left` groups are in flight
-    switch (left) {
-        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-    }
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -338,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                         const int r = (i0 + lane) / CPR, col = (i0 + lane) % CPR * 16;
                         const uint64_t o = __shfl_sync(0xffffffffu, off, r) * unit + col;
                         const uint32_t at = dst + r * pitch + (col ^ (swap_of<F8>(r) & swizzle) << 4);
-                        cp_async16(at, kb + o);
-                        cp_async16(at + U * pitch, vb + o);
+                        cp_row16(at, kb + o);
+                        cp_row16(at + U * pitch, vb + o);
                     }
                 } else {
                     for (int i0 = 0; i0 < U * cpr; i0 += 32) {
@@ -349,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                         if (row < U) {
                             const uint32_t bytes = (mask >> row & 1u) ? 16u : 0u;  // rows left out are zeros
                             const uint32_t at = dst + row * pitch + (col ^ (swap_of<F8>(row) & swizzle) << 4);
-                            cp_async16(at, kb + o, bytes);
-                            cp_async16(at + U * pitch, vb + o, bytes);
+                            cp_row16(at, kb + o, bytes);
+                            cp_row16(at + U * pitch, vb + o, bytes);
                         }
                     }
                 }
@@ -710,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                     for (int k = k0; k < min(parts, k0 + fit); ++k) {
 #pragma unroll
                         for (int x = 0; x < IT; ++x)
-                            if (tid + x * kThreads < pieces) cp_async16(to + x * kThreads * 16, from + 4 * x * kThreads);
+                            if (tid + x * kThreads < pieces) cp_row16(to + x * kThreads * 16, from + 4 * x * kThreads);
                         from += k == 0 ? stride / 2 : stride;
                         to += pieces * 16;
                     }

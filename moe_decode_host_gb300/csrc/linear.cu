@@ -171,12 +171,6 @@ __device__ __forceinline__ float fast_rcp(float x) {
     return y;
 }
 
-__device__ __forceinline__ float fast_exp2(float x) {
-    float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // GELU of two values, v Phi(v) = max(v, 0) - |v| Phi(-|v|), so that small results keep their
 // precision.  With x = |v| and t = 1 / (1 + 0.3 x),
 //   Phi(-x) = exp(-x^2 / 2) t P(t),

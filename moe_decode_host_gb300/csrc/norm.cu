@@ -23,18 +23,6 @@ constexpr float kE4M3Max = 448.f;
 constexpr int kRingBytes = 48 * 1024;  // of a CTA, where two stages fit
 constexpr int kAny = -1;  // a type known only at run time
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_wait(int left) {  // until at most `left` groups are in flight
-    switch (left) {
-        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    }
-}
-
 // The larger of two, NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
