@@ -491,7 +491,10 @@ int moe_kv_clear_status(moe_kv* kv);
  *  y device [T][N] of y_type (MOE_BF16, MOE_F16, MOE_F32), rows y_stride apart.
  *  status_dev device int, or NULL: set to MOE_ERR_TIMEOUT when a bounded device wait ran
  *    out (zero it first; y is then undefined).
- * T, N (at most 2^22) and the strides of y and residual are free; T = 0 is valid; N, K >= 1.
+ * The sums are the tensor cores' fp32 accumulators, which round towards zero at every step of 32
+ * bytes of K (bf16 and f16: about 1e-9 K of the output's size).
+ * T, N (at most 2^22) and the strides of y and residual are free; x and w rows are at least K
+ * apart; T = 0 is valid; N, K >= 1.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
 int moe_linear(const void* x, int64_t x_stride, const void* w, int64_t w_stride, int in_type, int T, int N, int K,
                const float* x_scale, const float* w_scale, const void* bias, int bias_type, int act,

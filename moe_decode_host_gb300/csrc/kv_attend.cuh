@@ -4,9 +4,9 @@
 //
 // Bound by the cache's bytes, each read once for a block of up to 32 query heads of a key
 // head (16 from head_dim 144 on).  Measured on a GB300, with the share of a plain copy's
-// rate: 32 ragged sequences (1.1 GB of bf16) 170 us (96%); 64 long ones in E4M3, 16 query
-// heads a key head (1.6 GB) 272 to 300 us (87 to 79%: issue latency); one sequence of 4097
-// tokens 13 us, a chain of latencies.
+// rate: 32 ragged sequences (1.1 GB of bf16) 174 us (94%); 64 long ones in E4M3, 16 query
+// heads a key head (1.6 GB) 295 us (81%: issue latency); one sequence of 4097 tokens 13.5 us, 15.1
+// with its rows in memory and not in L2, a chain of latencies.
 //
 // Split.  The attended tokens of a (sequence, key head, block of query heads) form a
 // segment of units of 16 tokens (32 where a row is at most 128 bytes), and a few places more
@@ -24,8 +24,9 @@
 // same lanes for S and O, so rescaling needs no exchange.  E4M3 keys and values become
 // f16 in registers (exactly): the order of dimensions within a 16-wide step of the
 // contraction is free, so a lane's four consecutive bytes serve as its four elements, in the
-// tokens of V^T P^T as in the dimensions of K Q^T.  mma.sync suffices: the products take 9%
-// (bf16) and 32% (E4M3, 16 heads) of the tensor pipe, and their operands come from registers.
+// tokens of V^T P^T as in the dimensions of K Q^T.  The weights P are two 16-bit terms each.
+// mma.sync suffices: the products take 14% (bf16) and 46% (E4M3, 16 heads) of the tensor pipe,
+// and their operands come from registers.
 #pragma once
 
 #include <algorithm>

@@ -15,11 +15,16 @@
 //                 operands), persistent, with two accumulators so that the epilogue of a
 //                 tile runs under the next tile's products.
 //
-// Measured on a GB300 (launches of a graph): 1 x 4096 x 4096 bf16 with residual 7.3 us (4.6
-// TB/s of weights, launch and fill included), 32 x 6144 x 4096 E4M3 6.4 us, 8192 x 6144 x
-// 4096 bf16 with bias, GELU and residual 231 us (1780 TFLOP/s; 263 us back to back under the
-// power cap), without an epilogue 217 us (cuBLAS 231 in the same bursts of 30).  Between them
-// 128 x 4096 x 4096 10.8 us (cuBLAS 7.6), 512 16.7 (11.6), 1024 23.4 (19.8).
+// Measured on a GB300 (launches of a graph): 1 x 4096 x 4096 bf16 with residual 7.2 us over three
+// sets of weights, of which L2 holds much, 8.2 us over 24 (4.1 TB/s, launch and fill included); 32 x
+// 6144 x 4096 E4M3 6.5 and 8.6 us; 8192 x 6144 x 4096 bf16 with bias, GELU and residual 235 us
+// (1750 TFLOP/s; 262 us back to back under the power cap), E4M3 with bias 115 us (3580 TFLOP/s;
+// 130 back to back).  Between them 128 x 4096 x 4096 10.8 us (cuBLAS 7.6), 512 17.4 (11.6), 1024 24.3
+// (19.8).
+//
+// The tensor cores' fp32 sums round towards zero, a step of 32 bytes of K at a time: fp32 outputs of
+// bf16 products are off by 1.0e-6 at K = 1024 and 9.1e-6 at 8192 in tiles, as the library's are, and by
+// less where K is split.
 #include <algorithm>
 
 #include "ptx.cuh"
@@ -177,7 +182,8 @@ __device__ __forceinline__ float fast_rcp(float x) {
 // P the polynomial of degree 7 nearest to the quotient in relative terms for x up to 14.5
 // (Remez exchange; 1.6e-7).  The exponent -x^2 log2(e) / 2 reaches 126, where fp32 alone would
 // lose 2^-17 of the result: what its two products round off is brought back as a factor.  In
-// all 2^-18 of the value at most, wherever it is a normal fp32 number.  At 64 the tail has long
+// all 2^-18 of the value at most, wherever it is a normal fp32 number (2048 x 4096 x 512 23.8 us;
+// 22.2 with Abramowitz and Stegun 7.1.28, which is good to 5e-7 absolutely alone).  At 64 the tail has long
 // vanished; the argument is held there, so that no infinity is multiplied by 0.
 __device__ __forceinline__ void gelu2(float& v0, float& v1) {
     const float x0 = fabsf(v0), x1 = fabsf(v1);

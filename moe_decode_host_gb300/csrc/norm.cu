@@ -8,7 +8,7 @@
 // is common to the row, so max |y| = rsqrt(...) * max |s * w| and the maximum can be
 // taken before the factor is known.
 //
-// Measured on a GB300: 8192 x 4096 bf16 with residual to E4M3 37.8 us (6.2 TB/s, 91% of a
+// Measured on a GB300: 8192 x 4096 bf16 with residual to E4M3 38.2 us (6.2 TB/s, 91% of a
 // plain copy's rate), 777 x 5003 f16 with an fp32 residual (rows at odd addresses) 13.8 us
 // (3.4 TB/s), one row 1.7 us.
 #include <algorithm>
