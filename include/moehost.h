@@ -467,7 +467,8 @@ int moe_kv_append(moe_kv* kv, int type, const void* q, int64_t q_ts, int64_t q_h
  * tokens are left out, the length is clamped.  The result does not depend on the
  * timing of the GPU: the same call gives the same bits.
  * 0 <= B <= max_batch; scale finite.  The softmax is fp32; its weights meet the values as two
- * 16-bit terms each, which lose at most 2^-16 of a weight (bf16 caches) or 2^-22 (f16, E4M3).
+ * 16-bit terms each, which lose at most 2^-16 of a weight (bf16 caches), or 2^-22 of it and
+ * 2^-31 of the largest one (f16, E4M3).
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
 int moe_kv_attend(moe_kv* kv, const void* q, int q_type, int64_t q_ts, int64_t q_hs, const int32_t* page_table,
                   int64_t table_stride, int max_pages, const int32_t* lengths, int B, float scale, int window,
