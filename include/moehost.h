@@ -72,8 +72,8 @@ extern "C" {
 #define MOE_ERR_SCRATCH_TOO_SMALL (-8)
 #define MOE_ERR_BAD_INDEX (-9)
 
-/* Element types of the decoder-layer operators (moe_add_rms_norm, moe_kv_*,
- * moe_linear).  MOE_E4M3 is the 8-bit float with 4 exponent and 3 mantissa bits,
+/* Element types of the decoder-layer operators (moe_add_rms_norm, moe_quant_e4m3, moe_kv_*,
+ * moe_linear, moe_linear_blocks).  MOE_E4M3 is the 8-bit float with 4 exponent and 3 mantissa bits,
  * largest value 448; conversions to it round to nearest, ties to even, and saturate. */
 #define MOE_BF16 0
 #define MOE_F16 1
@@ -397,6 +397,17 @@ int moe_add_rms_norm(const void* x, int x_type, int64_t x_stride, const void* re
                      int64_t res_stride, const void* weight, int weight_type, float eps, int T, int H, void* sum_out,
                      int64_t sum_stride, void* y, int y_type, int64_t y_stride, float* y_scale, void* stream);
 
+/* Rows to E4M3 with one fp32 scale for each 128 elements, the operands of moe_linear_blocks:
+ *   scale[t][g] = max(max_k |x_tk| / 448, 2^-126),  y_tk = x_tk / scale[t][g],  k in [128 g, 128 g + 128)
+ * A group with a NaN or an infinity gets a NaN scale and NaN codes.  Each group is independent.
+ *  x     device [T][K] of x_type (MOE_BF16, MOE_F16 or MOE_F32), rows x_stride apart.
+ *  y     device E4M3 [T][K], rows y_stride apart.
+ *  scale device fp32 [T][ceil(K / 128)], rows scale_stride apart.
+ * The outputs must not share memory with x.  K >= 1; T = 0 is valid.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
+int moe_quant_e4m3(const void* x, int x_type, int64_t x_stride, int T, int K, void* y, int64_t y_stride, float* scale,
+                   int64_t scale_stride, void* stream);
+
 /* A paged key-value cache of one layer.  Token slot s is entry s % page_size of page
  * s / page_size; element d of key head h there is at
  *   k_cache[(s / page_size) * page_stride + (s % page_size) * token_stride + h * head_stride + d]
@@ -428,6 +439,25 @@ int moe_kv_create(const moe_kv_params* p, void* k_cache, void* v_cache, const fl
                   moe_kv** out);
 int moe_kv_destroy(moe_kv* kv);
 
+/* A cache of MOE_E4M3 with one fp32 scale for each block of scale_tokens tokens of a page and key
+ * head, so that no scale has to be known before the tokens are:
+ *   value = scale[page][entry / scale_tokens][h] * code,
+ * k_scale and v_scale device fp32 [n_pages][page_size / scale_tokens][kv_heads], contiguous, which
+ * moe_kv_append writes and moe_kv_attend reads (a scale of the caller's own making may be any
+ * number).  scale_tokens: 1 to 1024, a divisor of page_size.  The rest as moe_kv_create, and the handle
+ * is used in the same calls:
+ *  moe_kv_append  gives a block the smallest power of two with which the largest magnitude among the
+ *    tokens that it takes in, at most 448 * scale, held to 2^-126 and 2^119 (larger values, infinities among
+ *    them, saturate; NaN stays NaN and does not count).  A block whose first entry is among them starts anew:
+ *    what else it held means nothing any more, though its bytes stay.  Any other block keeps its scale
+ *    where that is large enough; where it is not, the codes of its other entries are rewritten under the
+ *    new one (exact but where codes of less than 2^-6 lose their low bits), so the block's scale has to be
+ *    initialised (zero will do) before a block is begun in its middle.  The tokens of a call that go to
+ *    one block have to follow one another in the call.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA, MOE_ERR_NOMEM. */
+int moe_kv_create_blocks(const moe_kv_params* p, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                         int scale_tokens, moe_kv** out);
+
 /* Position rotation and append.  For each token t: the first rot_dim elements of
  * every head of q and k are turned by the token's position,
  *   (a, b) -> (a cos - b sin, a sin + b cos),
@@ -448,6 +478,19 @@ int moe_kv_append(moe_kv* kv, int type, const void* q, int64_t q_ts, int64_t q_h
                   int64_t k_hs, const void* v, int64_t v_ts, int64_t v_hs, const int32_t* positions,
                   const int64_t* slots, const float* cos_sin, int n_positions, int rot_dim, int interleaved, int T,
                   void* q_out, int64_t qo_ts, int64_t qo_hs, void* stream);
+
+/* moe_kv_append where a token's position has several axes (time, height and width of an image's or a
+ * video's tokens): pair i of a head is turned by the table's row of position positions[axis_of_pair[i]][t].
+ *  positions     device int32 [n_axes][T], rows positions_stride apart.  A token with any position
+ *                outside the table is left out.
+ *  axis_of_pair  host uint8 [rot_dim / 2], each below n_axes; read during the call.
+ *  1 <= n_axes <= 4, and rot_dim > 0.  The rest as moe_kv_append.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
+int moe_kv_append_axes(moe_kv* kv, int type, const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts,
+                       int64_t k_hs, const void* v, int64_t v_ts, int64_t v_hs, const int32_t* positions,
+                       int64_t positions_stride, int n_axes, const uint8_t* axis_of_pair, const int64_t* slots,
+                       const float* cos_sin, int n_positions, int rot_dim, int interleaved, int T, void* q_out,
+                       int64_t qo_ts, int64_t qo_hs, void* stream);
 
 /* Attention of one query token per sequence over the cache:
  *   out[b][h] = sum_j softmax_j(scale * q[b][h] . k_j) v_j,  j in [max(0, n - window), n)
@@ -501,6 +544,19 @@ int moe_linear(const void* x, int64_t x_stride, const void* w, int64_t w_stride,
                const float* x_scale, const float* w_scale, const void* bias, int bias_type, int act,
                const void* residual, int64_t res_stride, void* y, int y_type, int64_t y_stride, int* status_dev,
                void* stream);
+
+/* moe_linear on E4M3 operands with a scale for each block of 128: with G = ceil(K / 128),
+ *   y = act(sum_g x_scale[t][g] * w_scale[n / 128][g] * (sum_{k in g} x_tk w_nk) + bias) + residual
+ *  x device E4M3 [T][K], w device E4M3 [N][K], as in moe_linear.
+ *  x_scale device fp32 [T][G], rows x_scale_stride apart; w_scale device fp32 [ceil(N / 128)][G], rows
+ *    w_scale_stride apart: any numbers.
+ * The rest as moe_linear.  The products of a block of K are summed by the tensor cores (fp32, towards zero
+ * at every 32 of K), the blocks in fp32 to nearest.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
+int moe_linear_blocks(const void* x, int64_t x_stride, const void* w, int64_t w_stride, int T, int N, int K,
+                      const float* x_scale, int64_t x_scale_stride, const float* w_scale, int64_t w_scale_stride,
+                      const void* bias, int bias_type, int act, const void* residual, int64_t res_stride, void* y,
+                      int y_type, int64_t y_stride, int* status_dev, void* stream);
 
 /* Copies the placement map to host int32 [E] (synchronous). */
 int moe_layer_get_loc(moe_layer* L, int32_t* loc_host);

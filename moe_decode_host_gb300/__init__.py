@@ -269,7 +269,8 @@ def run_step(layer: Layer, buf: StepBuffers, logits, x, stream=None, residency=T
     return residency_update(layer, stream) if residency else 0
 
 
-_DECODER_OPS = ("KvCache", "moe_add_rms_norm", "moe_kv_append", "moe_kv_attend", "moe_linear")
+_DECODER_OPS = ("KvCache", "moe_add_rms_norm", "moe_quant_e4m3", "moe_kv_append", "moe_kv_attend", "moe_linear",
+                "moe_linear_blocks")
 if importlib.util.find_spec("torch") is not None:  # without torch "import *" brings the rest
     __all__ += _DECODER_OPS
 

@@ -17,6 +17,8 @@ constexpr int budget_of(int ctas) { return ctas == 3 ? 73 * 1024 : (ctas == 2 ? 
 // work a token that does not depend on its row (page look-up, the maxima's exchange).
 __host__ __device__ constexpr int unit_tokens(int bytes) { return bytes <= 128 ? 32 : 16; }
 constexpr int kMaxStages = 8;    // units of a warp's ring
+// Bytes of the scales of a unit's keys and values, where each token has its own.
+__host__ __device__ constexpr int scale_bytes(int tokens) { return 8 * tokens; }
 constexpr int kMinUnits = 4;     // units worth a CTA of its own: one a warp
 // Units that a CTA could stream in the time that starting and ending a piece takes (about 5
 // us): each segment is that much longer on the line that the CTAs share out, or those with
@@ -62,5 +64,6 @@ __host__ __device__ constexpr int row_pitch(int pieces) {
 cudaError_t launch_attend_bf16(const AttendArgs& a, const AttendPlan& p, cudaStream_t st);
 cudaError_t launch_attend_f16(const AttendArgs& a, const AttendPlan& p, cudaStream_t st);
 cudaError_t launch_attend_e4m3(const AttendArgs& a, const AttendPlan& p, cudaStream_t st);
+cudaError_t launch_attend_e4m3_blocks(const AttendArgs& a, const AttendPlan& p, cudaStream_t st);
 
 }  // namespace moe

@@ -9,6 +9,8 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "moehost.h"
 
 namespace {
@@ -25,6 +27,9 @@ decltype(&moe_add_rms_norm) f_norm = nullptr;
 decltype(&moe_kv_append) f_append = nullptr;
 decltype(&moe_kv_attend) f_attend = nullptr;
 decltype(&moe_linear) f_linear = nullptr;
+decltype(&moe_quant_e4m3) f_quant = nullptr;
+decltype(&moe_kv_append_axes) f_append_axes = nullptr;
+decltype(&moe_linear_blocks) f_linear_blocks = nullptr;
 
 PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device, *s_device_index, *s_cuda_stream, *s_call;
 
@@ -143,6 +148,12 @@ bool vector(PyObject* o, Tensor& t, int64_t n, int type, Call& where, const char
     return true;
 }
 
+// fp32 [rows, blocks], contiguous in its last dimension.
+bool scales(PyObject* o, Tensor& t, int64_t rows, int64_t blocks, Call& where, const char* name) {
+    if (!matrix(o, t, rows, blocks, where, name)) return false;
+    return t.type == kF32 || refuse(where, name, "has a type that the call does not take");
+}
+
 // [rows, heads, dim] of one type, contiguous in its last dimension.
 bool heads(PyObject* o, Tensor& t, int64_t rows, int64_t n, int64_t dim, int type, Call& where, const char* name) {
     if (!read(o, t, where, name)) return false;
@@ -221,6 +232,25 @@ bool integer(PyObject* o, int& v) {
     return true;
 }
 
+// The axis of each of `pairs` pairs: bytes, or any sequence of small integers.
+constexpr int kMaxPairs = 128;
+bool axis_list(PyObject* o, uint8_t (&out)[kMaxPairs], int64_t pairs, const Call& w) {
+    if (PyBytes_Check(o) && PyBytes_GET_SIZE(o) == pairs && pairs <= kMaxPairs) {
+        memcpy(out, PyBytes_AS_STRING(o), (size_t)pairs);
+        return true;
+    }
+    PyObject* s = PySequence_Fast(o, "axes: a sequence was expected");
+    if (!s) return false;
+    bool ok = PySequence_Fast_GET_SIZE(s) == pairs && pairs <= kMaxPairs;
+    for (int64_t i = 0; ok && i < pairs; ++i) {
+        const long a = PyLong_AsLong(PySequence_Fast_GET_ITEM(s, i));
+        ok = a >= 0 && a < 256 && !PyErr_Occurred();
+        if (ok) out[i] = (uint8_t)a;
+    }
+    Py_DECREF(s);
+    return ok || (!PyErr_Occurred() && refuse(w, "axes", "do not give each pair of the table an axis"));
+}
+
 // handle, q_heads, kv_heads, head_dim and device of a KvCache
 struct Cache {
     moe_kv* kv = nullptr;
@@ -269,10 +299,29 @@ PyObject* py_norm(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) 
                   w.name);
 }
 
-PyObject* n_append[10];
+PyObject* n_quant[4];
+PyObject* py_quant(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+    Call w{"moe_quant_e4m3"};
+    PyObject* v[4];  // x, y, scale, stream
+    if (!arguments(args, n, kw, w.name, n_quant, 3, v)) return nullptr;
+    Tensor x, y, sc;
+    void* st = nullptr;
+    if (!matrix(v[0], x, -1, 0, w, "x")) return nullptr;
+    const int64_t T = x.shape[0], K = x.shape[1];
+    if (x.type == kE4m3) return refuse(w, "x", "has a type that the call does not take"), nullptr;
+    if (!matrix(v[1], y, T, K, w, "y")) return nullptr;
+    if (y.type != kE4m3) return refuse(w, "y", "has a type that the call does not take"), nullptr;
+    if (!scales(v[2], sc, T, (K + 127) / 128, w, "scale") || !stream_of(v[3], w, st)) return nullptr;
+    if (T > INT32_MAX || K > INT32_MAX) return refuse(w, "x", "is too large"), nullptr;
+    return finish(f_quant(x.ptr, x.type, x.stride[0], (int)T, (int)K, y.ptr, y.stride[0], static_cast<float*>(sc.ptr),
+                          sc.stride[0], st),
+                  w.name);
+}
+
+PyObject* n_append[11];
 PyObject* py_append(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
     Call w{"moe_kv_append"};
-    PyObject* v[10];  // kv, q, k, v, positions, slots, cos_sin, q_out, interleaved, stream
+    PyObject* v[11];  // kv, q, k, v, positions, slots, cos_sin, q_out, interleaved, stream, axes
     if (!arguments(args, n, kw, w.name, n_append, 8, v)) return nullptr;
     Cache c;
     Tensor q, k, x, o, pos, slots, cs;
@@ -286,11 +335,28 @@ PyObject* py_append(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw
         if (!matrix(v[6], cs, -1, 0, w, "cos_sin")) return nullptr;
         if (cs.type != kF32 || (cs.stride[0] != cs.shape[1] && cs.shape[0] > 1) || cs.shape[0] > INT32_MAX)
             return refuse(w, "cos_sin", "is not a contiguous fp32 table"), nullptr;
-        if (!vector(v[4], pos, T, kI32, w, "positions")) return nullptr;
+        if (!given(v[10]) && !vector(v[4], pos, T, kI32, w, "positions")) return nullptr;
     }
     const int turn = given(v[8]) ? PyObject_IsTrue(v[8]) : 0;
-    if (turn < 0 || !stream_of(v[9], w, st)) return nullptr;
+    if (turn < 0) return nullptr;
+    uint8_t axis[kMaxPairs];
+    if (given(v[10])) {
+        if (!given(v[6])) return refuse(w, "axes", "are given without cos_sin"), nullptr;
+        if (!read(v[4], pos, w, "positions")) return nullptr;
+        if (pos.type != kI32 || pos.dims != 2 || pos.shape[1] != T || (T > 1 && pos.stride[1] != 1))
+            return refuse(w, "positions", "is not an int32 [axes, T] with contiguous rows"), nullptr;
+        if (pos.shape[0] > INT32_MAX) return refuse(w, "positions", "is too large"), nullptr;
+        if (!axis_list(v[10], axis, cs.shape[1] / 2, w)) return nullptr;
+    }
+    if (!stream_of(v[9], w, st)) return nullptr;
     if (T > INT32_MAX || cs.shape[1] > 1024) return refuse(w, "q or cos_sin", "is too large"), nullptr;
+    if (given(v[10]))
+        return finish(f_append_axes(c.kv, q.type, q.ptr, q.stride[0], q.stride[1], k.ptr, k.stride[0], k.stride[1], x.ptr,
+                                    x.stride[0], x.stride[1], static_cast<int32_t*>(pos.ptr), pos.stride[0],
+                                    (int)pos.shape[0], axis, static_cast<int64_t*>(slots.ptr),
+                                    static_cast<float*>(cs.ptr), (int)cs.shape[0], (int)cs.shape[1], turn, (int)T, o.ptr,
+                                    o.stride[0], o.stride[1], st),
+                      w.name);
     return finish(f_append(c.kv, q.type, q.ptr, q.stride[0], q.stride[1], k.ptr, k.stride[0], k.stride[1], x.ptr,
                            x.stride[0], x.stride[1], static_cast<int32_t*>(pos.ptr), static_cast<int64_t*>(slots.ptr),
                            static_cast<float*>(cs.ptr), (int)cs.shape[0], (int)cs.shape[1], turn, (int)T, o.ptr,
@@ -335,61 +401,95 @@ PyObject* py_attend(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw
                   w.name);
 }
 
-PyObject* n_linear[10];
 PyObject* g_acts[4];  // "none", "relu", "silu", "gelu"
+
+// What moe_linear and moe_linear_blocks take alike, read and checked.
+struct Product {
+    Tensor x, w, y, bias, residual, status;
+    int64_t T = 0, N = 0, K = 0;
+    int act = MOE_ACT_NONE;
+    void* stream = nullptr;
+    bool read_all(PyObject* px, PyObject* pw, PyObject* py, PyObject* pb, PyObject* pact, PyObject* pr, PyObject* pstatus,
+                  PyObject* pstream, Call& f) {
+        if (!matrix(px, x, -1, 0, f, "x") || !matrix(pw, w, -1, 0, f, "w")) return false;
+        T = x.shape[0], K = x.shape[1], N = w.shape[0];
+        if (w.shape[1] != K || w.type != x.type) return refuse(f, "w", "is not [N, K] of x's type");
+        if (!matrix(py, y, T, N, f, "y")) return false;
+        if (given(pb) && !vector(pb, bias, N, -1, f, "bias")) return false;
+        if (given(pact)) {
+            act = -1;
+            for (int i = 0; i < 4; ++i)
+                if (pact == g_acts[i] || (PyUnicode_Check(pact) && PyUnicode_Compare(pact, g_acts[i]) == 0)) act = i;
+            if (act < 0) return refuse(f, "act", "is not none, relu, silu or gelu");
+        }
+        if (given(pr)) {
+            if (!matrix(pr, residual, T, N, f, "residual")) return false;
+            if (residual.type != y.type) return refuse(f, "residual", "has another type than y");
+        }
+        if (given(pstatus) && !vector(pstatus, status, 1, kI32, f, "status")) return false;
+        if (!stream_of(pstream, f, stream)) return false;
+        return (T <= INT32_MAX && N <= INT32_MAX && K <= INT32_MAX) || refuse(f, "x or w", "is too large");
+    }
+};
+
+PyObject* n_linear[10];
 PyObject* py_linear(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
     Call f{"moe_linear"};
     PyObject* v[10];  // x, w, y, bias, act, residual, x_scale, w_scale, status, stream
     if (!arguments(args, n, kw, f.name, n_linear, 3, v)) return nullptr;
-    Tensor x, w, y, b, r, xs, ws, status;
-    void* st = nullptr;
-    if (!matrix(v[0], x, -1, 0, f, "x") || !matrix(v[1], w, -1, 0, f, "w")) return nullptr;
-    const int64_t T = x.shape[0], K = x.shape[1], N = w.shape[0];
-    if (w.shape[1] != K || w.type != x.type) return refuse(f, "w", "is not [N, K] of x's type"), nullptr;
-    if (!matrix(v[2], y, T, N, f, "y")) return nullptr;
-    if (given(v[3]) && !vector(v[3], b, N, -1, f, "bias")) return nullptr;
-    int act = MOE_ACT_NONE;
-    if (given(v[4])) {
-        act = -1;
-        for (int i = 0; i < 4; ++i)
-            if (v[4] == g_acts[i] || (PyUnicode_Check(v[4]) && PyUnicode_Compare(v[4], g_acts[i]) == 0)) act = i;
-        if (act < 0) return refuse(f, "act", "is not none, relu, silu or gelu"), nullptr;
-    }
-    if (given(v[5])) {
-        if (!matrix(v[5], r, T, N, f, "residual")) return nullptr;
-        if (r.type != y.type) return refuse(f, "residual", "has another type than y"), nullptr;
-    }
-    if (given(v[6]) && !vector(v[6], xs, T, kF32, f, "x_scale")) return nullptr;
-    if (given(v[7]) && !vector(v[7], ws, N, kF32, f, "w_scale")) return nullptr;
-    if (given(v[8]) && !vector(v[8], status, 1, kI32, f, "status")) return nullptr;
-    if (!stream_of(v[9], f, st)) return nullptr;
-    if (T > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return refuse(f, "x or w", "is too large"), nullptr;
-    return finish(f_linear(x.ptr, x.stride[0], w.ptr, w.stride[0], x.type, (int)T, (int)N, (int)K,
-                           static_cast<float*>(xs.ptr), static_cast<float*>(ws.ptr), b.ptr, b.type, act, r.ptr,
-                           r.stride[0], y.ptr, y.type, y.stride[0], static_cast<int*>(status.ptr), st),
+    Product p;
+    Tensor xs, ws;
+    if (!p.read_all(v[0], v[1], v[2], v[3], v[4], v[5], v[8], v[9], f)) return nullptr;
+    if (given(v[6]) && !vector(v[6], xs, p.T, kF32, f, "x_scale")) return nullptr;
+    if (given(v[7]) && !vector(v[7], ws, p.N, kF32, f, "w_scale")) return nullptr;
+    return finish(f_linear(p.x.ptr, p.x.stride[0], p.w.ptr, p.w.stride[0], p.x.type, (int)p.T, (int)p.N, (int)p.K,
+                           static_cast<float*>(xs.ptr), static_cast<float*>(ws.ptr), p.bias.ptr, p.bias.type, p.act,
+                           p.residual.ptr, p.residual.stride[0], p.y.ptr, p.y.type, p.y.stride[0],
+                           static_cast<int*>(p.status.ptr), p.stream),
                   f.name);
 }
 
-// bind(MoeError, raw_stream, current_device, (six dtypes), (four addresses))
+PyObject* n_linear_blocks[10];
+PyObject* py_linear_blocks(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+    Call f{"moe_linear_blocks"};
+    PyObject* v[10];  // x, w, y, x_scale, w_scale, bias, act, residual, status, stream
+    if (!arguments(args, n, kw, f.name, n_linear_blocks, 5, v)) return nullptr;
+    Product p;
+    Tensor xs, ws;
+    if (!p.read_all(v[0], v[1], v[2], v[5], v[6], v[7], v[8], v[9], f)) return nullptr;
+    if (p.x.type != kE4m3) return refuse(f, "x", "has a type that the call does not take"), nullptr;
+    const int64_t G = (p.K + 127) / 128;
+    if (!scales(v[3], xs, p.T, G, f, "x_scale") || !scales(v[4], ws, (p.N + 127) / 128, G, f, "w_scale")) return nullptr;
+    return finish(f_linear_blocks(p.x.ptr, p.x.stride[0], p.w.ptr, p.w.stride[0], (int)p.T, (int)p.N, (int)p.K,
+                                  static_cast<float*>(xs.ptr), xs.stride[0], static_cast<float*>(ws.ptr), ws.stride[0],
+                                  p.bias.ptr, p.bias.type, p.act, p.residual.ptr, p.residual.stride[0], p.y.ptr, p.y.type,
+                                  p.y.stride[0], static_cast<int*>(p.status.ptr), p.stream),
+                  f.name);
+}
+
+// bind(MoeError, raw_stream, current_device, (six dtypes), (the first addresses, in the order below))
 PyObject* py_bind(PyObject*, PyObject* args) {
     PyObject *error, *raw, *current, *types, *addr;
     if (!PyArg_ParseTuple(args, "OOOO!O!", &error, &raw, &current, &PyTuple_Type, &types, &PyTuple_Type, &addr))
         return nullptr;
-    if (PyTuple_GET_SIZE(types) != kTypes || PyTuple_GET_SIZE(addr) != 4) {
-        PyErr_SetString(PyExc_ValueError, "six types and four addresses");
+    constexpr int kCalls = 7;
+    const Py_ssize_t calls = PyTuple_GET_SIZE(addr);
+    if (PyTuple_GET_SIZE(types) != kTypes || calls > kCalls) {
+        PyErr_SetString(PyExc_ValueError, "six types and at most seven addresses");
         return nullptr;
     }
-    void* p[4];
-    for (int i = 0; i < 4; ++i) p[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(addr, i));
+    void* p[kCalls];
+    for (Py_ssize_t i = 0; i < calls; ++i) p[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(addr, i));
     if (PyErr_Occurred()) return nullptr;
     g_error = Py_NewRef(error);
     g_raw_stream = Py_NewRef(raw);
     g_current = Py_NewRef(current);
     for (int i = 0; i < kTypes; ++i) g_types[i] = Py_NewRef(PyTuple_GET_ITEM(types, i));
-    f_norm = reinterpret_cast<decltype(f_norm)>(p[0]);
-    f_append = reinterpret_cast<decltype(f_append)>(p[1]);
-    f_attend = reinterpret_cast<decltype(f_attend)>(p[2]);
-    f_linear = reinterpret_cast<decltype(f_linear)>(p[3]);
+    auto take = [&](int i, auto& f) {  // those not given stay as they were
+        if (i < calls) f = reinterpret_cast<std::remove_reference_t<decltype(f)>>(p[i]);
+    };
+    take(0, f_norm), take(1, f_append), take(2, f_attend), take(3, f_linear);
+    take(4, f_quant), take(5, f_append_axes), take(6, f_linear_blocks);
     Py_RETURN_NONE;
 }
 
@@ -404,13 +504,21 @@ PyMethodDef methods[] = {
      "None; y [T, H].  A float8_e4m3fn y holds y / scale[t], scale [T] fp32 being the\n"
      "row's largest |y| / 448.  sum_out may be residual or x; y may be x."},
     {"moe_kv_append", FAST(py_append),
-     "moe_kv_append(kv, q, k, v, positions, slots, cos_sin, q_out, interleaved=False, stream=None)\n--\n\n"
+     "moe_kv_append(kv, q, k, v, positions, slots, cos_sin, q_out, interleaved=False, stream=None, axes=None)\n--\n\n"
      "Rotates q and k by position, writes q to q_out and k, v to their cache slots.\n\n"
      "q, q_out [T, q_heads, head_dim]; k, v [T, kv_heads, head_dim], strided views of a\n"
      "fused projection's rows among them; positions int32 [T]; slots int64 [T] (page *\n"
      "page_size + entry, negative: not appended); cos_sin fp32 [positions, rot_dim]\n"
      "(cosines, then sines), or None for no rotation.  interleaved pairs (2i, 2i + 1)\n"
-     "instead of (i, i + rot_dim / 2).  q_out may be q."},
+     "instead of (i, i + rot_dim / 2).  q_out may be q.\n\n"
+     "axes (bytes or a sequence of rot_dim / 2 small integers): pair i is turned by\n"
+     "positions[axes[i]], positions being int32 [n_axes, T], at most four axes.  A cache\n"
+     "with scales of blocks: the tokens that share a block follow one another."},
+    {"moe_quant_e4m3", FAST(py_quant),
+     "moe_quant_e4m3(x, y, scale, stream=None)\n--\n\n"
+     "y = x / scale in float8_e4m3fn, scale the largest |x| / 448 of each 128 elements.\n\n"
+     "x [T, K] bfloat16, float16 or float32; y [T, K] float8_e4m3fn; scale fp32\n"
+     "[T, ceil(K / 128)]."},
     {"moe_kv_attend", FAST(py_attend),
      "moe_kv_attend(kv, q, page_table, lengths, out, scale=None, window=0, lse=None, stream=None)\n--\n\n"
      "Attention of one query token per sequence over the cache.\n\n"
@@ -426,6 +534,13 @@ PyMethodDef methods[] = {
      "x_scale fp32 [T] and w_scale fp32 [N]; y [T, N] bfloat16, float16 or float32;\n"
      "bias [N]; residual [T, N] of y's type (may be y); act 'none', 'relu', 'silu' or\n"
      "'gelu' (exact); status int32 [1], set to MOE_ERR_TIMEOUT if a device wait ran out."},
+    {"moe_linear_blocks", FAST(py_linear_blocks),
+     "moe_linear_blocks(x, w, y, x_scale, w_scale, bias=None, act='none', residual=None, status=None, "
+     "stream=None)\n--\n\n"
+     "y = act(sum over blocks g of 128 elements of K of x_scale[t, g] * w_scale[n // 128, g] *\n"
+     "(x w^T of block g) + bias) + residual.\n\n"
+     "x [T, K] and w [N, K] float8_e4m3fn; x_scale fp32 [T, ceil(K / 128)]; w_scale fp32\n"
+     "[ceil(N / 128), ceil(K / 128)]; the rest as moe_linear."},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_decoder_ops", "Entry points of the decoder-layer operators.", -1, methods,
@@ -444,7 +559,11 @@ PyMODINIT_FUNC PyInit__decoder_ops() {
     PyObject* attr[8];
     if (!intern(attr, {"dtype", "shape", "stride", "data_ptr", "get_device", "device_index", "cuda_stream", "_call"}) ||
         !intern(n_norm, {"x", "weight", "y", "residual", "sum_out", "scale", "eps", "stream"}) ||
-        !intern(n_append, {"kv", "q", "k", "v", "positions", "slots", "cos_sin", "q_out", "interleaved", "stream"}) ||
+        !intern(n_append, {"kv", "q", "k", "v", "positions", "slots", "cos_sin", "q_out", "interleaved", "stream",
+                           "axes"}) ||
+        !intern(n_quant, {"x", "y", "scale", "stream"}) ||
+        !intern(n_linear_blocks,
+                {"x", "w", "y", "x_scale", "w_scale", "bias", "act", "residual", "status", "stream"}) ||
         !intern(n_attend, {"kv", "q", "page_table", "lengths", "out", "scale", "window", "lse", "stream"}) ||
         !intern(n_linear, {"x", "w", "y", "bias", "act", "residual", "x_scale", "w_scale", "status", "stream"}) ||
         !intern(g_acts, {"none", "relu", "silu", "gelu"}))

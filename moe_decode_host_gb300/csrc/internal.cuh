@@ -222,15 +222,39 @@ struct NormArgs {
 };
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);
 
+// Rows to E4M3 with a scale for each kScaleGroup elements.
+constexpr int kScaleGroup = 128;
+struct QuantArgs {
+    const void* x;
+    int x_type;
+    int64_t x_stride;
+    int T, K;
+    void* y;
+    int64_t y_stride;
+    float* scale;  // [T][ceil(K / kScaleGroup)], rows scale_stride apart
+    int64_t scale_stride;
+};
+cudaError_t launch_quant(const QuantArgs& a, cudaStream_t st);
+
 // A paged cache as the kernels see it.
 struct KvView {
     void *k, *v;
-    const float *k_scale, *v_scale;  // [kv_heads], E4M3 caches only, else null
+    float *k_scale, *v_scale;  // E4M3 caches only, else null: [kv_heads], or [n_pages][blocks][kv_heads]
     int type;
     int n_pages, page_size, kv_heads, q_heads, head_dim;
     int64_t page_stride, token_stride, head_stride;
     int* status;
+    int scale_tokens;     // tokens of a block of scales, a divisor of page_size; 0: a scale a head
+    int blocks;           // of a page
+    uint32_t block_mul;   // entry / scale_tokens = entry * block_mul >> 32 for entry < 2^16 (scale_tokens > 1)
 };
+// The block of scales that entry `e` of a page lies in.
+__host__ __device__ __forceinline__ int block_of(const KvView& kv, int e) {
+    return kv.scale_tokens == 1 ? e : (int)((uint64_t)(uint32_t)e * kv.block_mul >> 32);
+}
+
+constexpr int kMaxAxes = 4;      // of a token's position
+constexpr int kMaxScaleTokens = 1024;
 
 struct AppendArgs {
     KvView kv;
@@ -244,8 +268,16 @@ struct AppendArgs {
     void* q_out;
     int64_t qo_ts, qo_hs;
     int sm_count;
+    int axes;            // of a position; axis i of token t is positions[i * pos_stride + t]
+    int64_t pos_stride;
+    uint32_t axis[8];    // of each pair, two bits: pair i in bits 2 (i % 16) of word i / 16 (axes > 1)
 };
+__host__ __device__ __forceinline__ int axis_of(const AppendArgs& a, int pair) {
+    return (int)(a.axis[pair >> 4] >> (2 * (pair & 15)) & 3u);
+}
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st);
+// The same on a cache with a scale for each block of tokens and head.
+cudaError_t launch_append_blocks(const AppendArgs& a, cudaStream_t st);
 
 struct AttendArgs {
     KvView kv;
@@ -288,5 +320,8 @@ struct LinearArgs {
     int sm_count;
 };
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t st);
+// E4M3 operands with x_scale [T][G] and w_scale [ceil(N / 128)][G], G = ceil(K / 128), rows xs_stride
+// and ws_stride apart.
+cudaError_t launch_linear_blocks(const LinearArgs& a, int64_t xs_stride, int64_t ws_stride, cudaStream_t st);
 
 }  // namespace moe

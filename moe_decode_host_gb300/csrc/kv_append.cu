@@ -18,8 +18,7 @@
 // us (5.8 TB/s, 85% of a plain copy's rate); 8 tokens 2.8 us.
 #include <algorithm>
 
-#include "ptx.cuh"
-#include "vec.cuh"
+#include "kv_append.cuh"
 
 namespace moe {
 namespace {
@@ -27,52 +26,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kHeads = 4;
 constexpr int kStages = 2;  // three leave an SM fewer CTAs: 38.8 us instead of 32.3 for 8192 tokens into E4M3
-
-// Element offsets of item j's two runs in a head, and whether it is rotated (else copied).
-template <int VEC>
-struct Item {
-    int j, e0, e1;
-    bool turn;
-    __device__ __forceinline__ Item(const AppendArgs& a, int item) : j(item) {
-        const int half = a.rot / 2;
-        turn = j * VEC < half;
-        e0 = !turn || a.interleaved ? 2 * j * VEC : j * VEC;
-        e1 = !turn || a.interleaved ? e0 + VEC : e0 + half;
-    }
-};
-
-// Head h of a token: 0 query, 1 key, 2 value, and its number there.
-__device__ __forceinline__ int kind_of(const AppendArgs& a, int h, int& n) {
-    const int hq = a.kv.q_heads, hkv = a.kv.kv_heads;
-    const int kind = h < hq ? 0 : (h < hq + hkv ? 1 : 2);
-    n = kind == 0 ? h : (kind == 1 ? h - hq : h - hq - hkv);
-    return kind;
-}
-__device__ __forceinline__ const void* source(const AppendArgs& a, int64_t t, int h, int64_t& at) {
-    int n;
-    const int kind = kind_of(a, h, n);
-    at = kind == 0 ? t * a.q_ts + n * a.q_hs : kind == 1 ? t * a.k_ts + n * a.k_hs : t * a.v_ts + n * a.v_hs;
-    return kind == 0 ? a.q : (kind == 1 ? a.k : a.v);
-}
-
-// Where a token goes: its offset in the cache, or put = false.
-struct Slot {
-    int64_t at;
-    bool put;
-};
-__device__ __forceinline__ Slot slot_of(const AppendArgs& a, int64_t slot, bool tell) {
-    Slot s{0, slot >= 0};  // a negative slot: the token is not appended
-    if (s.put) {
-        const int64_t page = slot >> 32 ? slot / a.kv.page_size : (uint32_t)slot / (uint32_t)a.kv.page_size;
-        if (page >= a.kv.n_pages) {
-            s.put = false;
-            if (tell) set_status(a.kv.status, MOE_ERR_BAD_INDEX);
-        } else {
-            s.at = page * a.kv.page_stride + (slot - page * a.kv.page_size) * a.kv.token_stride;
-        }
-    }
-    return s;
-}
 
 // The scale of head h's values in an E4M3 cache, and what they are multiplied by on their way there.
 __device__ __forceinline__ float scale_of(const AppendArgs& a, int h) {
@@ -93,32 +46,7 @@ __device__ __forceinline__ void finish(const AppendArgs& a, int64_t t, int h, co
     float x0[VEC], x1[VEC];
     r0.get(xt, x0);
     r1.get(xt, x1);
-    if (it.turn && kind != 2) {
-        if (a.interleaved) {
-            // pair i is elements 2i, 2i + 1 of the double run
-            if constexpr (VEC == 1) {
-                const float p = x0[0], q = x1[0];
-                x0[0] = p * cs[0] - q * sn[0];
-                x1[0] = p * sn[0] + q * cs[0];
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC / 2; ++i) {
-                    const float p = x0[2 * i], q = x0[2 * i + 1], u = x1[2 * i], v = x1[2 * i + 1];
-                    x0[2 * i] = p * cs[i] - q * sn[i];
-                    x0[2 * i + 1] = p * sn[i] + q * cs[i];
-                    x1[2 * i] = u * cs[VEC / 2 + i] - v * sn[VEC / 2 + i];
-                    x1[2 * i + 1] = u * sn[VEC / 2 + i] + v * cs[VEC / 2 + i];
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float p = x0[i], q = x1[i];
-                x0[i] = p * cs[i] - q * sn[i];
-                x1[i] = p * sn[i] + q * cs[i];
-            }
-        }
-    }
+    if (it.turn && kind != 2) rotate<VEC>(a.interleaved, x0, x1, cs, sn);
     if (kind == 0) {
         store_run<VEC>(a.q_out, t * a.qo_ts + n * a.qo_hs + it.e0, xt, x0);
         store_run<VEC>(a.q_out, t * a.qo_ts + n * a.qo_hs + it.e1, xt, x1);
@@ -155,21 +83,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
     const int step = blockDim.x / items, g = threadIdx.x / items;
     if (g >= step) return;
     const Item<VEC> it(a, threadIdx.x % items);
-    const int pos = a.rot > 0 ? a.positions[t] : 0;
-    if (a.rot > 0 && (pos < 0 || pos >= a.n_positions)) {  // no table row: nothing of this token is written
+    const Place place = place_of(a, t);
+    if (!place.valid) {  // no table row: nothing of this token is written
         if (threadIdx.x == 0) set_status(a.kv.status, MOE_ERR_BAD_INDEX);
         return;
     }
     const Slot slot = slot_of(a, a.slots[t], threadIdx.x == 0);
     float cs[VEC], sn[VEC];
-    if (it.turn) {
-        const float* row = a.cos_sin + (int64_t)pos * a.rot + it.j * VEC;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            cs[i] = row[i];
-            sn[i] = row[a.rot / 2 + i];
-        }
-    }
+    if (it.turn) turn_of<VEC>(a, place, it.j * VEC, cs, sn);
     for (int h = g; h < heads; h += step) {
         int64_t at;
         const void* src = source(a, t, h, at);
@@ -187,8 +108,9 @@ __device__ __forceinline__ void cp_async16_l1(uint4* dst, const void* src) {  //
 // 16-bit q, k and v in runs of 8, the cache of their type (CT = XT) or E4M3.  CTAs walk the
 // (token, block of heads) pairs; a thread's runs and table entries of the next pair come
 // through a ring in shared memory that it alone reads, and the position that a copy of the
-// table needs is fetched one step before.
-template <int XT, int CT>
+// table needs is fetched one step before.  AX: 0 a position is one number; 1 it has axes, and
+// aligned fours of pairs have one axis each; 2 any pair any axis, its entries copied one by one.
+template <int XT, int CT, int AX>
 __global__ void __launch_bounds__(kThreads) append_ring_kernel(const AppendArgs a) {
     constexpr int VEC = 8, kPieces = 2 * kHeads + 4;
     extern __shared__ uint4 ring[];  // [stage][piece][thread]
@@ -202,9 +124,16 @@ __global__ void __launch_bounds__(kThreads) append_ring_kernel(const AppendArgs 
     const int64_t total = (int64_t)a.T * blocks;
     auto token = [&](int64_t n) { return blocks == 1 ? n : n / blocks; };
     auto piece = [&](int stage, int i) { return ring + (stage * kPieces + i) * blockDim.x + threadIdx.x; };
-    auto position = [&](int64_t n) { return a.rot > 0 && n < total ? a.positions[token(n)] : 0; };
-    auto valid = [&](int pos) { return a.rot == 0 || (pos >= 0 && pos < a.n_positions); };
-    auto copy = [&](int64_t n, int pos, int stage) {
+    auto position = [&](int64_t n) {
+        if constexpr (AX == 0) return a.rot > 0 && n < total ? a.positions[token(n)] : 0;
+        else return n < total ? place_of(a, token(n)) : Place{{0, 0, 0, 0}, false};
+    };
+    using Position = decltype(position(0));
+    auto valid = [&](const Position& pos) {
+        if constexpr (AX == 0) return a.rot == 0 || (pos >= 0 && pos < a.n_positions);
+        else return pos.valid;
+    };
+    auto copy = [&](int64_t n, const Position& pos, int stage) {
         if (n < total) {
             const int64_t t = token(n);
             const int h0 = (int)(n - t * blocks) * step * kHeads + g;
@@ -218,16 +147,33 @@ __global__ void __launch_bounds__(kThreads) append_ring_kernel(const AppendArgs 
                 cp_async16(piece(stage, 2 * i + 1), src + at + it.e1);
             }
             if (it.turn && valid(pos)) {
-                const float* row = a.cos_sin + (int64_t)pos * a.rot + it.j * VEC;
+                if constexpr (AX == 0) {
+                    const float* row = a.cos_sin + (int64_t)pos * a.rot + it.j * VEC;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) cp_async16_l1(piece(stage, 2 * kHeads + i), row + (i & 1) * 4 + (i >> 1) * (a.rot / 2));
+                    for (int i = 0; i < 4; ++i) cp_async16_l1(piece(stage, 2 * kHeads + i), row + (i & 1) * 4 + (i >> 1) * (a.rot / 2));
+                } else if constexpr (AX == 1) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int pair = it.j * VEC + (i & 1) * 4;
+                        cp_async16_l1(piece(stage, 2 * kHeads + i), a.cos_sin + (int64_t)pos.at(axis_of(a, pair)) * a.rot + pair +
+                                                                        (i >> 1) * (a.rot / 2));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const int pair = it.j * VEC + i;
+                        const float* at = a.cos_sin + (int64_t)pos.at(axis_of(a, pair)) * a.rot + pair;
+                        cp_async4(reinterpret_cast<float*>(piece(stage, 2 * kHeads + (i >> 2))) + (i & 3), at);
+                        cp_async4(reinterpret_cast<float*>(piece(stage, 2 * kHeads + 2 + (i >> 2))) + (i & 3), at + a.rot / 2);
+                    }
+                }
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     int64_t n = blockIdx.x;
     // positions and slots of this step and the next ones
-    int pos[kStages];
+    Position pos[kStages];
     int64_t slots[kStages];
     auto look = [&](int64_t m, int i) {
         pos[i] = position(m);
@@ -243,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) append_ring_kernel(const AppendArgs 
         copy(n + (int64_t)(kStages - 1) * gridDim.x, pos[kStages - 1], stage == 0 ? kStages - 1 : stage - 1);
         const int64_t t = token(n);
         const int h0 = (int)(n - t * blocks) * step * kHeads + g;
-        const int p0 = pos[0];
+        const Position p0 = pos[0];
         const Slot slot = slot_of(a, slots[0], threadIdx.x == 0);
 #pragma unroll
         for (int i = 0; i + 1 < kStages; ++i) {
@@ -284,13 +230,6 @@ __global__ void __launch_bounds__(kThreads) append_ring_kernel(const AppendArgs 
     }
 }
 
-// Whether every run of `vec` elements of the call is aligned, and the table's too.
-bool fits(const AppendArgs& a, int vec) {
-    return a.rot / 2 % vec == 0 && a.kv.head_dim % (2 * vec) == 0 && runs_aligned(a.q, a.type, vec, a.q_ts, a.q_hs) &&
-           runs_aligned(a.k, a.type, vec, a.k_ts, a.k_hs) && runs_aligned(a.v, a.type, vec, a.v_ts, a.v_hs) &&
-           runs_aligned(a.q_out, a.type, vec, a.qo_ts, a.qo_hs);
-}
-
 int threads_of(const AppendArgs& a, int vec, int each) {  // one item of `each` heads a thread
     const int items = a.kv.head_dim / (2 * vec), heads = a.kv.q_heads + 2 * a.kv.kv_heads;
     return std::min(kThreads, (items * ((heads + each - 1) / each) + 31) / 32 * 32);
@@ -301,9 +240,9 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
     return launch_pdl(append_kernel<VEC>, dim3(a.T), dim3(threads_of(a, VEC, 2)), 0, st, a);
 }
 
-template <int XT, int CT>
-cudaError_t launch_ring(const AppendArgs& a, cudaStream_t st) {
-    const auto kernel = append_ring_kernel<XT, CT>;
+template <int XT, int CT, int AX>
+cudaError_t launch_ring_axes(const AppendArgs& a, cudaStream_t st) {
+    const auto kernel = append_ring_kernel<XT, CT, AX>;
     const int threads = threads_of(a, 8, kHeads), warps = threads / 32;
     const int smem = kStages * (2 * kHeads + 4) * threads * 16;
     static std::atomic<uint64_t> configured;
@@ -324,17 +263,23 @@ cudaError_t launch_ring(const AppendArgs& a, cudaStream_t st) {
     return launch_pdl(kernel, dim3((unsigned)grid), dim3(threads), smem, st, a);
 }
 
+template <int XT, int CT>
+cudaError_t launch_ring(const AppendArgs& a, cudaStream_t st) {
+    if (a.axes == 1) return launch_ring_axes<XT, CT, 0>(a, st);
+    return one_axis_fours(a) ? launch_ring_axes<XT, CT, 1>(a, st) : launch_ring_axes<XT, CT, 2>(a, st);
+}
+
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
     const bool table16 = a.rot == 0 || (reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0 && a.rot % 8 == 0);
-    if (fits(a, 8) && table16 && is_float16(a.type) && (a.kv.type == a.type || a.kv.type == MOE_E4M3)) {
+    if (append_fits(a, 8) && table16 && is_float16(a.type) && (a.kv.type == a.type || a.kv.type == MOE_E4M3)) {
         if (a.type == MOE_BF16)
             return a.kv.type == MOE_BF16 ? launch_ring<MOE_BF16, MOE_BF16>(a, st) : launch_ring<MOE_BF16, MOE_E4M3>(a, st);
         return a.kv.type == MOE_F16 ? launch_ring<MOE_F16, MOE_F16>(a, st) : launch_ring<MOE_F16, MOE_E4M3>(a, st);
     }
-    return fits(a, 8) ? launch<8>(a, st) : fits(a, 4) ? launch<4>(a, st) : launch<1>(a, st);
+    return append_fits(a, 8) ? launch<8>(a, st) : append_fits(a, 4) ? launch<4>(a, st) : launch<1>(a, st);
 }
 
 }  // namespace moe

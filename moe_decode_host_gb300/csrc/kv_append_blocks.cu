@@ -1,0 +1,303 @@
+// Position rotation and append to an E4M3 cache with a scale for each block of tokens and head.
+//
+//   scale = 2^e, e the smallest with max |values| <= 448 * 2^e;  code = E4M3(value / scale)
+//
+// over the values that the call puts into the block; a block that had tokens keeps its scale if
+// that is as large, and else its other codes are rewritten under the new one.  Powers of two lose
+// nothing in the rewriting but low bits of codes that become subnormal, and E4M3 has as many bits
+// under them as under any other scale.
+//
+// Memory bound: q, k, v in, q_out and the codes out, each once.  The tokens of a block follow one
+// another in the call, so a team of threads (a warp where blocks are short, else four) takes what
+// the call puts into one block of one head of k or v: it turns the values, keeps them in registers
+// while their maximum is found, and writes codes and scale.  Teams look for the blocks that begin
+// in their window of tokens, so nothing has to be counted or sorted beforehand.  The queries are
+// turned by further CTAs of the same launch.
+#include <algorithm>
+
+#include "kv_append.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kKeep = 4;   // tokens a thread keeps in registers
+constexpr int kAny = -1;   // a type known only at run time
+
+// The smallest power of two s with top <= 448 s, from 2^-126 to 2^119.  448 = 1.75 * 2^8.
+__device__ __forceinline__ float scale_for(float top) {
+    const uint32_t b = __float_as_uint(top);
+    int e = (int)(b >> 23) + ((b & 0x7fffffu) > 0x600000u ? 1 : 0) - 8;  // biased
+    e = e < 1 ? 1 : (e > 127 + 119 ? 127 + 119 : e);
+    return __uint_as_float((uint32_t)e << 23);
+}
+
+// The block that a slot lies in, as the slot of its first entry; negative: the token is not appended.
+struct Home {
+    int64_t first;
+    int page, entry;  // of the slot
+};
+__device__ __forceinline__ Home home_of(const AppendArgs& a, int64_t slot) {
+    Home h{-1, 0, 0};
+    if (slot < 0) return h;
+    const int64_t page = slot >> 32 ? slot / a.kv.page_size : (int64_t)((uint32_t)slot / (uint32_t)a.kv.page_size);
+    if (page >= a.kv.n_pages) {
+        set_status(a.kv.status, MOE_ERR_BAD_INDEX);
+        return h;
+    }
+    h.page = (int)page;
+    h.entry = (int)(slot - page * a.kv.page_size);
+    h.first = slot - h.entry + (int64_t)block_of(a.kv, h.entry) * a.kv.scale_tokens;
+    return h;
+}
+
+// Four codes as fp32.
+__device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float (&v)[4]) {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
+
+// TEAM threads, 32 or all of the CTA.
+template <int TEAM>
+__device__ __forceinline__ void team_sync() {
+    if constexpr (TEAM == 32) __syncwarp();
+    else __syncthreads();
+}
+
+// A team's share of k and v: the blocks that begin among `window` tokens from w0 on (at most 32), of
+// head `head` of k (side 0) or v (side 1).
+template <int XT, int VEC, int TEAM, bool FOURS>
+__device__ __forceinline__ void append_block_runs(const AppendArgs& a, int64_t w0, int window, int side, int head,
+                                                  uint32_t* mask, float (*part)[kThreads / 32]) {
+    const int me = threadIdx.x % TEAM, lane = threadIdx.x & 31;
+    const int items = a.kv.head_dim / (2 * VEC), step = TEAM / items, g = me / items;
+    const bool works = g < step;
+    const Item<VEC> it(a, me % items);
+    const int xt = XT == kAny ? a.type : XT;
+    const void* src = side ? a.v : a.k;
+    const int64_t ts = side ? a.v_ts : a.k_ts, hs = side ? a.v_hs : a.k_hs;
+    uint8_t* cache = static_cast<uint8_t*>(side ? a.kv.v : a.kv.k) + head * a.kv.head_stride;
+    float* scales = side ? a.kv.v_scale : a.kv.k_scale;
+    // lane i: the home of token w0 + i; a run begins where it differs from the token before
+    const int64_t mine = lane < window && w0 + lane < a.T ? home_of(a, a.slots[w0 + lane]).first : -1;
+    int64_t before = __shfl_up_sync(0xffffffffu, mine, 1);
+    if (lane == 0) before = w0 > 0 ? home_of(a, a.slots[w0 - 1]).first : -1;
+    uint32_t begins = __ballot_sync(0xffffffffu, mine >= 0 && mine != before);
+    while (begins) {  // the same in every warp of the team
+        const int i0 = __ffs(begins) - 1;
+        begins &= begins - 1;
+        const int64_t t0 = w0 + i0, first = __shfl_sync(0xffffffffu, mine, i0);
+        // the run's end: the next token of another home, maybe behind the window
+        const uint32_t others = __ballot_sync(0xffffffffu, lane > i0 && mine != first);
+        int64_t t1 = others ? w0 + __ffs(others) - 1 : w0 + 32;
+        if (!others || t1 >= w0 + window) {
+            t1 = w0 + window;
+            for (bool on = true; on && t1 < a.T;) {
+                const int64_t t = t1 + lane;
+                const uint32_t same = __ballot_sync(0xffffffffu, t < a.T && home_of(a, a.slots[t]).first == first);
+                on = same == 0xffffffffu;
+                t1 += on ? 32 : __ffs(~same) - 1;
+            }
+            if (t1 > a.T) t1 = a.T;
+        }
+        const Home home = home_of(a, first);
+        const int64_t base = (int64_t)home.page * a.kv.page_stride + (int64_t)home.entry * a.kv.token_stride;
+        float* scale_at = scales + ((int64_t)home.page * a.kv.blocks + block_of(a.kv, home.entry)) * a.kv.kv_heads + head;
+        const float old = *scale_at;
+
+        // a token's values, turned; false: not appended
+        auto fetch = [&](int64_t t, float (&x0)[VEC], float (&x1)[VEC], int& entry) {
+            const Place place = place_of(a, t);
+            entry = (int)(a.slots[t] - first);
+            if (!place.valid) {
+                set_status(a.kv.status, MOE_ERR_BAD_INDEX);
+                return false;
+            }
+            Raw<VEC, XT == kAny || XT == MOE_F32> r0, r1;
+            r0.load(src, t * ts + head * hs + it.e0, xt);
+            r1.load(src, t * ts + head * hs + it.e1, xt);
+            float cs[VEC], sn[VEC];
+            const bool turn = it.turn && side == 0;
+            if (turn) turn_of<VEC, FOURS>(a, place, it.j * VEC, cs, sn);
+            r0.get(xt, x0);
+            r1.get(xt, x1);
+            if (turn) rotate<VEC>(a.interleaved, x0, x1, cs, sn);
+            return true;
+        };
+        float x[kKeep][2][VEC];
+        int at[kKeep];  // entries, or -1
+        float top = 0.f;
+        bool anew = false;
+        auto see = [&](const float (&x0)[VEC], const float (&x1)[VEC], int entry) {
+            anew = anew || entry == 0;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) top = fmaxf(top, fmaxf(fabsf(x0[i]), fabsf(x1[i])));  // NaN does not count
+        };
+#pragma unroll
+        for (int k = 0; k < kKeep; ++k) {
+            const int64_t t = t0 + g + (int64_t)k * step;
+            at[k] = -1;
+            int entry;
+            if (works && t < t1 && fetch(t, x[k][0], x[k][1], entry)) {
+                at[k] = entry;
+                see(x[k][0], x[k][1], entry);
+            }
+        }
+        for (int64_t t = t0 + g + (int64_t)kKeep * step; works && t < t1; t += step) {
+            float y0[VEC], y1[VEC];
+            int entry;
+            if (fetch(t, y0, y1, entry)) see(y0, y1, entry);
+        }
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // not negative: ordered as its bits
+        anew = __any_sync(0xffffffffu, anew);
+        if constexpr (TEAM > 32) {
+            if (lane == 0) {
+                part[0][threadIdx.x >> 5] = top;
+                part[1][threadIdx.x >> 5] = anew ? 1.f : 0.f;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < TEAM / 32; ++w) {
+                top = fmaxf(top, part[0][w]);
+                anew = anew || part[1][w] != 0.f;
+            }
+        }
+        const float need = scale_for(top);
+        const float scale = anew || !(old >= need) ? need : old;
+        const float inv = 1.f / scale;
+        auto put = [&](const float (&x0)[VEC], const float (&x1)[VEC], int entry) {
+            float y0[VEC], y1[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                y0[i] = x0[i] * inv;
+                y1[i] = x1[i] * inv;
+            }
+            const int64_t to = base + (int64_t)entry * a.kv.token_stride;
+            store_run<VEC>(cache, to + it.e0, MOE_E4M3, y0);
+            store_run<VEC>(cache, to + it.e1, MOE_E4M3, y1);
+        };
+#pragma unroll
+        for (int k = 0; k < kKeep; ++k)
+            if (at[k] >= 0) put(x[k][0], x[k][1], at[k]);
+        for (int64_t t = t0 + g + (int64_t)kKeep * step; works && t < t1; t += step) {
+            float y0[VEC], y1[VEC];
+            int entry;
+            if (fetch(t, y0, y1, entry)) put(y0, y1, entry);
+        }
+        if (!anew && scale != old) {  // the block's other entries keep their values
+            const int n = a.kv.scale_tokens;
+            for (int i = me; i < (n + 31) / 32; i += TEAM) mask[i] = 0;
+            team_sync<TEAM>();
+            for (int64_t t = t0 + me; t < t1; t += TEAM)
+                if (place_of(a, t).valid) {
+                    const int entry = (int)(a.slots[t] - first);
+                    atomicOr(mask + (entry >> 5), 1u << (entry & 31));
+                }
+            team_sync<TEAM>();
+            const float factor = old * inv;
+            const int pieces = a.kv.head_dim / 16;
+            for (int i = me; i < n * pieces; i += TEAM) {
+                const int entry = i / pieces;
+                if (mask[entry >> 5] >> (entry & 31) & 1u) continue;
+                uint4* p = reinterpret_cast<uint4*>(cache + base + (int64_t)entry * a.kv.token_stride) + i % pieces;
+                uint4 w = *p;
+                auto again = [&](uint32_t& c) {
+                    float v[4];
+                    e4m3x4_to_f32(c, v);
+                    c = pack_e4m3(v[0] * factor, v[1] * factor) | pack_e4m3(v[2] * factor, v[3] * factor) << 16;
+                };
+                again(w.x), again(w.y), again(w.z), again(w.w);
+                *p = w;
+            }
+        }
+        team_sync<TEAM>();  // the parts and the mask are free, and every thread has read the old scale
+        if (me == 0) *scale_at = scale;
+    }
+}
+
+// The first CTAs take k and v, a team per (window of tokens, head of either); the others a token's
+// queries each.
+template <int XT, int VEC, int TEAM, bool FOURS>
+__global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendArgs a, int window, int kv_ctas) {
+    __shared__ uint32_t mask[kThreads / TEAM][kMaxScaleTokens / 32];
+    __shared__ float part[2][kThreads / 32];
+    grid_launch_next();
+    grid_dep_wait();
+    const int xt = XT == kAny ? a.type : XT;
+    if ((int)blockIdx.x < kv_ctas) {
+        const int heads = 2 * a.kv.kv_heads;
+        const int64_t unit = (int64_t)blockIdx.x * (kThreads / TEAM) + threadIdx.x / TEAM;
+        const int64_t w = unit / heads;
+        const int h = (int)(unit - w * heads);
+        if (w * window < a.T)  // a team of one warp leaves alone; a CTA's has the same w
+            append_block_runs<XT, VEC, TEAM, FOURS>(a, w * window, window, h >= a.kv.kv_heads, h % a.kv.kv_heads,
+                                                    mask[threadIdx.x / TEAM], part);
+        return;
+    }
+    const int64_t t = blockIdx.x - kv_ctas;
+    const int items = a.kv.head_dim / (2 * VEC), step = kThreads / items, g = threadIdx.x / items;
+    if (g >= step) return;
+    const Item<VEC> it(a, threadIdx.x % items);
+    const Place place = place_of(a, t);
+    if (!place.valid) {  // no table row: nothing of this token is written
+        if (threadIdx.x == 0) set_status(a.kv.status, MOE_ERR_BAD_INDEX);
+        return;
+    }
+    float cs[VEC], sn[VEC];
+    if (it.turn) turn_of<VEC, FOURS>(a, place, it.j * VEC, cs, sn);
+#pragma unroll 2
+    for (int h = g; h < a.kv.q_heads; h += step) {
+        Raw<VEC, XT == kAny || XT == MOE_F32> r0, r1;
+        r0.load(a.q, t * a.q_ts + h * a.q_hs + it.e0, xt);
+        r1.load(a.q, t * a.q_ts + h * a.q_hs + it.e1, xt);
+        float x0[VEC], x1[VEC];
+        r0.get(xt, x0);
+        r1.get(xt, x1);
+        if (it.turn) rotate<VEC>(a.interleaved, x0, x1, cs, sn);
+        store_run<VEC>(a.q_out, t * a.qo_ts + h * a.qo_hs + it.e0, xt, x0);
+        store_run<VEC>(a.q_out, t * a.qo_ts + h * a.qo_hs + it.e1, xt, x1);
+    }
+}
+
+template <int XT, int VEC, int TEAM, bool FOURS>
+cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
+    // windows of a token while there are CTAs for them all, so that sequences' tokens go to teams of
+    // their own; else as long as a block, where most windows begin one
+    const int64_t units = (int64_t)a.T * 2 * a.kv.kv_heads;
+    const int window = units <= 4096 ? 1 : std::min(32, a.kv.scale_tokens);
+    const int64_t teams = ((int64_t)a.T + window - 1) / window * 2 * a.kv.kv_heads, per = kThreads / TEAM;
+    const int64_t kv_ctas = (teams + per - 1) / per;
+    if (kv_ctas + a.T > 0x7fffffff) return cudaErrorInvalidValue;
+    return launch_pdl(append_blocks_kernel<XT, VEC, TEAM, FOURS>, dim3((unsigned)(kv_ctas + a.T)), dim3(kThreads), 0, st, a,
+                      window, (int)kv_ctas);
+}
+
+template <int XT, int TEAM>
+cudaError_t launch_fours(const AppendArgs& a, cudaStream_t st) {
+    return fours_of(a) ? launch<XT, 8, TEAM, true>(a, st) : launch<XT, 8, TEAM, false>(a, st);
+}
+
+template <int XT>
+cudaError_t launch_team(const AppendArgs& a, cudaStream_t st) {
+    // a warp turns 512 / head_dim tokens at a time: few for a long block, which four warps share
+    return a.kv.scale_tokens <= 8 ? launch_fours<XT, 32>(a, st) : launch_fours<XT, kThreads>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_append_blocks(const AppendArgs& a, cudaStream_t st) {
+    if (a.T == 0) return cudaSuccess;
+    if (append_fits(a, 8)) {
+        if (a.type == MOE_BF16) return launch_team<MOE_BF16>(a, st);
+        if (a.type == MOE_F16) return launch_team<MOE_F16>(a, st);
+        return launch_team<MOE_F32>(a, st);
+    }
+    return append_fits(a, 4) ? launch<kAny, 4, kThreads, false>(a, st) : launch<kAny, 1, kThreads, false>(a, st);
+}
+
+}  // namespace moe

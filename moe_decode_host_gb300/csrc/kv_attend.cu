@@ -37,7 +37,8 @@ AttendPlan plan_of(const KvView& kv, int sm_count) {
     // as many units in flight as fit beside the other CTAs of the SM; the ring also holds the
     // warp's [hc][head_dim + 4] sums when a piece ends, and when a segment is joined the parts'
     // weights (hc * slots floats at most) with the sums of one part or more (hc * head_dim floats)
-    const int unit = 2 * unit_tokens(p.dp * es) * p.pitch, fixed = hc * (p.dp * 2 + 16) + 16;
+    const int tokens = unit_tokens(p.dp * es);
+    const int unit = 2 * tokens * p.pitch + (kv.scale_tokens ? scale_bytes(tokens) : 0), fixed = hc * (p.dp * 2 + 16) + 16;
     const int least = std::max((hc * (D + 4) * 4 + unit - 1) / unit,
                                (hc * (p.slots + D) * 4 + kAttendWarps * unit - 1) / (kAttendWarps * unit));
     p.stages = kMaxStages;
@@ -66,7 +67,7 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     const AttendPlan p = plan_of(a.kv, a.sm_count);
     if (a.kv.type == MOE_BF16) return launch_attend_bf16(a, p, st);
     if (a.kv.type == MOE_F16) return launch_attend_f16(a, p, st);
-    return launch_attend_e4m3(a, p, st);
+    return a.kv.scale_tokens ? launch_attend_e4m3_blocks(a, p, st) : launch_attend_e4m3(a, p, st);
 }
 
 }  // namespace moe

@@ -100,6 +100,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// 4 bytes, or a zero where `bytes` is 0.
+__device__ __forceinline__ void cp_4(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
 // What a part with maximum m counts under the joint maximum (a part may have seen nothing).
 __device__ __forceinline__ float part_weight(float m, float top) { return m == -INFINITY ? 0.f : fast_exp2(m - top); }
 
@@ -135,13 +140,13 @@ __device__ __forceinline__ int places_of(const Span& s, int unit) {
     return s.count > 0 ? (s.count + unit - 1) / unit + kStart : 0;
 }
 
-// T: 0 bf16, 1 f16, 2 E4M3 (computed in f16).  DP: head_dim (EXACT) or a bound of it; with
+// T: 0 bf16, 1 f16, 2 E4M3 (computed in f16), 3 E4M3 with a scale for each block of tokens.  DP: head_dim (EXACT) or a bound of it; with
 // the dimension known no step of the products is conditional, and they overlap.  NT: blocks
 // of 8 query heads.
 template <int T, int DP, int NT, bool EXACT>
-__global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
+__global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T >= 2 ? 1 : 2, NT))
     attend_kernel(const AttendArgs a, const AttendPlan p) {
-    constexpr bool BF = T == 0, F8 = T == 2;
+    constexpr bool BF = T == 0, F8 = T >= 2, BLOCKS = T == 3;
     constexpr float lift = BF ? 0.f : kLift;
     constexpr int HC = 8 * NT;
     constexpr int ES = F8 ? 1 : 2;
@@ -159,7 +164,8 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
     const int qpitch = D * 2 + 16;
     const int pitch = EXACT ? row_pitch(CPR) : p.pitch, swizzle = EXACT ? row_swizzle(CPR) : p.swizzle;
     const int cpr = EXACT ? CPR : p.cpr;
-    const int unit_bytes = 2 * U * pitch;
+    // behind a unit's rows the scales of its tokens' keys, then of its values
+    const int unit_bytes = 2 * U * pitch + (BLOCKS ? scale_bytes(U) : 0);
     uint8_t* s_q = smem;
     uint8_t* ring = smem + HC * (DP * 2 + 16) + warp * p.stages * unit_bytes;
     const uint32_t ring_u = smem_u32(ring), q_u = smem_u32(s_q);
@@ -295,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
         const uint8_t* kb = static_cast<const uint8_t*>(a.kv.k) + kh * a.kv.head_stride * ES;
         const uint8_t* vb = static_cast<const uint8_t*>(a.kv.v) + kh * a.kv.head_stride * ES;
         const int32_t* table = a.page_table + b * a.table_stride;
+        const float *k_scales = a.kv.k_scale, *v_scales = a.kv.v_scale;
         int next_page = -1, next_entry = 0;  // the page and entry of row `lane` of the next unit
         auto look_up = [&](int x) {
             const int j = (first_u + warp + kWarps * x) * U + lane;
@@ -314,6 +321,14 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                 const uint32_t mask = __ballot_sync(0xffffffffu, ok);
                 if (lane == 0) s_mask[warp][slot] = mask;
                 const uint32_t dst = ring_u + slot * unit_bytes;
+                if constexpr (BLOCKS) {
+                    if (lane < U) {
+                        const int64_t at = ok ? ((int64_t)next_page * a.kv.blocks + block_of(a.kv, next_entry)) * a.kv.kv_heads + kh : 0;
+                        const uint32_t to = dst + 2 * U * pitch + 4 * lane;
+                        cp_4(to, k_scales + at, ok ? 4u : 0u);
+                        cp_4(to + 4 * U, v_scales + at, ok ? 4u : 0u);
+                    }
+                }
                 if (EXACT && mask == kAll) {
                     static_assert(!EXACT || U * CPR % 32 == 0, "whole rounds of the warp");
                     const uint64_t unit = 1ull << p.shift;
@@ -344,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
         // queries first, so that they are on their way together with the first units
         constexpr int HW = HC / kWarps;  // heads a warp brings: warp, warp + kWarps, ...
         uint16_t raw[HW][DP / 32];
-        const float k_scale = F8 ? a.kv.k_scale[kh] : 1.f, v_scale = F8 ? a.kv.v_scale[kh] : 1.f;
+        const float k_scale = T == 2 ? a.kv.k_scale[kh] : 1.f, v_scale = T == 2 ? a.kv.v_scale[kh] : 1.f;
 #pragma unroll
         for (int x = 0; x < HW; ++x) {
             const int h = warp + kWarps * x;
@@ -405,6 +420,8 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                 sc[t][j] = s_scale[8 * t + 2 * c + j];
             }
         }
+
+        float v_ref = 0.f;  // BLOCKS: the sums are in units of it, the largest power of two in a value's scale so far
 
         // where ldmatrix lanes read.  Keys: row lane % 16 of S^T, the 16-byte piece lane / 16 further on;
         // pieces come in pairs, so piece 2j + x is in place 2j ^ (x ^ swap)
@@ -469,6 +486,41 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                     }
                 }
             }
+            float fv[MT][2];  // BLOCKS: what the weights of this lane's tokens are multiplied by
+            if constexpr (BLOCKS) {
+                const float* ks = reinterpret_cast<const float*>(ring + slot * unit_bytes + 2 * U * pitch);
+                const float* vs = ks + U;
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(vs[lane & (U - 1)]) & 0x7f800000u);
+                const float unit = __uint_as_float(top < 0x00800000u ? 0x00800000u : (top > 0x7f000000u ? 0x7f000000u : top));
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int t = 16 * i + token_of<F8>(g + 8 * h);
+                        fv[i][h] = vs[t];
+                        const float k = ks[t];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            s[i][n][2 * h] *= k;
+                            s[i][n][2 * h + 1] *= k;
+                        }
+                    }
+                if (unit > v_ref) {  // the same in all lanes
+                    const float down = v_ref / unit;
+                    v_ref = unit;
+#pragma unroll
+                    for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) o[i][n][j] *= down;
+                }
+                const float inv = 1.f / v_ref;
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) fv[i][h] *= inv;
+            }
             // softmax: lane (g, c) holds rows g, g + 8 of each tile, heads 2c, 2c + 1 of each block
             if (mask != kAll) {
 #pragma unroll
@@ -520,7 +572,9 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float x = s[i][t][2 * j], y = s[i][t][2 * j + 1];
+                        // a value's scale is below twice the reference, so that a weight stays below 2^15
+                        const float x = BLOCKS ? s[i][t][2 * j] * fv[i][j] : s[i][t][2 * j];
+                        const float y = BLOCKS ? s[i][t][2 * j + 1] * fv[i][j] : s[i][t][2 * j + 1];
                         const uint32_t p = pack(x, y);
                         pb[i][t][0][j] = transpose8x8(p);
                         pb[i][t][1][j] = transpose8x8(pack(x - low(p), y - low(p >> 16)));
@@ -603,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
                 float top = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][h]);
-                const float f = m[t][j] == -INFINITY ? 0.f : fast_exp2(m[t][j] - top);
+                const float f = m[t][j] == -INFINITY ? 0.f : fast_exp2(m[t][j] - top) * (BLOCKS ? v_ref : 1.f);
 #pragma unroll
                 for (int i = 0; i < DP / 16; ++i) {
                     if (i < steps) {
@@ -767,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T == 2 ? 1 : 2, NT))
 
 template <int T, int DP, int NT, bool EXACT>
 cudaError_t launch(const AttendArgs& a, const AttendPlan& p, cudaStream_t st) {
-    constexpr int ES = T == 2 ? 1 : 2;
+    constexpr int ES = T >= 2 ? 1 : 2;
     const auto kernel = attend_kernel<T, DP, NT, EXACT>;
     static std::atomic<uint64_t> configured;
     // one limit serves every launch of the kernel; the CTAs share the SM's whole memory

@@ -174,6 +174,10 @@ __device__ __forceinline__ uint4 ld_host_v4(const void* p) {
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
+// 4 bytes, through L1 (the only way there is).
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_wait(int left) {  // until at most `left` groups are in flight
     switch (left) {
         case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
