@@ -23,6 +23,7 @@ namespace {
 struct BlockScales {
     const float *x, *w;  // [T][groups], [ceil(N / 128)][groups]
     int64_t x_stride, w_stride;
+    bool fours;  // rows of both are aligned for reads of four
 };
 
 // ---- split kernel ------------------------------------------------------------
@@ -207,23 +208,286 @@ __device__ __forceinline__ void tile_of(const Tiles& g, int i, int& m, int& n) {
     m = 8 * b + r - n * rows;
 }
 
-// A CTA pair works on 256 tokens x 64 NC outputs; each CTA has 128 tokens, an epilogue warp 32 of them (a lane
-// each) and half of the outputs, NC chunks of 32.
-template <int NC>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+// Warp 0 loads, warp 1 issues, warp 2 brings the scales, warps 4-11 add up and finish.
+constexpr int kBlockThreads = 32 * (4 + kEpiWarps);
+// Registers of a thread (setmaxnreg) of the first four warps and of the others, out of the launch's 168.  The
+// adding warps hold up to 128 sums and must not spill: the L1 that is left beside the ring does not hold it (with
+// 50 bytes spilled 8192 x 6144 x 4096 took 270 us).
+__host__ __device__ constexpr int few_regs(int bn) { return bn == 256 ? 56 : 72; }
+__host__ __device__ constexpr int many_regs(int bn) { return bn == 256 ? 224 : 216; }
+static_assert(4 * few_regs(256) + kEpiWarps * many_regs(256) <= (4 + kEpiWarps) * 168 &&
+                  4 * few_regs(128) + kEpiWarps * many_regs(128) <= (4 + kEpiWarps) * 168,
+              "registers of the CTA at its launch");
+constexpr int kBlockRing = 144 * 1024;  // bytes of the ring of operands
+constexpr int kBatch = 8;               // blocks of K whose scales come together
+constexpr int kPiece = 32 * 64;         // bytes of 32 rows of 64 bytes of outputs
+constexpr int kPieces = 4;              // of an adding warp: all its 16-bit outputs
+
+// What the warps of a tile share beside the operands and the staging.
+struct Shared {
+    float x[2][kBatch][128];  // scales of the CTA's tokens, of two batches
+    float w[2][kBatch][2];    // and of the tile's one or two blocks of outputs
+    float beyond[2];          // read behind the last batch, and not used
+    alignas(16) float bias[3][256];  // of three tiles, for a tile's is read when the next one's scales are all in use
+    uint64_t scales_full[2], scales_empty[2], res_full[kEpiWarps];
+    Head<kMaxAcc> head;
+};
+constexpr int kBlockSmem = 1024 + kBlockRing + kEpiWarps * kPieces * kPiece + (int)sizeof(Shared);
+static_assert(kBlockSmem <= 227 * 1024, "shared memory of a CTA");
+
+// s += f * 32 columns of this thread's lane: two loads, their wait and the arithmetic in one piece, so that the
+// loaded values need not be moved to registers of the compiler's choice (which took as many instructions again).
+__device__ __forceinline__ void add_columns(uint32_t at, float f, float (&s0)[16], float (&s1)[16]) {
+    asm volatile(
+        "{\n\t.reg .b32 a<16>, b<16>;\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {a0,a1,a2,a3,a4,a5,a6,a7,a8,a9,a10,a11,a12,a13,a14,a15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {b0,b1,b2,b3,b4,b5,b6,b7,b8,b9,b10,b11,b12,b13,b14,b15}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t"
+        "fma.rn.f32 %0, a0, %34, %0;\n\tfma.rn.f32 %1, a1, %34, %1;\n\tfma.rn.f32 %2, a2, %34, %2;\n\tfma.rn.f32 %3, a3, %34, %3;\n\t"
+        "fma.rn.f32 %4, a4, %34, %4;\n\tfma.rn.f32 %5, a5, %34, %5;\n\tfma.rn.f32 %6, a6, %34, %6;\n\tfma.rn.f32 %7, a7, %34, %7;\n\t"
+        "fma.rn.f32 %8, a8, %34, %8;\n\tfma.rn.f32 %9, a9, %34, %9;\n\tfma.rn.f32 %10, a10, %34, %10;\n\tfma.rn.f32 %11, a11, %34, %11;\n\t"
+        "fma.rn.f32 %12, a12, %34, %12;\n\tfma.rn.f32 %13, a13, %34, %13;\n\tfma.rn.f32 %14, a14, %34, %14;\n\tfma.rn.f32 %15, a15, %34, %15;\n\t"
+        "fma.rn.f32 %16, b0, %34, %16;\n\tfma.rn.f32 %17, b1, %34, %17;\n\tfma.rn.f32 %18, b2, %34, %18;\n\tfma.rn.f32 %19, b3, %34, %19;\n\t"
+        "fma.rn.f32 %20, b4, %34, %20;\n\tfma.rn.f32 %21, b5, %34, %21;\n\tfma.rn.f32 %22, b6, %34, %22;\n\tfma.rn.f32 %23, b7, %34, %23;\n\t"
+        "fma.rn.f32 %24, b8, %34, %24;\n\tfma.rn.f32 %25, b9, %34, %25;\n\tfma.rn.f32 %26, b10, %34, %26;\n\tfma.rn.f32 %27, b11, %34, %27;\n\t"
+        "fma.rn.f32 %28, b12, %34, %28;\n\tfma.rn.f32 %29, b13, %34, %29;\n\tfma.rn.f32 %30, b14, %34, %30;\n\tfma.rn.f32 %31, b15, %34, %31;\n\t"
+        "}"
+        : "+f"(s0[0]), "+f"(s0[1]), "+f"(s0[2]), "+f"(s0[3]), "+f"(s0[4]), "+f"(s0[5]), "+f"(s0[6]), "+f"(s0[7]),
+          "+f"(s0[8]), "+f"(s0[9]), "+f"(s0[10]), "+f"(s0[11]), "+f"(s0[12]), "+f"(s0[13]), "+f"(s0[14]), "+f"(s0[15]),
+          "+f"(s1[0]), "+f"(s1[1]), "+f"(s1[2]), "+f"(s1[3]), "+f"(s1[4]), "+f"(s1[5]), "+f"(s1[6]), "+f"(s1[7]),
+          "+f"(s1[8]), "+f"(s1[9]), "+f"(s1[10]), "+f"(s1[11]), "+f"(s1[12]), "+f"(s1[13]), "+f"(s1[14]), "+f"(s1[15])
+        : "r"(at), "r"(at + 16), "f"(f)
+        : "memory");
+}
+
+// The waits of linear.cuh without a call: a kernel that shifts registers between its warps may not hold any.  What is
+// usual takes one poll and one vote.
+__device__ __forceinline__ bool wait_inline(uint64_t* bar, unsigned parity, Head<kMaxAcc>& hd, int* status) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t since = globaltimer();
+#pragma unroll 1
+    for (unsigned it = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++it) {
+        if ((it & 63u) == 0) {
+            bool gone = *reinterpret_cast<volatile int*>(&hd.abort) != 0;
+            if (!gone && globaltimer() - since > kTimeoutNs) {
+                *reinterpret_cast<volatile int*>(&hd.abort) = 1;
+                set_status(status, MOE_ERR_TIMEOUT);
+                gone = true;
+            }
+            if (__any_sync(0xffffffffu, gone)) return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ void drain_inline(Head<kMaxAcc>& hd, int s, unsigned ph, int stages, int64_t loads) {
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll 1
+        for (int k = 0; k < stages && k < loads; ++k) {
+            const uint64_t since = globaltimer();
+            while (!mbar_try_wait(&hd.empty[k], k < s ? ph : ph ^ 1u) && globaltimer() - since < kTimeoutNs) {
+            }
+        }
+    __syncwarp();
+}
+
+// 16 values to 16 columns of this thread's lane.
+__device__ __forceinline__ void keep_columns(uint32_t at, const float (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        : "memory");
+}
+
+// Activation of 16 values, two after two: all at once would not leave the sums their registers.
+__device__ __forceinline__ void activate_in_turn(float (&v)[16], int act) {
+    if (act == MOE_ACT_NONE) return;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        if (i > 0) asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]) : "f"(v[i - 2]), "f"(v[i - 1]));
+        float w[2] = {v[i], v[i + 1]};
+        activate<2, Two>(w, act);
+        v[i] = w[0], v[i + 1] = w[1];
+    }
+}
+
+// A piece holds 32 rows (a lane each) of 64 bytes; 16-byte part j of row r is in place j ^ (r / 2 % 4), as TMA's
+// 64-byte swizzle has it, so that 8 lanes meet every bank once.
+__device__ __forceinline__ uint4* part_of(uint8_t* piece, int row, int j) {
+    return reinterpret_cast<uint4*>(piece + row * 64 + ((j ^ (row >> 1 & 3)) << 4));
+}
+
+// One lane's copy of a piece's box (column x, row y) of an output or residual.
+__device__ __forceinline__ void store_piece(const CUtensorMap* map, const uint8_t* piece, int x, int y) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
+        "@e cp.async.bulk.commit_group;\n\t}" ::"l"(map),
+        "r"(smem_u32(piece)), "r"(x), "r"(y)
+        : "memory");
+}
+// Residuals of `count` pieces side by side; they arrive on `bar` together.
+__device__ __forceinline__ void load_pieces(uint8_t* pieces, const CUtensorMap* map, int x, int y, int count, uint64_t* bar) {
+    mbar_arrive_expect_tx_elect(bar, count * kPiece);
+    for (int i = 0; i < count; ++i)
+        asm volatile(
+            "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(
+                smem_u32(pieces + i * kPiece)),
+            "l"(map), "r"(x + 64 * i), "r"(y), "r"(smem_u32(bar))
+            : "memory");
+}
+// Until this warp's stores have read their pieces (the electing instruction picks the same lane each time; the others
+// have nothing to wait for).
+__device__ __forceinline__ void stores_read() {
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+}
+
+// 16 outputs of a lane's token into its row of a piece, from part `first` on, `res`: onto the residuals there.
+template <int YT>
+__device__ __forceinline__ void put_row(uint8_t* piece, int lane, int first, float (&v)[16], bool res) {
+    constexpr int kRun = YT == MOE_F32 ? 4 : 8;  // values of a part
+#pragma unroll
+    for (int j = 0; j < 16 / kRun; ++j) {
+        uint4* at = part_of(piece, lane, first + j);
+        if (res) {
+            float f[kRun];
+            if constexpr (YT == MOE_F32) {
+                const float4 r = *reinterpret_cast<const float4*>(at);
+                f[0] = r.x, f[1] = r.y, f[2] = r.z, f[3] = r.w;
+            } else {
+                Raw<8, false> r;
+                r.set(at, 0);
+                r.get(YT, f);
+            }
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) v[kRun * j + i] += f[i];
+        }
+        store_run<kRun>(at, 0, YT, *reinterpret_cast<const float(*)[kRun]>(v + kRun * j));
+    }
+}
+
+// Outputs [n0, n1) (at most 16) of 32 tokens from t0, rows of any alignment: fp32 through the piece, then an output of
+// every other token a lane, so that half a warp's stores are consecutive.
+template <int YT>
+__device__ __forceinline__ void put_columns(const LinearArgs& a, uint8_t* piece, int lane, int t0, int n0, int n1, const float (&v)[16]) {
+    constexpr int kSize = YT == MOE_F32 ? 4 : 2;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<float4*>(part_of(piece, lane, j)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    __syncwarp();
+    const int n = lane & 15, rows = min(32, a.T - t0);
+    if (n0 + n < n1) {
+        uint8_t* to = static_cast<uint8_t*>(a.y) + ((int64_t)(t0 + lane / 16) * a.y_stride + n0 + n) * kSize;
+        const uint8_t* from = static_cast<const uint8_t*>(a.res) + ((int64_t)(t0 + lane / 16) * a.res_stride + n0 + n) * kSize;
+#pragma unroll 1
+        for (int r0 = lane >> 4; r0 < rows; r0 += 8) {
+            Raw<1> raw[4];
+            if (a.res) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i, from += 2 * a.res_stride * kSize)
+                    if (r0 + 2 * i < rows) raw[i].load(from, 0, YT);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i, to += 2 * a.y_stride * kSize) {
+                const int r = r0 + 2 * i;
+                if (r >= rows) break;
+                float one[1] = {reinterpret_cast<const float*>(part_of(piece, r, n >> 2))[n & 3]};
+                if (a.res) {
+                    float f[1];
+                    raw[i].get(YT, f);
+                    one[0] += f[0];
+                }
+                store_run<1>(to, 0, YT, one);
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// The end of an adding warp's tile: 32 tokens from t0 and 16 W outputs from n0, from sums in tensor memory at `sums`.
+// Aligned rows: as many pieces as there are room for, two chunks of 16 at a time so that one's way hides the other's,
+// then their stores; the residuals of the first ones are on their way since the tile began.
+template <int YT, int W>
+__device__ __forceinline__ void finish_tile(const LinearArgs& a, const CUtensorMap* ymap, const CUtensorMap* rmap, uint8_t* pieces,
+                                            uint64_t* res_full, unsigned& res_phase, const float* bias, int lane, int t0, int n0,
+                                            uint32_t sums, bool vec, Head<kMaxAcc>& hd) {
+    constexpr int kSize = YT == MOE_F32 ? 4 : 2, kPer = YT == MOE_F32 ? 1 : 2;  // chunks of 16 in a piece
+    constexpr int kRound = W < kPieces * kPer ? W : kPieces * kPer;             // chunks between stores
+    const auto value = [&](int c, float (&v)[16]) {
+        tc_ld16(sums + 16 * c, v);
+        if (a.bias) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+                const float4 p = *reinterpret_cast<const float4*>(bias + 16 * c + j);
+                v[j] += p.x, v[j + 1] += p.y, v[j + 2] += p.z, v[j + 3] += p.w;
+            }
+        }
+        activate_in_turn(v, a.act);
+    };
+    if (t0 >= a.T || n0 >= a.N) return;
+    if (vec) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < W && n0 + 16 * c0 < a.N; c0 += kRound) {
+            const int x = (n0 + 16 * c0) * kSize, count = min(kRound / kPer, (a.N * kSize - x + 63) / 64);
+            if (a.res) {
+                if (c0 > 0) {
+                    stores_read();
+                    load_pieces(pieces, rmap, x, t0, count, res_full);
+                }
+                if (!wait_inline(res_full, res_phase, hd, a.status)) return;
+                res_phase ^= 1u;
+            } else {
+                stores_read();
+            }
+#pragma unroll 2
+            for (int c = 0; c < kRound; ++c) {
+                float v[16];
+                value(c0 + c, v);
+                put_row<YT>(pieces + c / kPer * kPiece, lane, c % kPer * 2, v, a.res != nullptr);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            for (int i = 0; i < count; ++i) store_piece(ymap, pieces + i * kPiece, x + 64 * i, t0);
+        }
+    } else {
+#pragma unroll 1
+        for (int c = 0; c < W && n0 + 16 * c < a.N; ++c) {
+            float v[16];
+            value(c, v);
+            put_columns<YT>(a, pieces + (c & 1) * kPiece, lane, t0, n0 + 16 * c, min(n0 + 16 * c + 16, a.N), v);
+        }
+    }
+}
+
+// The sums are in registers when this arrives (tcgen05.wait::ld): nothing in memory has to be released, and a
+// release at the cluster's scope would wait for the scales' loads that are on their way.
+__device__ __forceinline__ void arrive_cluster_relaxed(uint32_t bar, bool on) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+                 "r"((uint32_t)on)
+                 : "memory");
+}
+
+// A CTA pair works on 256 tokens x BN outputs; each CTA has 128 tokens, an adding warp 32 of them (a lane each) and
+// half of the outputs.
+template <int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBlockThreads, 1)
     blocks_tile_kernel(const LinearArgs a, const BlockScales sc, const __grid_constant__ CUtensorMap wmap,
-                       const __grid_constant__ CUtensorMap xmap, const Tiles g, bool vec) {
-    constexpr int kBn = 64 * NC, kPitch = NC == 3 ? 256 : kBn, kAccs = 512 / kPitch;
+                       const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap ymap,
+                       const __grid_constant__ CUtensorMap rmap, const Tiles g, bool vec) {
+    constexpr int kAccs = 512 / BN, W = BN / 32;  // accumulators; chunks of 16 outputs of an adding warp
     static_assert(kAccs <= kMaxAcc, "barriers of the accumulators");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t* epi = base + kTileRing;
-    constexpr int kStageBytes = kABytes + kBn / 2 * kRowBytes;
-    Head<kMaxAcc>& hd = *reinterpret_cast<Head<kMaxAcc>*>(epi + kEpiWarps * kEpiBytes);
+    uint8_t* epi = base + kBlockRing;
+    constexpr int kStageBytes = kABytes + BN / 2 * kRowBytes;
+    Shared& sh = *reinterpret_cast<Shared*>(epi + kEpiWarps * kPieces * kPiece);
+    Head<kMaxAcc>& hd = sh.head;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int nkb = (a.K + kRowBytes - 1) / kRowBytes;
-    const int tiles = g.tm * g.tn, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const int tiles = g.tm * g.tn, pairs = gridDim.x / 2, pair_id = blockIdx.x / 2;
     if (threadIdx.x == 0) {
         prefetch_tmap(&wmap);
         prefetch_tmap(&xmap);
@@ -236,6 +500,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&hd.acc_full[s], 1);
             mbar_init(&hd.acc_empty[s], 2 * kEpiWarps);
         }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sh.scales_full[s], 32);
+            mbar_init(&sh.scales_empty[s], kEpiWarps);
+        }
+        for (int w = 0; w < kEpiWarps; ++w) mbar_init(&sh.res_full[w], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -252,118 +521,165 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grid_launch_next();
     grid_dep_wait();
     bool ok = true;
-    if (warp == 0) {
-        // each CTA stages its half: 128 tokens and kBn / 2 outputs; the leader's barrier counts both
-        const uint64_t keep = l2_policy_evict_last();
-        int s = 0;
-        unsigned ph = 0;
-        for (int i = pair; i < tiles && ok; i += pairs) {
-            int m, n;
-            tile_of(g, i, m, n);
-            const int t0 = m * 256 + (int)rank * 128, n0 = n * kBn + (int)rank * (kBn / 2);
-            for (int kb = 0; kb < nkb; ++kb) {
-                if (!wait_warp(&hd.empty[s], ph ^ 1u, hd, a.status, 2, s)) {
-                    ok = false;
-                    break;
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(few_regs(BN)));
+        if (warp == 0) {
+            // each CTA stages its half: 128 tokens and BN / 2 outputs; the leader's barrier counts both
+            const uint64_t keep = l2_policy_evict_last();
+            int s = 0;
+            unsigned ph = 0;
+            for (int i = pair_id; i < tiles && ok; i += pairs) {
+                int m, n;
+                tile_of(g, i, m, n);
+                const int t0 = m * 256 + (int)rank * 128, n0 = n * BN + (int)rank * (BN / 2);
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!wait_inline(&hd.empty[s], ph ^ 1u, hd, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t st = smem_u32(base) + (uint32_t)(s * kStageBytes);
+                    load_pair_block(&hd.full[s], rank == 0, 2u * kStageBytes, map_rank(smem_u32(&hd.full[s]), 0), st, &xmap,
+                                    st + kABytes, &wmap, kb * kRowBytes, t0, n0, keep);
+                    advance(s, ph, g.stages);
                 }
-                const uint32_t st = smem_u32(base) + (uint32_t)(s * kStageBytes);
-                load_pair_block(&hd.full[s], rank == 0, 2u * kStageBytes, map_rank(smem_u32(&hd.full[s]), 0), st, &xmap,
-                                st + kABytes, &wmap, kb * kRowBytes, t0, n0, keep);
-                advance(s, ph, g.stages);
+            }
+            if (ok) drain_inline(hd, s, ph, g.stages, (int64_t)nkb * ((tiles - pair_id + pairs - 1) / pairs));
+        } else if (warp == 1 && rank == 0) {
+            const uint32_t idesc = mma_idesc(a.in_type, 256, BN);
+            const uint64_t a0 = sw128_desc(smem_u32(base)), b0 = sw128_desc(smem_u32(base) + kABytes);
+            int s = 0, buf = 0;
+            unsigned ph = 0, aph = 0;
+            for (int i = pair_id; i < tiles && ok; i += pairs) {
+#pragma unroll 1
+                for (int kb = 0; kb < nkb; ++kb) {
+                    ok = wait_inline(&hd.full[s], ph, hd, a.status) && wait_inline(&hd.acc_empty[buf], aph ^ 1u, hd, a.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t at = s * (kStageBytes >> 4);
+                    mma_stage<true, 2>(tmem + buf * BN, a0 + at, b0 + at, idesc, 0, &hd.empty[s]);
+                    commit_pair_elect(&hd.acc_full[buf]);
+                    advance(s, ph, g.stages);
+                    advance(buf, aph, kAccs);
+                }
+            }
+        } else if (warp == 2) {
+            // the scales of kBatch blocks of K at a time: four tokens a lane, one after the other; with a
+            // tile's first ones its bias
+            int s = 0, slot = 0;
+            unsigned ph = 0;
+            for (int i = pair_id; i < tiles && ok; i += pairs) {
+                int m, n;
+                tile_of(g, i, m, n);
+                const int t0 = m * 256 + (int)rank * 128 + lane;
+                for (int kb = 0; kb < nkb; kb += kBatch) {
+                    if (!wait_inline(&sh.scales_empty[s], ph ^ 1u, hd, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const int left = nkb - kb;
+                    if (kb == 0 && a.bias) {
+#pragma unroll 1
+                        for (int j = lane; j < BN; j += 32) {
+                            const int at = min(n * BN + j, a.N - 1);
+                            sh.bias[slot][j] = a.bias_type == MOE_F32
+                                                   ? static_cast<const float*>(a.bias)[at]
+                                                   : half_bits_to_f32(static_cast<const uint16_t*>(a.bias)[at], a.bias_type);
+                        }
+                    }
+                    if (lane < 2 * kBatch && lane / 2 < left)
+                        sh.w[s][lane / 2][lane & 1] =
+                            sc.w[(int64_t)min(n * BN / 128 + (lane & 1), (a.N - 1) / 128) * sc.w_stride + kb + lane / 2];
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j) {
+                        const float* x = sc.x + (int64_t)min(t0 + 32 * j, a.T - 1) * sc.x_stride + kb;
+                        float v[kBatch];
+                        if (sc.fours && left >= kBatch) {
+#pragma unroll
+                            for (int k = 0; k < kBatch; k += 4) {
+                                const float4 p = *reinterpret_cast<const float4*>(x + k);
+                                v[k] = p.x, v[k + 1] = p.y, v[k + 2] = p.z, v[k + 3] = p.w;
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < kBatch; ++k) v[k] = k < left ? x[k] : 0.f;
+                        }
+#pragma unroll
+                        for (int k = 0; k < kBatch; ++k) sh.x[s][k][lane + 32 * j] = v[k];
+                    }
+                    mbar_arrive(&sh.scales_full[s]);
+                    advance(s, ph, 2);
+                }
+                slot = slot == 2 ? 0 : slot + 1;
             }
         }
-        if (ok) drain(hd, s, ph, g.stages, (int64_t)nkb * ((tiles - pair + pairs - 1) / pairs));
-    } else if (warp == 1 && rank == 0) {
-        const uint32_t idesc = mma_idesc(a.in_type, 256, kBn);
-        int s = 0, buf = 0;
-        unsigned ph = 0, aph = 0;
-        for (int i = pair; i < tiles && ok; i += pairs) {
-            for (int kb = 0; kb < nkb; ++kb) {
-                if (!wait_warp(&hd.acc_empty[buf], aph ^ 1u, hd, a.status, 4, buf) ||
-                    !wait_warp(&hd.full[s], ph, hd, a.status, 1, s)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t ad = sw128_desc(smem_u32(base) + s * kStageBytes);
-                const uint64_t bd = sw128_desc(smem_u32(base) + s * kStageBytes + kABytes);
-                mma_stage<true, 2>(tmem + buf * kPitch, ad, bd, idesc, 0, &hd.empty[s]);
-                commit_pair_elect(&hd.acc_full[buf]);
-                advance(s, ph, g.stages);
-                advance(buf, aph, kAccs);
-            }
-        }
-    } else if (warp >= 2) {
-        const int q = warp & 3, half = warp >= 6 ? 1 : 0;
-        uint8_t* stage = epi + (warp - 2) * kEpiBytes;
-        int buf = 0;
-        unsigned aph = 0;
-        for (int i = pair; i < tiles && ok; i += pairs) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(many_regs(BN)));
+        const int q = warp & 3, half = (warp - 4) >> 2, n_mine = half * (BN / 2);
+        uint8_t* pieces = epi + (warp - 4) * kPieces * kPiece;
+        uint64_t* res_full = &sh.res_full[warp - 4];
+        const uint32_t acc_empty = map_rank(smem_u32(hd.acc_empty), 0);
+        const uint32_t mine = tmem + ((uint32_t)(q * 32) << 16) + n_mine;
+        int buf = 0, batch = 0, slot = 0;
+        unsigned aph = 0, sph = 0, rph = 0;
+        for (int i = pair_id; i < tiles && ok; i += pairs) {
             int m, n;
             tile_of(g, i, m, n);
-            const int t0 = m * 256 + (int)rank * 128 + q * 32, n0 = n * kBn, c0 = half * (kBn / 2);
-            // this lane's token's scales, and those of the one or two blocks that its outputs lie in
-            const float* xs = sc.x + (int64_t)min(t0 + lane, a.T - 1) * sc.x_stride;
-            const int nb = (n0 + c0) / 128, last = (a.N - 1) / 128;
-            const float* ws0 = sc.w + min(nb, last) * sc.w_stride;
-            const float* ws1 = sc.w + min(nb + 1, last) * sc.w_stride;
-            float fx[2], fw[2][2];  // two blocks of K ahead
-            auto fetch = [&](int kb, int at) {
-                const int k = min(kb, nkb - 1);
-                fx[at] = xs[k];
-                fw[at][0] = ws0[k];
-                if (NC == 3) fw[at][1] = ws1[k];
-            };
-            fetch(0, 0);
-            fetch(1, 1);
-            float sum[NC][32];
+            const int t0 = m * 256 + (int)rank * 128 + q * 32, n0 = n * BN + n_mine;
+            if (vec && a.res && t0 < a.T && n0 < a.N) {  // the first pieces' residuals
+                const int size = a.y_type == MOE_F32 ? 4 : 2;
+                stores_read();
+                load_pieces(pieces, &rmap, n0 * size, t0, min(min(kPieces, W * size / 4), ((a.N - n0) * size + 63) / 64), res_full);
+            }
+            float sum[W][16];
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
+            for (int c = 0; c < W; ++c)
 #pragma unroll
-                for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
-            for (int kb = 0; kb < nkb; ++kb) {
-                const float f0 = fx[0] * fw[0][0], f1 = NC == 3 ? fx[0] * fw[0][1] : f0;
-                fx[0] = fx[1], fw[0][0] = fw[1][0];
-                if (NC == 3) fw[0][1] = fw[1][1];
-                fetch(kb + 2, 1);
-                if (!wait_warp(&hd.acc_full[buf], aph, hd, a.status, 3, buf)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+                for (int j = 0; j < 16; ++j) sum[c][j] = 0.f;
+            for (int kb = 0; kb < nkb && ok; kb += kBatch) {
+                ok = wait_inline(&sh.scales_full[batch], sph, hd, a.status);
+                const float* x = &sh.x[batch][0][q * 32 + lane];
+                const float* w = &sh.w[batch][0][BN == 256 ? half : 0];
+                const int end = min(kBatch, nkb - kb);
+                float f = x[0] * w[0];
+#pragma unroll 1
+                for (int j = 0; j < end && ok; ++j) {
+                    x += 128, w += 2;  // of the next block of K; behind the batch's last one nothing uses them
+                    const float x1 = x[0], w1 = w[0];
+                    ok = wait_inline(&hd.acc_full[buf], aph, hd, a.status);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    float v0[16], v1[16];
-                    const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + buf * kPitch + c0 + 32 * c;
-                    tc_ld16x2(at, at + 16, v0, v1);
-                    const float f = (n0 + c0 + 32 * c) / 128 == nb ? f0 : f1;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        sum[c][j] = fmaf(v0[j], f, sum[c][j]);
-                        sum[c][16 + j] = fmaf(v1[j], f, sum[c][16 + j]);
+                    for (int c = 0; c < W; c += 2) add_columns(mine + buf * BN + 16 * c, f, sum[c], sum[c + 1]);
+                    // the warp's loads are done (tcgen05.wait::ld): the next products may have the accumulator
+                    tc_fence_before();
+                    if (kb + j + 1 < nkb) {
+                        arrive_cluster_relaxed(acc_empty + 8 * buf, lane == 0);
+                        f = x1 * w1;
+                        advance(buf, aph, kAccs);
                     }
                 }
-                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_cluster(map_rank(smem_u32(&hd.acc_empty[buf]), 0));
-                advance(buf, aph, kAccs);
+                if (lane == 0) mbar_arrive(&sh.scales_empty[batch]);
+                advance(batch, sph, 2);
             }
             if (!ok) break;
-            const int cols = min(kBn, a.N - n0);
+            // The sums go to the last accumulator, which is held until the tile is finished: in registers they would
+            // leave none to the epilogue.  The next tile's first products go to another one meanwhile.
+            const uint32_t held = mine + buf * BN;
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                if (c0 + 32 * c < cols)
-                    finish_chunk(a, stage, lane, t0, n0, c0 + 32 * c, cols, vec, [&]() {
-                        float v0[16], v1[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            v0[j] = sum[c][j];
-                            v1[j] = sum[c][16 + j];
-                        }
-                        stage_row(stage, lane, v0, v1);
-                    });
-            }
+            for (int c = 0; c < W; ++c) keep_columns(held + 16 * c, sum[c]);
+            tc_wait_st();
+            const float* bias = sh.bias[slot] + n_mine;
+            slot = slot == 2 ? 0 : slot + 1;
+            if (a.y_type == MOE_BF16) finish_tile<MOE_BF16, W>(a, &ymap, &rmap, pieces, res_full, rph, bias, lane, t0, n0, held, vec, hd);
+            else if (a.y_type == MOE_F16) finish_tile<MOE_F16, W>(a, &ymap, &rmap, pieces, res_full, rph, bias, lane, t0, n0, held, vec, hd);
+            else finish_tile<MOE_F32, W>(a, &ymap, &rmap, pieces, res_full, rph, bias, lane, t0, n0, held, vec, hd);
+            tc_fence_before();
+            __syncwarp();
+            arrive_cluster_relaxed(acc_empty + 8 * buf, lane == 0);
+            advance(buf, aph, kAccs);
         }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the stores are done before the CTA's memory goes
     }
     __syncwarp();
     __syncthreads();
@@ -416,25 +732,34 @@ cudaError_t launch_split_chunks(const LinearArgs& a, const BlockScales& sc, int 
     return cudaErrorInvalidValue;
 }
 
-template <int NC>
+template <int BN>
 cudaError_t launch_tiles(const LinearArgs& a, const BlockScales& sc, bool vec, cudaStream_t st) {
-    CUtensorMap wmap, xmap;
-    if (!encode_rows(&wmap, a, a.w, a.N, a.w_stride, 32 * NC) || !encode_rows(&xmap, a, a.x, a.T, a.x_stride, 128))
+    CUtensorMap wmap, xmap, ymap = {}, rmap = {};
+    if (!encode_rows(&wmap, a, a.w, a.N, a.w_stride, BN / 2) || !encode_rows(&xmap, a, a.x, a.T, a.x_stride, 128))
         return cudaErrorInvalidValue;
-    const auto kernel = blocks_tile_kernel<NC>;
+    // pieces of 64 bytes x 32 tokens; rows that TMA does not take are stored one by one, and so are those that end
+    // inside 16 bytes, for it writes the rest of these
+    const int size = type_bytes(a.y_type);
+    const auto pieces = [&](CUtensorMap* map, const void* p, int64_t stride) {
+        return stride >= a.N && encode_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, (uint64_t)a.N * size, (uint64_t)a.T,
+                                               (uint64_t)(stride * size), 64, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    };
+    vec = vec && (int64_t)a.N * size % 16 == 0 && pieces(&ymap, a.y, a.y_stride) && (!a.res || pieces(&rmap, a.res, a.res_stride));
+    const auto kernel = blocks_tile_kernel<BN>;
     static std::atomic<uint64_t> configured;
-    cudaError_t err = ensure_smem_limit((const void*)kernel, kTileSmem, configured);
+    cudaError_t err = ensure_smem_limit((const void*)kernel, kBlockSmem, configured);
     if (err != cudaSuccess) return err;
-    const Tiles g{(a.T + 255) / 256, (a.N + 64 * NC - 1) / (64 * NC), std::min(kMaxStages, kTileRing / (kABytes + 32 * NC * kRowBytes))};
+    const Tiles g{(a.T + 255) / 256, (a.N + BN - 1) / BN, std::min(kMaxStages, kBlockRing / (kABytes + BN / 2 * kRowBytes))};
     const int pairs = std::min(a.sm_count / 2, g.tm * g.tn);
-    return launch_pdl(kernel, dim3(2 * pairs), dim3(kThreads), kTileSmem, st, a, sc, wmap, xmap, g, vec);
+    return launch_pdl(kernel, dim3(2 * pairs), dim3(kBlockThreads), kBlockSmem, st, a, sc, wmap, xmap, ymap, rmap, g, vec);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_blocks(const LinearArgs& args, int64_t xs_stride, int64_t ws_stride, cudaStream_t st) {
     if (args.T == 0) return cudaSuccess;
-    const BlockScales sc{args.x_scale, args.w_scale, xs_stride, ws_stride};
+    const BlockScales sc{args.x_scale, args.w_scale, xs_stride, ws_stride,
+                         runs_aligned(args.x_scale, MOE_F32, 4, xs_stride) && runs_aligned(args.w_scale, MOE_F32, 4, ws_stride)};
     LinearArgs a = args;
     a.x_scale = a.w_scale = nullptr;  // none are left for the epilogue
     const bool vec = runs_aligned(a.y, a.y_type, 8, a.y_stride) && (!a.res || runs_aligned(a.res, a.y_type, 8, a.res_stride));
@@ -442,15 +767,14 @@ cudaError_t launch_linear_blocks(const LinearArgs& args, int64_t xs_stride, int6
     const int nkb = (a.K + kRowBytes - 1) / kRowBytes, pairs = a.sm_count / 2;
     const int tm = (a.T + 255) / 256;
     int64_t tiles_ns = INT64_MAX;
-    int nc = 4;
-    for (int c = 4; c >= 1; --c) {
-        const int bn = 64 * c;
+    int width = 256;
+    for (int bn = 256; bn >= 64; bn /= 2) {
         const int64_t tn = (a.N + bn - 1) / bn, rounds = (tm * tn + pairs - 1) / pairs;
         const int64_t pass = nkb * (int64_t)std::max(170, bn * 12 / 10), epi = 1000 + 14 * bn;
         const int64_t ns = 1600 + rounds * (pass + epi);
         if (ns < tiles_ns) {
             tiles_ns = ns;
-            nc = c;
+            width = bn;
         }
     }
     const int tz = (a.T + 255) / 256, bn = ((a.T + tz - 1) / tz + 15) / 16 * 16;
@@ -463,12 +787,8 @@ cudaError_t launch_linear_blocks(const LinearArgs& args, int64_t xs_stride, int6
     const int64_t at_once = (int64_t)a.sm_count * (two ? 2 : 1), rounds = (blocks * ksplit + at_once - 1) / at_once;
     const int64_t split_ns = 2500 + rounds * (20 * bn + ((nkb + ksplit - 1) / ksplit) * (200 + bn * 12 / 10));
     if (a.T > 64 && tiles_ns < split_ns) {
-        switch (nc) {
-            case 1: return launch_tiles<1>(a, sc, vec, st);
-            case 2: return launch_tiles<2>(a, sc, vec, st);
-            case 3: return launch_tiles<3>(a, sc, vec, st);
-            default: return launch_tiles<4>(a, sc, vec, st);
-        }
+        if (width == 256) return launch_tiles<256>(a, sc, vec, st);
+        return width == 128 ? launch_tiles<128>(a, sc, vec, st) : launch_tiles<64>(a, sc, vec, st);
     }
     return two ? launch_split_chunks<2>(a, sc, bn, ksplit, vec4, st) : launch_split_chunks<1>(a, sc, bn, ksplit, vec4, st);
 }
