@@ -5,14 +5,17 @@
 // The two kernels are the plain product's (linear.cu): TMA, tcgen05 kind::f8f6f4, a split kernel for
 // few tiles and a kernel of CTA pairs for many.  What differs is that the tensor cores' sums last for
 // one block of K only, the 128 bytes of a stage: each block's products go to an accumulator of their
-// own in a ring in tensor memory, from where the epilogue warps add them, times their two scales, to
-// fp32 sums in registers.  The scales are any fp32 numbers, which the block-scaled MMA forms (powers of
-// two for 32 elements) could not take, and the registers' sums are rounded to nearest, so that a long K
-// loses less than in the tensor cores' own sums.
+// own in a ring in tensor memory, from where warps add them, times their two scales, to fp32 sums in
+// registers.  The scales are any fp32 numbers, which the block-scaled MMA forms (powers of two for 32
+// elements) could not take, and the registers' sums are rounded to nearest, so that a long K loses less
+// than in the tensor cores' own sums.
 //
-// An addition for every output and block of K keeps the fp32 units busy for half of the products' time
-// at 256 x 256 outputs a pair (128 x 256 a CTA: 256 cycles of 512), and so does reading the accumulators
-// from tensor memory; both run beside the products as long as there are two accumulators.
+// Measured on a GB300 (launches of a graph): 8192 x 6144 x 4096 with bias 184 us (2240 TFLOP/s; the plain
+// E4M3 product 117), 4096 x 4096 x 4096 73, 1024 x 4096 x 4096 24, 32 x 6144 x 4096 8.0, 1 x 4096 x 4096 5.2.
+// What bounds the tiles is a circle of two accumulators: products (some 600 cycles for 256 x 256 outputs
+// and a block of K), their commit, the additions up to the last read of the accumulator (some 450) and the
+// arrival that lets the next products have it, 1550 cycles for two blocks of K.  The additions alone
+// are 256 cycles of fp32 work a block.
 #include <algorithm>
 
 #include "linear.cuh"
@@ -213,8 +216,8 @@ constexpr int kBlockThreads = 32 * (4 + kEpiWarps);
 // Registers of a thread (setmaxnreg) of the first four warps and of the others, out of the launch's 168.  The
 // adding warps hold up to 128 sums and must not spill: the L1 that is left beside the ring does not hold it (with
 // 50 bytes spilled 8192 x 6144 x 4096 took 270 us).
-__host__ __device__ constexpr int few_regs(int bn) { return bn == 256 ? 56 : 72; }
-__host__ __device__ constexpr int many_regs(int bn) { return bn == 256 ? 224 : 216; }
+__host__ __device__ constexpr int few_regs(int bn) { return bn == 256 ? 56 : 88; }
+__host__ __device__ constexpr int many_regs(int bn) { return bn == 256 ? 224 : 208; }
 static_assert(4 * few_regs(256) + kEpiWarps * many_regs(256) <= (4 + kEpiWarps) * 168 &&
                   4 * few_regs(128) + kEpiWarps * many_regs(128) <= (4 + kEpiWarps) * 168,
               "registers of the CTA at its launch");
@@ -278,6 +281,21 @@ __device__ __forceinline__ bool wait_inline(uint64_t* bar, unsigned parity, Head
         }
     }
     return true;
+}
+// Both waits of the issuing warp: two polls on their way at once, and the waits themselves where they fail.
+__device__ __forceinline__ bool wait_both(uint64_t* one, unsigned one_parity, uint64_t* other, unsigned other_parity, Head<kMaxAcc>& hd,
+                                          int* status) {
+    unsigned got;
+    asm volatile(
+        "{\n\t.reg .pred a, b;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 a, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 b, [%3], %4;\n\t"
+        "and.pred a, a, b;\n\tselp.u32 %0, 1, 0, a;\n\t}"
+        : "=r"(got)
+        : "r"(smem_u32(one)), "r"(one_parity), "r"(smem_u32(other)), "r"(other_parity)
+        : "memory");
+    if (__all_sync(0xffffffffu, got != 0)) return true;
+    return wait_inline(one, one_parity, hd, status) && wait_inline(other, other_parity, hd, status);
 }
 __device__ __forceinline__ void drain_inline(Head<kMaxAcc>& hd, int s, unsigned ph, int stages, int64_t loads) {
     if ((threadIdx.x & 31) == 0)
@@ -469,6 +487,22 @@ __device__ __forceinline__ void arrive_cluster_relaxed(uint32_t bar, bool on) {
                  : "memory");
 }
 
+// A block of K into a new accumulator, and the commits that announce it and free its stage in both CTAs, under one
+// election.
+__device__ __forceinline__ void mma_block(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint64_t* free, uint64_t* done) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b64 x, y;\n\t.reg .b16 m;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %3, %3;\n\tsetp.eq.u32 t, %3, %3;\n\tmov.u16 m, 3;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+        "add.u64 x, %1, 2;\n\tadd.u64 y, %2, 2;\n\t@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %3, t;\n\t"
+        "add.u64 x, %1, 4;\n\tadd.u64 y, %2, 4;\n\t@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %3, t;\n\t"
+        "add.u64 x, %1, 6;\n\tadd.u64 y, %2, 6;\n\t@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %3, t;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], m;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%4], m;\n\t}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(smem_u32(free)), "r"(smem_u32(done))
+        : "memory");
+}
+
 // A CTA pair works on 256 tokens x BN outputs; each CTA has 128 tokens, an adding warp 32 of them (a lane each) and
 // half of the outputs.
 template <int BN>
@@ -552,12 +586,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBlockThreads, 1)
             for (int i = pair_id; i < tiles && ok; i += pairs) {
 #pragma unroll 1
                 for (int kb = 0; kb < nkb; ++kb) {
-                    ok = wait_inline(&hd.full[s], ph, hd, a.status) && wait_inline(&hd.acc_empty[buf], aph ^ 1u, hd, a.status);
+                    ok = wait_both(&hd.full[s], ph, &hd.acc_empty[buf], aph ^ 1u, hd, a.status);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t at = s * (kStageBytes >> 4);
-                    mma_stage<true, 2>(tmem + buf * BN, a0 + at, b0 + at, idesc, 0, &hd.empty[s]);
-                    commit_pair_elect(&hd.acc_full[buf]);
+                    mma_block(tmem + buf * BN, a0 + at, b0 + at, idesc, &hd.empty[s], &hd.acc_full[buf]);
                     advance(s, ph, g.stages);
                     advance(buf, aph, kAccs);
                 }
@@ -727,9 +760,7 @@ template <int CTAS>
 cudaError_t launch_split_chunks(const LinearArgs& a, const BlockScales& sc, int bn, int ksplit, bool vec, cudaStream_t st) {
     if (bn <= 32) return launch_split<CTAS, 1>(a, sc, bn, ksplit, vec, st);
     if (bn <= 64) return launch_split<CTAS, 2>(a, sc, bn, ksplit, vec, st);
-    if (CTAS == 2 || bn <= 128) return launch_split<CTAS, 4>(a, sc, bn, ksplit, vec, st);
-    if constexpr (CTAS == 1) return launch_split<1, 8>(a, sc, bn, ksplit, vec, st);
-    return cudaErrorInvalidValue;
+    return launch_split<CTAS, 4>(a, sc, bn, ksplit, vec, st);  // bn <= 128
 }
 
 template <int BN>
@@ -756,6 +787,12 @@ cudaError_t launch_tiles(const LinearArgs& a, const BlockScales& sc, bool vec, c
 
 }  // namespace
 
+// Which kernel, by what each is expected to take in ns (fitted to products of 96 to 4096 tokens, 512 to 8192 outputs
+// and depths of 512 to 8192):
+//  tiles  2600 + rounds * (blocks of K * step + epilogue), step 470, 290 and 245 and epilogue 4000, 2400 and 1500 for
+//         tiles of 256, 128 and 64 outputs.  1024 x 1024 x 1024 10.4, 7.2 and 6.9 us; 4096 x 2048 x 8192 67, 78 and 117.
+//  split  3000 + rounds * (45 bn for the join + blocks of K of a CTA * (200 + 1.2 bn)).  128 x 4096 x 4096 11.2 us
+//         against 12.0 in tiles, 128 x 1024 x 1024 8.8 against 6.0.
 cudaError_t launch_linear_blocks(const LinearArgs& args, int64_t xs_stride, int64_t ws_stride, cudaStream_t st) {
     if (args.T == 0) return cudaSuccess;
     const BlockScales sc{args.x_scale, args.w_scale, xs_stride, ws_stride,
@@ -769,23 +806,25 @@ cudaError_t launch_linear_blocks(const LinearArgs& args, int64_t xs_stride, int6
     int64_t tiles_ns = INT64_MAX;
     int width = 256;
     for (int bn = 256; bn >= 64; bn /= 2) {
-        const int64_t tn = (a.N + bn - 1) / bn, rounds = (tm * tn + pairs - 1) / pairs;
-        const int64_t pass = nkb * (int64_t)std::max(170, bn * 12 / 10), epi = 1000 + 14 * bn;
-        const int64_t ns = 1600 + rounds * (pass + epi);
+        const int64_t rounds = ((int64_t)tm * ((a.N + bn - 1) / bn) + pairs - 1) / pairs;
+        const int64_t step = bn == 256 ? 470 : (bn == 128 ? 290 : 245), end = bn == 256 ? 4000 : (bn == 128 ? 2400 : 1500);
+        const int64_t ns = 2600 + rounds * (nkb * step + end);
         if (ns < tiles_ns) {
             tiles_ns = ns;
             width = bn;
         }
     }
-    const int tz = (a.T + 255) / 256, bn = ((a.T + tz - 1) / tz + 15) / 16 * 16;
+    // split: token blocks as even as they come, and K over what is left of the GPU.  Two CTAs an SM while the
+    // smaller ring is as deep as a short pass over K needs
+    const int tz = (a.T + 127) / 128, bn = ((a.T + tz - 1) / tz + 15) / 16 * 16;
     const int64_t blocks = (int64_t)((a.N + 127) / 128) * tz;
     int ksplit = 1;
-    cudaError_t err = bn <= 128 ? cluster_size<2>(blocks, nkb, &ksplit) : cudaSuccess;
-    const bool two = bn <= 32 || (bn <= 128 && (nkb + ksplit - 1) / ksplit <= split_stages(2, bn));
+    cudaError_t err = cluster_size<2>(blocks, nkb, &ksplit);
+    const bool two = bn <= 32 || (nkb + ksplit - 1) / ksplit <= split_stages(2, bn);
     if (err == cudaSuccess && !two) err = cluster_size<1>(blocks, nkb, &ksplit);
     if (err != cudaSuccess) return err;
     const int64_t at_once = (int64_t)a.sm_count * (two ? 2 : 1), rounds = (blocks * ksplit + at_once - 1) / at_once;
-    const int64_t split_ns = 2500 + rounds * (20 * bn + ((nkb + ksplit - 1) / ksplit) * (200 + bn * 12 / 10));
+    const int64_t split_ns = 3000 + rounds * (45 * bn + ((nkb + ksplit - 1) / ksplit) * (200 + bn * 12 / 10));
     if (a.T > 64 && tiles_ns < split_ns) {
         if (width == 256) return launch_tiles<256>(a, sc, vec, st);
         return width == 128 ? launch_tiles<128>(a, sc, vec, st) : launch_tiles<64>(a, sc, vec, st);
