@@ -101,10 +101,6 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
     }
 }
 
-__device__ __forceinline__ void cp_async16_l1(uint4* dst, const void* src) {  // read by the whole CTA: through L1
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-
 // 16-bit q, k and v in runs of 8, the cache of their type (CT = XT) or E4M3.  CTAs walk the
 // (token, block of heads) pairs; a thread's runs and table entries of the next pair come
 // through a ring in shared memory that it alone reads, and the position that a copy of the

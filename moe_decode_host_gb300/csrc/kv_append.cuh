@@ -34,6 +34,10 @@ __device__ __forceinline__ const void* source(const AppendArgs& a, int64_t t, in
     return kind == 0 ? a.q : (kind == 1 ? a.k : a.v);
 }
 
+__device__ __forceinline__ void cp_async16_l1(uint4* dst, const void* src) {  // read by the whole CTA: through L1
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // A token's position along its axes; valid: the table has a row for each.
 struct Place {
     int pos[kMaxAxes];

@@ -21,7 +21,6 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kKeep = 4;   // tokens a thread keeps in registers
 constexpr int kAny = -1;   // a type known only at run time
 
 // The smallest power of two s with top <= 448 s, from 2^-126 to 2^119.  448 = 1.75 * 2^8.
@@ -62,6 +61,9 @@ __device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float (&v)[4]) {
     v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
 }
 
+// Calls whose tokens may go to different teams each: up to some warps for each that the GPU holds at once.
+bool few(const AppendArgs& a) { return (int64_t)a.T * 2 * a.kv.kv_heads <= 16384; }
+
 // TEAM threads, 32 or all of the CTA.
 template <int TEAM>
 __device__ __forceinline__ void team_sync() {
@@ -69,11 +71,20 @@ __device__ __forceinline__ void team_sync() {
     else __syncthreads();
 }
 
+// What a thread has brought of KEEP tokens at a time, in shared memory that it alone reads: two runs of a head and,
+// for keys, the cosines and sines of their pairs, and the tokens' entries in the block.
+template <int KEEP>
+struct Kept {
+    uint4 piece[KEEP][6][kThreads];
+    int at[KEEP][kThreads];  // -1: not appended
+};
+
 // A team's share of k and v: the blocks that begin among `window` tokens from w0 on (at most 32), of
-// head `head` of k (side 0) or v (side 1).
-template <int XT, int VEC, int TEAM, bool FOURS>
+// head `head` of k (side 0) or v (side 1).  KEEP > 0: 16-bit values and table rows that can be copied 16 bytes at
+// a time, KEEP tokens of a thread at once, so that a block that they hold is read once; 0: read twice.
+template <int XT, int VEC, int TEAM, int KEEP, bool FOURS>
 __device__ __forceinline__ void append_block_runs(const AppendArgs& a, int64_t w0, int window, int side, int head,
-                                                  uint32_t* mask, float (*part)[kThreads / 32]) {
+                                                  uint32_t* mask, float (*part)[kThreads / 32], Kept<KEEP ? KEEP : 1>& kept) {
     const int me = threadIdx.x % TEAM, lane = threadIdx.x & 31;
     const int items = a.kv.head_dim / (2 * VEC), step = TEAM / items, g = me / items;
     const bool works = g < step;
@@ -83,6 +94,7 @@ __device__ __forceinline__ void append_block_runs(const AppendArgs& a, int64_t w
     const int64_t ts = side ? a.v_ts : a.k_ts, hs = side ? a.v_hs : a.k_hs;
     uint8_t* cache = static_cast<uint8_t*>(side ? a.kv.v : a.kv.k) + head * a.kv.head_stride;
     float* scales = side ? a.kv.v_scale : a.kv.k_scale;
+    const bool turn = it.turn && side == 0;
     // lane i: the home of token w0 + i; a run begins where it differs from the token before
     const int64_t mine = lane < window && w0 + lane < a.T ? home_of(a, a.slots[w0 + lane]).first : -1;
     int64_t before = __shfl_up_sync(0xffffffffu, mine, 1);
@@ -110,49 +122,103 @@ __device__ __forceinline__ void append_block_runs(const AppendArgs& a, int64_t w
         float* scale_at = scales + ((int64_t)home.page * a.kv.blocks + block_of(a.kv, home.entry)) * a.kv.kv_heads + head;
         const float old = *scale_at;
 
-        // a token's values, turned; false: not appended
-        auto fetch = [&](int64_t t, float (&x0)[VEC], float (&x1)[VEC], int& entry) {
-            const Place place = place_of(a, t);
-            entry = (int)(a.slots[t] - first);
-            if (!place.valid) {
-                set_status(a.kv.status, MOE_ERR_BAD_INDEX);
-                return false;
-            }
-            Raw<VEC, XT == kAny || XT == MOE_F32> r0, r1;
-            r0.load(src, t * ts + head * hs + it.e0, xt);
-            r1.load(src, t * ts + head * hs + it.e1, xt);
-            float cs[VEC], sn[VEC];
-            const bool turn = it.turn && side == 0;
-            if (turn) turn_of<VEC, FOURS>(a, place, it.j * VEC, cs, sn);
-            r0.get(xt, x0);
-            r1.get(xt, x1);
-            if (turn) rotate<VEC>(a.interleaved, x0, x1, cs, sn);
-            return true;
+        // the entry of a token in the block, or -1 where it has no position in the table
+        auto entry_of = [&](int64_t t, Place& place) {
+            place = place_of(a, t);
+            if (place.valid) return (int)(a.slots[t] - first);
+            set_status(a.kv.status, MOE_ERR_BAD_INDEX);
+            return -1;
         };
-        float x[kKeep][2][VEC];
-        int at[kKeep];  // entries, or -1
+        // KEEP tokens of this thread from t on
+        auto bring = [&](int64_t t) {
+            if constexpr (KEEP > 0) {
+#pragma unroll
+                for (int k = 0; k < KEEP; ++k, t += step) {
+                    int at = -1;
+                    if (works && t < t1) {
+                        Place place;
+                        at = entry_of(t, place);
+                        const uint16_t* x = static_cast<const uint16_t*>(src) + t * ts + head * hs;
+                        cp_async16(&kept.piece[k][0][threadIdx.x], x + it.e0);
+                        cp_async16(&kept.piece[k][1][threadIdx.x], x + it.e1);
+                        if (turn && at >= 0) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int pair = it.j * VEC + (i & 1) * 4;
+                                const int axis = a.axes == 1 ? 0 : axis_of(a, pair);
+                                cp_async16_l1(&kept.piece[k][2 + i][threadIdx.x],
+                                              a.cos_sin + (int64_t)place.at(axis) * a.rot + pair + (i >> 1) * (a.rot / 2));
+                            }
+                        }
+                    }
+                    kept.at[k][threadIdx.x] = at;
+                }
+                asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+            }
+        };
+        // values of token t, or of the k-th of those kept, turned; its entry, or -1
+        auto values = [&](int64_t t, int k, float (&x0)[VEC], float (&x1)[VEC]) {
+            if constexpr (KEEP > 0) {
+                const int at = kept.at[k][threadIdx.x];
+                if (at < 0) return at;
+                Raw<VEC, false> r0, r1;
+                r0.set(&kept.piece[k][0][threadIdx.x], 0);
+                r1.set(&kept.piece[k][1][threadIdx.x], 0);
+                r0.get(XT, x0);
+                r1.get(XT, x1);
+                if (turn) {
+                    float cs[VEC], sn[VEC];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 c = kept.piece[k][2 + i][threadIdx.x], s = kept.piece[k][4 + i][threadIdx.x];
+                        cs[4 * i] = __uint_as_float(c.x), cs[4 * i + 1] = __uint_as_float(c.y);
+                        cs[4 * i + 2] = __uint_as_float(c.z), cs[4 * i + 3] = __uint_as_float(c.w);
+                        sn[4 * i] = __uint_as_float(s.x), sn[4 * i + 1] = __uint_as_float(s.y);
+                        sn[4 * i + 2] = __uint_as_float(s.z), sn[4 * i + 3] = __uint_as_float(s.w);
+                    }
+                    rotate<VEC>(a.interleaved, x0, x1, cs, sn);
+                }
+                return at;
+            } else {
+                Place place;
+                const int at = entry_of(t, place);
+                if (at < 0) return at;
+                Raw<VEC, XT == kAny || XT == MOE_F32> r0, r1;
+                r0.load(src, t * ts + head * hs + it.e0, xt);
+                r1.load(src, t * ts + head * hs + it.e1, xt);
+                r0.get(xt, x0);
+                r1.get(xt, x1);
+                if (turn) {
+                    float cs[VEC], sn[VEC];
+                    turn_of<VEC, FOURS>(a, place, it.j * VEC, cs, sn);
+                    rotate<VEC>(a.interleaved, x0, x1, cs, sn);
+                }
+                return at;
+            }
+        };
+        constexpr int kEach = KEEP > 0 ? KEEP : 1;  // tokens of a thread at a time
+        const bool once = t1 - t0 <= (int64_t)kEach * step;
+        auto all = [&](bool again, auto&& use) {  // every token of this thread
+#pragma unroll 1
+            for (int64_t c = t0; c < t1; c += (int64_t)kEach * step) {
+                if (!again || !once) bring(c + g);
+#pragma unroll 1
+                for (int k = 0; k < kEach; ++k) {
+                    const int64_t t = c + g + (int64_t)k * step;
+                    if (!works || t >= t1) break;
+                    float x0[VEC], x1[VEC];
+                    const int at = values(t, k, x0, x1);
+                    if (at >= 0) use(x0, x1, at);
+                }
+            }
+        };
         float top = 0.f;
         bool anew = false;
-        auto see = [&](const float (&x0)[VEC], const float (&x1)[VEC], int entry) {
+        all(false, [&](const float (&x0)[VEC], const float (&x1)[VEC], int entry) {
             anew = anew || entry == 0;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) top = fmaxf(top, fmaxf(fabsf(x0[i]), fabsf(x1[i])));  // NaN does not count
-        };
-#pragma unroll
-        for (int k = 0; k < kKeep; ++k) {
-            const int64_t t = t0 + g + (int64_t)k * step;
-            at[k] = -1;
-            int entry;
-            if (works && t < t1 && fetch(t, x[k][0], x[k][1], entry)) {
-                at[k] = entry;
-                see(x[k][0], x[k][1], entry);
-            }
-        }
-        for (int64_t t = t0 + g + (int64_t)kKeep * step; works && t < t1; t += step) {
-            float y0[VEC], y1[VEC];
-            int entry;
-            if (fetch(t, y0, y1, entry)) see(y0, y1, entry);
-        }
+        });
         top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // not negative: ordered as its bits
         anew = __any_sync(0xffffffffu, anew);
         if constexpr (TEAM > 32) {
@@ -170,25 +236,16 @@ __device__ __forceinline__ void append_block_runs(const AppendArgs& a, int64_t w
         const float need = scale_for(top);
         const float scale = anew || !(old >= need) ? need : old;
         const float inv = 1.f / scale;
-        auto put = [&](const float (&x0)[VEC], const float (&x1)[VEC], int entry) {
-            float y0[VEC], y1[VEC];
+        all(true, [&](float (&x0)[VEC], float (&x1)[VEC], int entry) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                y0[i] = x0[i] * inv;
-                y1[i] = x1[i] * inv;
+                x0[i] *= inv;
+                x1[i] *= inv;
             }
             const int64_t to = base + (int64_t)entry * a.kv.token_stride;
-            store_run<VEC>(cache, to + it.e0, MOE_E4M3, y0);
-            store_run<VEC>(cache, to + it.e1, MOE_E4M3, y1);
-        };
-#pragma unroll
-        for (int k = 0; k < kKeep; ++k)
-            if (at[k] >= 0) put(x[k][0], x[k][1], at[k]);
-        for (int64_t t = t0 + g + (int64_t)kKeep * step; works && t < t1; t += step) {
-            float y0[VEC], y1[VEC];
-            int entry;
-            if (fetch(t, y0, y1, entry)) put(y0, y1, entry);
-        }
+            store_run<VEC>(cache, to + it.e0, MOE_E4M3, x0);
+            store_run<VEC>(cache, to + it.e1, MOE_E4M3, x1);
+        });
         if (!anew && scale != old) {  // the block's other entries keep their values
             const int n = a.kv.scale_tokens;
             for (int i = me; i < (n + 31) / 32; i += TEAM) mask[i] = 0;
@@ -220,12 +277,13 @@ __device__ __forceinline__ void append_block_runs(const AppendArgs& a, int64_t w
     }
 }
 
-// The first CTAs take k and v, a team per (window of tokens, head of either); the others a token's
-// queries each.
-template <int XT, int VEC, int TEAM, bool FOURS>
+// The first CTAs take k and v, a team per (window of tokens, head of either); the others, where there are any, a
+// token's queries each.
+template <int XT, int VEC, int TEAM, int KEEP, bool FOURS>
 __global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendArgs a, int window, int kv_ctas) {
     __shared__ uint32_t mask[kThreads / TEAM][kMaxScaleTokens / 32];
     __shared__ float part[2][kThreads / 32];
+    extern __shared__ __align__(16) uint8_t room[];
     grid_launch_next();
     grid_dep_wait();
     const int xt = XT == kAny ? a.type : XT;
@@ -235,8 +293,9 @@ __global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendArg
         const int64_t w = unit / heads;
         const int h = (int)(unit - w * heads);
         if (w * window < a.T)  // a team of one warp leaves alone; a CTA's has the same w
-            append_block_runs<XT, VEC, TEAM, FOURS>(a, w * window, window, h >= a.kv.kv_heads, h % a.kv.kv_heads,
-                                                    mask[threadIdx.x / TEAM], part);
+            append_block_runs<XT, VEC, TEAM, KEEP, FOURS>(a, w * window, window, h >= a.kv.kv_heads, h % a.kv.kv_heads,
+                                                          mask[threadIdx.x / TEAM], part,
+                                                          *reinterpret_cast<Kept<KEEP ? KEEP : 1>*>(room));
         return;
     }
     const int64_t t = blockIdx.x - kv_ctas;
@@ -264,28 +323,44 @@ __global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendArg
     }
 }
 
-template <int XT, int VEC, int TEAM, bool FOURS>
+template <int XT, int VEC, int TEAM, int KEEP, bool FOURS>
 cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
-    // windows of a token while there are CTAs for them all, so that sequences' tokens go to teams of
+    // windows of a token while there are warps for them all, so that sequences' tokens go to teams of
     // their own; else as long as a block, where most windows begin one
-    const int64_t units = (int64_t)a.T * 2 * a.kv.kv_heads;
-    const int window = units <= 4096 ? 1 : std::min(32, a.kv.scale_tokens);
+    const int window = few(a) ? 1 : std::min(32, a.kv.scale_tokens);
     const int64_t teams = ((int64_t)a.T + window - 1) / window * 2 * a.kv.kv_heads, per = kThreads / TEAM;
     const int64_t kv_ctas = (teams + per - 1) / per;
-    if (kv_ctas + a.T > 0x7fffffff) return cudaErrorInvalidValue;
-    return launch_pdl(append_blocks_kernel<XT, VEC, TEAM, FOURS>, dim3((unsigned)(kv_ctas + a.T)), dim3(kThreads), 0, st, a,
-                      window, (int)kv_ctas);
+    // many queries go faster through the ring of the plain append's kernel, as tokens that are not appended
+    const bool alone = !few(a);
+    if (alone) {
+        AppendArgs q = a;
+        q.kv.kv_heads = 0;
+        q.kv.type = a.type;
+        cudaError_t err = launch_append(q, st);
+        if (err != cudaSuccess) return err;
+    }
+    const int64_t grid = kv_ctas + (alone ? 0 : a.T);
+    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+    const auto kernel = append_blocks_kernel<XT, VEC, TEAM, KEEP, FOURS>;
+    constexpr int smem = KEEP ? (int)sizeof(Kept<KEEP ? KEEP : 1>) : 0;
+    static std::atomic<uint64_t> configured;
+    cudaError_t err = ensure_smem_limit((const void*)kernel, smem, configured, true);
+    if (err != cudaSuccess) return err;
+    return launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), smem, st, a, window, (int)kv_ctas);
 }
 
-template <int XT, int TEAM>
-cudaError_t launch_fours(const AppendArgs& a, cudaStream_t st) {
-    return fours_of(a) ? launch<XT, 8, TEAM, true>(a, st) : launch<XT, 8, TEAM, false>(a, st);
+template <int XT, bool FOURS>
+cudaError_t launch_team(const AppendArgs& a, cudaStream_t st) {
+    constexpr bool ring = FOURS && XT != MOE_F32;
+    // a warp turns 512 / head_dim tokens at a time: few for a long block, which four warps share, and enough
+    // for a block that gets a token or two, as those of a decode step do
+    return a.kv.scale_tokens <= 8 || few(a) ? launch<XT, 8, 32, ring ? 4 : 0, FOURS>(a, st)
+                                            : launch<XT, 8, kThreads, ring ? 4 : 0, FOURS>(a, st);
 }
 
 template <int XT>
-cudaError_t launch_team(const AppendArgs& a, cudaStream_t st) {
-    // a warp turns 512 / head_dim tokens at a time: few for a long block, which four warps share
-    return a.kv.scale_tokens <= 8 ? launch_fours<XT, 32>(a, st) : launch_fours<XT, kThreads>(a, st);
+cudaError_t launch_fours(const AppendArgs& a, cudaStream_t st) {
+    return fours_of(a) ? launch_team<XT, true>(a, st) : launch_team<XT, false>(a, st);
 }
 
 }  // namespace
@@ -293,11 +368,11 @@ cudaError_t launch_team(const AppendArgs& a, cudaStream_t st) {
 cudaError_t launch_append_blocks(const AppendArgs& a, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
     if (append_fits(a, 8)) {
-        if (a.type == MOE_BF16) return launch_team<MOE_BF16>(a, st);
-        if (a.type == MOE_F16) return launch_team<MOE_F16>(a, st);
-        return launch_team<MOE_F32>(a, st);
+        if (a.type == MOE_BF16) return launch_fours<MOE_BF16>(a, st);
+        if (a.type == MOE_F16) return launch_fours<MOE_F16>(a, st);
+        return launch_fours<MOE_F32>(a, st);
     }
-    return append_fits(a, 4) ? launch<kAny, 4, kThreads, false>(a, st) : launch<kAny, 1, kThreads, false>(a, st);
+    return append_fits(a, 4) ? launch<kAny, 4, kThreads, 0, false>(a, st) : launch<kAny, 1, kThreads, 0, false>(a, st);
 }
 
 }  // namespace moe

@@ -3,7 +3,6 @@
 #pragma once
 
 #include <algorithm>
-#include <type_traits>
 
 #include "ptx.cuh"
 #include "vec.cuh"
@@ -131,20 +130,6 @@ __device__ __forceinline__ Pair mul2(Pair a, Pair b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
 }
-// The same on two registers: an instruction each, which takes constants as immediates, where a pair's
-// constants would need registers of their own.  The results are the same bits.
-struct Two {
-    float a, b;
-};
-__device__ __forceinline__ void unpair(Two p, float& a, float& b) { a = p.a, b = p.b; }
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) { return {fmaf(a.a, b.a, c.a), fmaf(a.b, b.b, c.b)}; }
-__device__ __forceinline__ Two mul2(Two a, Two b) { return {__fmul_rn(a.a, b.a), __fmul_rn(a.b, b.b)}; }
-template <class P>
-__device__ __forceinline__ P two_of(float a, float b) {
-    if constexpr (std::is_same_v<P, Pair>) return pair(a, b);
-    else return P{a, b};
-}
-
 __device__ __forceinline__ float fast_rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -160,16 +145,14 @@ __device__ __forceinline__ float fast_rcp(float x) {
 // all 2^-18 of the value at most, wherever it is a normal fp32 number (2048 x 4096 x 512 23.8 us;
 // 22.2 with Abramowitz and Stegun 7.1.28, which is good to 5e-7 absolutely alone).  At 64 the tail has long
 // vanished; the argument is held there, so that no infinity is multiplied by 0.
-template <class P>
 __device__ __forceinline__ void gelu2(float& v0, float& v1) {
-    const auto pair = [](float a, float b) { return two_of<P>(a, b); };
     const float x0 = fabsf(v0), x1 = fabsf(v1);
-    const P x = pair(fminf(x0, 64.f), fminf(x1, 64.f));
-    auto both = [](float c) { return two_of<P>(c, c); };
+    const Pair x = pair(fminf(x0, 64.f), fminf(x1, 64.f));
+    auto both = [](float c) { return pair(c, c); };
     float d0, d1;
     unpair(fma2(x, both(0.3f), both(1.f)), d0, d1);
-    const P t = pair(fast_rcp(d0), fast_rcp(d1));
-    P p = fma2(t, both(0.0354237072f), both(-0.156158343f));
+    const Pair t = pair(fast_rcp(d0), fast_rcp(d1));
+    Pair p = fma2(t, both(0.0354237072f), both(-0.156158343f));
     p = fma2(p, t, both(0.204556614f));
     p = fma2(p, t, both(-0.0520338714f));
     p = fma2(p, t, both(0.127691701f));
@@ -177,46 +160,44 @@ __device__ __forceinline__ void gelu2(float& v0, float& v1) {
     p = fma2(p, t, both(0.120712131f));
     p = fma2(p, t, both(0.119632006f));
     constexpr float kC = 0.72134752f;  // log2(e) / 2
-    const P xc = mul2(x, both(-kC)), z = mul2(xc, x), minus_z = mul2(z, both(-1.f));
-    const P rest = fma2(fma2(x, both(-kC), mul2(xc, both(-1.f))), x, fma2(xc, x, minus_z));
+    const Pair xc = mul2(x, both(-kC)), z = mul2(xc, x), minus_z = mul2(z, both(-1.f));
+    const Pair rest = fma2(fma2(x, both(-kC), mul2(xc, both(-1.f))), x, fma2(xc, x, minus_z));
     float z0, z1;
     unpair(z, z0, z1);
-    P tail = mul2(pair(fast_exp2(z0), fast_exp2(z1)), mul2(p, t));
+    Pair tail = mul2(pair(fast_exp2(z0), fast_exp2(z1)), mul2(p, t));
     tail = fma2(tail, mul2(rest, both(0.693147181f)), tail);
-    const P pos = fma2(pair(v0, v1), both(0.5f), mul2(pair(x0, x1), both(0.5f)));
+    const Pair pos = fma2(pair(v0, v1), both(0.5f), mul2(pair(x0, x1), both(0.5f)));
     unpair(fma2(mul2(x, both(-1.f)), tail, pos), v0, v1);
 }
 
 // SiLU of two values, v / (1 + exp(-v)), by the exponential that cannot overflow: v / (1 + e) above 0
 // and v e / (1 + e) below, e = exp(-|v|) = 2^z with what z loses to rounding brought back as a
 // factor.  2^-20 of the value at most.  At 256 e has long vanished, and no infinity meets another.
-template <class P>
 __device__ __forceinline__ void silu2(float& v0, float& v1) {
-    const auto pair = [](float a, float b) { return two_of<P>(a, b); };
     constexpr float kL = 1.4426950216293335f, kRest = 1.925963033500011e-08f;  // log2(e) and the rest of it
-    auto both = [](float c) { return two_of<P>(c, c); };
+    auto both = [](float c) { return pair(c, c); };
     const float x0 = fminf(fabsf(v0), 256.f), x1 = fminf(fabsf(v1), 256.f);
-    const P down = pair(-x0, -x1), z = mul2(down, both(kL)), minus_z = mul2(pair(x0, x1), both(kL));
-    const P rest = fma2(down, both(kRest), fma2(down, both(kL), minus_z));
+    const Pair down = pair(-x0, -x1), z = mul2(down, both(kL)), minus_z = mul2(pair(x0, x1), both(kL));
+    const Pair rest = fma2(down, both(kRest), fma2(down, both(kL), minus_z));
     float z0, z1, d0, d1, e0, e1;
     unpair(z, z0, z1);
-    P e = pair(fast_exp2(z0), fast_exp2(z1));
+    Pair e = pair(fast_exp2(z0), fast_exp2(z1));
     e = fma2(e, mul2(rest, both(0.693147181f)), e);
     unpair(fma2(e, both(1.f), both(1.f)), d0, d1);
     unpair(e, e0, e1);
-    const P up = mul2(pair(v0, v1), pair(v0 > 0.f ? 1.f : e0, v1 > 0.f ? 1.f : e1));
+    const Pair up = mul2(pair(v0, v1), pair(v0 > 0.f ? 1.f : e0, v1 > 0.f ? 1.f : e1));
     unpair(mul2(up, pair(fast_rcp(d0), fast_rcp(d1))), v0, v1);
 }
 
-template <int VEC, class P = Pair>
+template <int VEC>
 __device__ __forceinline__ void activate(float (&v)[VEC], int act) {
     if (act == MOE_ACT_NONE) return;
     if (act == MOE_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < VEC; i += 2) gelu2<P>(v[i], v[i + 1]);
+        for (int i = 0; i < VEC; i += 2) gelu2(v[i], v[i + 1]);
     } else if (act == MOE_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < VEC; i += 2) silu2<P>(v[i], v[i + 1]);
+        for (int i = 0; i < VEC; i += 2) silu2(v[i], v[i + 1]);
     } else if (act == MOE_ACT_RELU) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];

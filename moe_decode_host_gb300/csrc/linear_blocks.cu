@@ -317,18 +317,6 @@ __device__ __forceinline__ void keep_columns(uint32_t at, const float (&v)[16]) 
         : "memory");
 }
 
-// Activation of 16 values, two after two: all at once would not leave the sums their registers.
-__device__ __forceinline__ void activate_in_turn(float (&v)[16], int act) {
-    if (act == MOE_ACT_NONE) return;
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-        if (i > 0) asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]) : "f"(v[i - 2]), "f"(v[i - 1]));
-        float w[2] = {v[i], v[i + 1]};
-        activate<2, Two>(w, act);
-        v[i] = w[0], v[i + 1] = w[1];
-    }
-}
-
 // A piece holds 32 rows (a lane each) of 64 bytes; 16-byte part j of row r is in place j ^ (r / 2 % 4), as TMA's
 // 64-byte swizzle has it, so that 8 lanes meet every bank once.
 __device__ __forceinline__ uint4* part_of(uint8_t* piece, int row, int j) {
@@ -386,38 +374,39 @@ __device__ __forceinline__ void put_row(uint8_t* piece, int lane, int first, flo
     }
 }
 
-// Outputs [n0, n1) (at most 16) of 32 tokens from t0, rows of any alignment: fp32 through the piece, then an output of
-// every other token a lane, so that half a warp's stores are consecutive.
+// Outputs [n0, n1) (at most 32) of 32 tokens from t0, rows of any alignment, from sums that `stage` holds (stage_row): a
+// lane takes an output of every token, so that a warp's stores and residuals are consecutive.
 template <int YT>
-__device__ __forceinline__ void put_columns(const LinearArgs& a, uint8_t* piece, int lane, int t0, int n0, int n1, const float (&v)[16]) {
+__device__ __forceinline__ void put_columns(const LinearArgs& a, const uint8_t* stage, int lane, int t0, int n0, int n1) {
     constexpr int kSize = YT == MOE_F32 ? 4 : 2;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<float4*>(part_of(piece, lane, j)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    __syncwarp();
-    const int n = lane & 15, rows = min(32, a.T - t0);
-    if (n0 + n < n1) {
-        uint8_t* to = static_cast<uint8_t*>(a.y) + ((int64_t)(t0 + lane / 16) * a.y_stride + n0 + n) * kSize;
-        const uint8_t* from = static_cast<const uint8_t*>(a.res) + ((int64_t)(t0 + lane / 16) * a.res_stride + n0 + n) * kSize;
+    const int rows = min(32, a.T - t0);
+    if (n0 + lane < n1) {
+        uint8_t* to = static_cast<uint8_t*>(a.y) + ((int64_t)t0 * a.y_stride + n0 + lane) * kSize;
+        const uint8_t* from = static_cast<const uint8_t*>(a.res) + ((int64_t)t0 * a.res_stride + n0 + lane) * kSize;
 #pragma unroll 1
-        for (int r0 = lane >> 4; r0 < rows; r0 += 8) {
-            Raw<1> raw[4];
+        for (int r0 = 0; r0 < rows; r0 += 16) {
+            Raw<1> raw[16];
             if (a.res) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i, from += 2 * a.res_stride * kSize)
-                    if (r0 + 2 * i < rows) raw[i].load(from, 0, YT);
+                for (int i = 0; i < 16; ++i, from += a.res_stride * kSize)
+                    if (r0 + i < rows) raw[i].load(from, 0, YT);
+            }
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                v[i] = *reinterpret_cast<const float*>(stage + (r0 + i) * 128 + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4);
+            if (a.res) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float f[1] = {0.f};
+                    if (r0 + i < rows) raw[i].get(YT, f);
+                    v[i] += f[0];
+                }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i, to += 2 * a.y_stride * kSize) {
-                const int r = r0 + 2 * i;
-                if (r >= rows) break;
-                float one[1] = {reinterpret_cast<const float*>(part_of(piece, r, n >> 2))[n & 3]};
-                if (a.res) {
-                    float f[1];
-                    raw[i].get(YT, f);
-                    one[0] += f[0];
-                }
-                store_run<1>(to, 0, YT, one);
+            for (int i = 0; i < 16; ++i, to += a.y_stride * kSize) {
+                const float one[1] = {v[i]};
+                if (r0 + i < rows) store_run<1>(to, 0, YT, one);
             }
         }
     }
@@ -427,13 +416,13 @@ __device__ __forceinline__ void put_columns(const LinearArgs& a, uint8_t* piece,
 // The end of an adding warp's tile: 32 tokens from t0 and 16 W outputs from n0, from sums in tensor memory at `sums`.
 // Aligned rows: as many pieces as there are room for, two chunks of 16 at a time so that one's way hides the other's,
 // then their stores; the residuals of the first ones are on their way since the tile began.
-template <int YT, int W>
+template <int YT, int W, bool LEAN>
 __device__ __forceinline__ void finish_tile(const LinearArgs& a, const CUtensorMap* ymap, const CUtensorMap* rmap, uint8_t* pieces,
                                             uint64_t* res_full, unsigned& res_phase, const float* bias, int lane, int t0, int n0,
                                             uint32_t sums, bool vec, Head<kMaxAcc>& hd) {
     constexpr int kSize = YT == MOE_F32 ? 4 : 2, kPer = YT == MOE_F32 ? 1 : 2;  // chunks of 16 in a piece
     constexpr int kRound = W < kPieces * kPer ? W : kPieces * kPer;             // chunks between stores
-    const auto value = [&](int c, float (&v)[16]) {
+    const auto value = [&](int c, float (&v)[16], int act) {
         tc_ld16(sums + 16 * c, v);
         if (a.bias) {
 #pragma unroll
@@ -442,10 +431,10 @@ __device__ __forceinline__ void finish_tile(const LinearArgs& a, const CUtensorM
                 v[j] += p.x, v[j + 1] += p.y, v[j + 2] += p.z, v[j + 3] += p.w;
             }
         }
-        activate_in_turn(v, a.act);
+        activate<16>(v, act);
     };
     if (t0 >= a.T || n0 >= a.N) return;
-    if (vec) {
+    if (LEAN || vec) {
 #pragma unroll 1
         for (int c0 = 0; c0 < W && n0 + 16 * c0 < a.N; c0 += kRound) {
             const int x = (n0 + 16 * c0) * kSize, count = min(kRound / kPer, (a.N * kSize - x + 63) / 64);
@@ -462,7 +451,7 @@ __device__ __forceinline__ void finish_tile(const LinearArgs& a, const CUtensorM
 #pragma unroll 2
             for (int c = 0; c < kRound; ++c) {
                 float v[16];
-                value(c0 + c, v);
+                value(c0 + c, v, LEAN ? MOE_ACT_NONE : a.act);
                 put_row<YT>(pieces + c / kPer * kPiece, lane, c % kPer * 2, v, a.res != nullptr);
             }
             fence_proxy_async_shared();
@@ -471,10 +460,12 @@ __device__ __forceinline__ void finish_tile(const LinearArgs& a, const CUtensorM
         }
     } else {
 #pragma unroll 1
-        for (int c = 0; c < W && n0 + 16 * c < a.N; ++c) {
-            float v[16];
-            value(c, v);
-            put_columns<YT>(a, pieces + (c & 1) * kPiece, lane, t0, n0 + 16 * c, min(n0 + 16 * c + 16, a.N), v);
+        for (int c = 0; c < W && n0 + 16 * c < a.N; c += 2) {
+            float v0[16], v1[16];
+            value(c, v0, a.act);
+            value(c + 1, v1, a.act);
+            stage_row(pieces, lane, v0, v1);
+            put_columns<YT>(a, pieces, lane, t0, n0 + 16 * c, min(n0 + 16 * c + 32, a.N));
         }
     }
 }
@@ -504,8 +495,9 @@ __device__ __forceinline__ void mma_block(uint32_t d, uint64_t ad, uint64_t bd, 
 }
 
 // A CTA pair works on 256 tokens x BN outputs; each CTA has 128 tokens, an adding warp 32 of them (a lane each) and
-// half of the outputs.
-template <int BN>
+// half of the outputs.  LEAN: rows that TMA takes and no activation, whose code costs the sums' loop registers (8192 x
+// 6144 x 4096 196 us with it there).
+template <int BN, bool LEAN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBlockThreads, 1)
     blocks_tile_kernel(const LinearArgs a, const BlockScales sc, const __grid_constant__ CUtensorMap wmap,
                        const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap ymap,
@@ -658,7 +650,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBlockThreads, 1)
             int m, n;
             tile_of(g, i, m, n);
             const int t0 = m * 256 + (int)rank * 128 + q * 32, n0 = n * BN + n_mine;
-            if (vec && a.res && t0 < a.T && n0 < a.N) {  // the first pieces' residuals
+            if ((LEAN || vec) && a.res && t0 < a.T && n0 < a.N) {  // the first pieces' residuals
                 const int size = a.y_type == MOE_F32 ? 4 : 2;
                 stores_read();
                 load_pieces(pieces, &rmap, n0 * size, t0, min(min(kPieces, W * size / 4), ((a.N - n0) * size + 63) / 64), res_full);
@@ -704,9 +696,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBlockThreads, 1)
             tc_wait_st();
             const float* bias = sh.bias[slot] + n_mine;
             slot = slot == 2 ? 0 : slot + 1;
-            if (a.y_type == MOE_BF16) finish_tile<MOE_BF16, W>(a, &ymap, &rmap, pieces, res_full, rph, bias, lane, t0, n0, held, vec, hd);
-            else if (a.y_type == MOE_F16) finish_tile<MOE_F16, W>(a, &ymap, &rmap, pieces, res_full, rph, bias, lane, t0, n0, held, vec, hd);
-            else finish_tile<MOE_F32, W>(a, &ymap, &rmap, pieces, res_full, rph, bias, lane, t0, n0, held, vec, hd);
+            if (a.y_type == MOE_BF16) finish_tile<MOE_BF16, W, LEAN>(a, &ymap, &rmap, pieces, res_full, rph, bias, lane, t0, n0, held, vec, hd);
+            else if (a.y_type == MOE_F16) finish_tile<MOE_F16, W, LEAN>(a, &ymap, &rmap, pieces, res_full, rph, bias, lane, t0, n0, held, vec, hd);
+            else finish_tile<MOE_F32, W, LEAN>(a, &ymap, &rmap, pieces, res_full, rph, bias, lane, t0, n0, held, vec, hd);
             tc_fence_before();
             __syncwarp();
             arrive_cluster_relaxed(acc_empty + 8 * buf, lane == 0);
@@ -776,13 +768,15 @@ cudaError_t launch_tiles(const LinearArgs& a, const BlockScales& sc, bool vec, c
                                                (uint64_t)(stride * size), 64, 32, CU_TENSOR_MAP_SWIZZLE_64B);
     };
     vec = vec && (int64_t)a.N * size % 16 == 0 && pieces(&ymap, a.y, a.y_stride) && (!a.res || pieces(&rmap, a.res, a.res_stride));
-    const auto kernel = blocks_tile_kernel<BN>;
-    static std::atomic<uint64_t> configured;
-    cudaError_t err = ensure_smem_limit((const void*)kernel, kBlockSmem, configured);
-    if (err != cudaSuccess) return err;
     const Tiles g{(a.T + 255) / 256, (a.N + BN - 1) / BN, std::min(kMaxStages, kBlockRing / (kABytes + BN / 2 * kRowBytes))};
     const int pairs = std::min(a.sm_count / 2, g.tm * g.tn);
-    return launch_pdl(kernel, dim3(2 * pairs), dim3(kBlockThreads), kBlockSmem, st, a, sc, wmap, xmap, ymap, rmap, g, vec);
+    const auto go = [&](auto kernel, std::atomic<uint64_t>& configured) {
+        cudaError_t err = ensure_smem_limit((const void*)kernel, kBlockSmem, configured);
+        if (err != cudaSuccess) return err;
+        return launch_pdl(kernel, dim3(2 * pairs), dim3(kBlockThreads), kBlockSmem, st, a, sc, wmap, xmap, ymap, rmap, g, vec);
+    };
+    static std::atomic<uint64_t> configured[2];
+    return vec && a.act == MOE_ACT_NONE ? go(blocks_tile_kernel<BN, true>, configured[1]) : go(blocks_tile_kernel<BN, false>, configured[0]);
 }
 
 }  // namespace
