@@ -49,6 +49,11 @@ struct Place {
 __device__ __forceinline__ Place place_of(const AppendArgs& a, int64_t t) {
     Place p{{0, 0, 0, 0}, true};
     if (a.rot == 0) return p;
+    if (a.axes == 1) {
+        p.pos[0] = a.positions[t];
+        p.valid = p.pos[0] >= 0 && p.pos[0] < a.n_positions;
+        return p;
+    }
 #pragma unroll
     for (int i = 0; i < kMaxAxes; ++i)
         if (i < a.axes) {

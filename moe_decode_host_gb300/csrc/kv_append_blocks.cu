@@ -75,7 +75,7 @@ __device__ __forceinline__ void team_sync() {
 // for keys, the cosines and sines of their pairs, and the tokens' entries in the block.
 template <int KEEP>
 struct Kept {
-    uint4 piece[KEEP][6][kThreads];
+    uint4 piece[KEEP][6][kThreads];  // two runs; four of the table, or the turned values
     int at[KEEP][kThreads];  // -1: not appended
 };
 
@@ -156,11 +156,22 @@ __device__ __forceinline__ void append_block_runs(const AppendArgs& a, int64_t w
                 asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
             }
         };
-        // values of token t, or of the k-th of those kept, turned; its entry, or -1
-        auto values = [&](int64_t t, int k, float (&x0)[VEC], float (&x1)[VEC]) {
+        // values of token t, or of the k-th of those kept, turned; its entry, or -1.  Turned ones take the table's place
+        // in what is kept; `again`: they are there
+        auto values = [&](int64_t t, int k, bool again, float (&x0)[VEC], float (&x1)[VEC]) {
             if constexpr (KEEP > 0) {
                 const int at = kept.at[k][threadIdx.x];
                 if (at < 0) return at;
+                uint4* piece = &kept.piece[k][0][threadIdx.x];
+                if (turn && again) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float* x = i < 2 ? x0 + 4 * i : x1 + 4 * (i - 2);
+                        const float4 v = *reinterpret_cast<const float4*>(piece + (2 + i) * kThreads);
+                        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+                    }
+                    return at;
+                }
                 Raw<VEC, false> r0, r1;
                 r0.set(&kept.piece[k][0][threadIdx.x], 0);
                 r1.set(&kept.piece[k][1][threadIdx.x], 0);
@@ -177,6 +188,11 @@ __device__ __forceinline__ void append_block_runs(const AppendArgs& a, int64_t w
                         sn[4 * i + 2] = __uint_as_float(s.z), sn[4 * i + 3] = __uint_as_float(s.w);
                     }
                     rotate<VEC>(a.interleaved, x0, x1, cs, sn);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float* x = i < 2 ? x0 + 4 * i : x1 + 4 * (i - 2);
+                        *reinterpret_cast<float4*>(piece + (2 + i) * kThreads) = make_float4(x[0], x[1], x[2], x[3]);
+                    }
                 }
                 return at;
             } else {
@@ -196,6 +212,8 @@ __device__ __forceinline__ void append_block_runs(const AppendArgs& a, int64_t w
                 return at;
             }
         };
+        float top = 0.f;
+        bool anew = false;
         constexpr int kEach = KEEP > 0 ? KEEP : 1;  // tokens of a thread at a time
         const bool once = t1 - t0 <= (int64_t)kEach * step;
         auto all = [&](bool again, auto&& use) {  // every token of this thread
@@ -207,13 +225,30 @@ __device__ __forceinline__ void append_block_runs(const AppendArgs& a, int64_t w
                     const int64_t t = c + g + (int64_t)k * step;
                     if (!works || t >= t1) break;
                     float x0[VEC], x1[VEC];
-                    const int at = values(t, k, x0, x1);
+                    if constexpr (KEEP > 0) {
+                        // the largest magnitude of 16-bit values that are not turned, from their bits: two an instruction
+                        if (!again && !turn) {
+                            const int at = kept.at[k][threadIdx.x];
+                            if (at < 0) continue;
+                            constexpr uint32_t kInf = XT == MOE_BF16 ? 0x7f80u : 0x7c00u;
+                            const uint4 p = kept.piece[k][0][threadIdx.x], q = kept.piece[k][1][threadIdx.x];
+                            const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+                            uint32_t most = 0;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) most = __vmaxu2(most, w[i] & 0x7fff7fffu);
+                            most = max(most & 0xffffu, most >> 16);
+                            if (most <= kInf) {  // else there is a NaN, which does not count: one by one
+                                top = fmaxf(top, half_bits_to_f32(most, XT));
+                                anew = anew || at == 0;
+                                continue;
+                            }
+                        }
+                    }
+                    const int at = values(t, k, again && once, x0, x1);
                     if (at >= 0) use(x0, x1, at);
                 }
             }
         };
-        float top = 0.f;
-        bool anew = false;
         all(false, [&](const float (&x0)[VEC], const float (&x1)[VEC], int entry) {
             anew = anew || entry == 0;
 #pragma unroll
@@ -354,7 +389,7 @@ cudaError_t launch_team(const AppendArgs& a, cudaStream_t st) {
     constexpr bool ring = FOURS && XT != MOE_F32;
     // a warp turns 512 / head_dim tokens at a time: few for a long block, which four warps share, and enough
     // for a block that gets a token or two, as those of a decode step do
-    return a.kv.scale_tokens <= 8 || few(a) ? launch<XT, 8, 32, ring ? 4 : 0, FOURS>(a, st)
+    return a.kv.scale_tokens <= 8 || few(a) ? launch<XT, 8, 32, ring ? 2 : 0, FOURS>(a, st)
                                             : launch<XT, 8, kThreads, ring ? 4 : 0, FOURS>(a, st);
 }
 
