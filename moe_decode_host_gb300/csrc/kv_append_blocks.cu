@@ -34,7 +34,7 @@ __device__ __forceinline__ float scale_for(float top) {
 // The block that a slot lies in, as the slot of its first entry; negative: the token is not appended.
 struct Home {
     int64_t first;
-    int page, entry;  // of the slot
+    int page, block;
 };
 __device__ __forceinline__ Home home_of(const AppendArgs& a, int64_t slot) {
     Home h{-1, 0, 0};
@@ -44,9 +44,10 @@ __device__ __forceinline__ Home home_of(const AppendArgs& a, int64_t slot) {
         set_status(a.kv.status, MOE_ERR_BAD_INDEX);
         return h;
     }
+    const int entry = (int)(slot - page * a.kv.page_size);
     h.page = (int)page;
-    h.entry = (int)(slot - page * a.kv.page_size);
-    h.first = slot - h.entry + (int64_t)block_of(a.kv, h.entry) * a.kv.scale_tokens;
+    h.block = block_of(a.kv, entry);
+    h.first = slot - entry + h.block * a.kv.scale_tokens;
     return h;
 }
 
@@ -95,31 +96,34 @@ __device__ __forceinline__ void append_block_runs(const AppendArgs& a, int64_t w
     uint8_t* cache = static_cast<uint8_t*>(side ? a.kv.v : a.kv.k) + head * a.kv.head_stride;
     float* scales = side ? a.kv.v_scale : a.kv.k_scale;
     const bool turn = it.turn && side == 0;
-    // lane i: the home of token w0 + i; a run begins where it differs from the token before
-    const int64_t mine = lane < window && w0 + lane < a.T ? home_of(a, a.slots[w0 + lane]).first : -1;
+    // lane i: the home of token w0 + i.  A block is scale_tokens slots in a row, so that only this takes a division:
+    // a run begins where the token before is in another one
+    const auto within = [&](int64_t slot, int64_t first) { return (uint64_t)(slot - first) < (uint64_t)a.kv.scale_tokens; };
+    const int64_t mine = lane < window && w0 + lane < a.T ? a.slots[w0 + lane] : -1;
     int64_t before = __shfl_up_sync(0xffffffffu, mine, 1);
-    if (lane == 0) before = w0 > 0 ? home_of(a, a.slots[w0 - 1]).first : -1;
-    uint32_t begins = __ballot_sync(0xffffffffu, mine >= 0 && mine != before);
+    if (lane == 0) before = w0 > 0 ? a.slots[w0 - 1] : -1;
+    const Home my_home = home_of(a, mine);
+    uint32_t begins = __ballot_sync(0xffffffffu, my_home.first >= 0 && (before < 0 || !within(before, my_home.first)));
     while (begins) {  // the same in every warp of the team
         const int i0 = __ffs(begins) - 1;
         begins &= begins - 1;
-        const int64_t t0 = w0 + i0, first = __shfl_sync(0xffffffffu, mine, i0);
+        const int64_t t0 = w0 + i0, first = __shfl_sync(0xffffffffu, my_home.first, i0);
+        const int page = __shfl_sync(0xffffffffu, my_home.page, i0), block = __shfl_sync(0xffffffffu, my_home.block, i0);
         // the run's end: the next token of another home, maybe behind the window
-        const uint32_t others = __ballot_sync(0xffffffffu, lane > i0 && mine != first);
+        const uint32_t others = __ballot_sync(0xffffffffu, lane > i0 && (mine < 0 || !within(mine, first)));
         int64_t t1 = others ? w0 + __ffs(others) - 1 : w0 + 32;
         if (!others || t1 >= w0 + window) {
             t1 = w0 + window;
             for (bool on = true; on && t1 < a.T;) {
                 const int64_t t = t1 + lane;
-                const uint32_t same = __ballot_sync(0xffffffffu, t < a.T && home_of(a, a.slots[t]).first == first);
+                const uint32_t same = __ballot_sync(0xffffffffu, t < a.T && within(a.slots[t], first));
                 on = same == 0xffffffffu;
                 t1 += on ? 32 : __ffs(~same) - 1;
             }
             if (t1 > a.T) t1 = a.T;
         }
-        const Home home = home_of(a, first);
-        const int64_t base = (int64_t)home.page * a.kv.page_stride + (int64_t)home.entry * a.kv.token_stride;
-        float* scale_at = scales + ((int64_t)home.page * a.kv.blocks + block_of(a.kv, home.entry)) * a.kv.kv_heads + head;
+        const int64_t base = (int64_t)page * a.kv.page_stride + (int64_t)(block * a.kv.scale_tokens) * a.kv.token_stride;
+        float* scale_at = scales + ((int64_t)page * a.kv.blocks + block) * a.kv.kv_heads + head;
         const float old = *scale_at;
 
         // the entry of a token in the block, or -1 where it has no position in the table
@@ -324,9 +328,9 @@ __global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendArg
     const int xt = XT == kAny ? a.type : XT;
     if ((int)blockIdx.x < kv_ctas) {
         const int heads = 2 * a.kv.kv_heads;
-        const int64_t unit = (int64_t)blockIdx.x * (kThreads / TEAM) + threadIdx.x / TEAM;
-        const int64_t w = unit / heads;
-        const int h = (int)(unit - w * heads);
+        const uint32_t unit = blockIdx.x * (kThreads / TEAM) + threadIdx.x / TEAM, w32 = unit / (uint32_t)heads;
+        const int64_t w = w32;
+        const int h = (int)(unit - w32 * heads);
         if (w * window < a.T)  // a team of one warp leaves alone; a CTA's has the same w
             append_block_runs<XT, VEC, TEAM, KEEP, FOURS>(a, w * window, window, h >= a.kv.kv_heads, h % a.kv.kv_heads,
                                                           mask[threadIdx.x / TEAM], part,
@@ -375,7 +379,7 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
         if (err != cudaSuccess) return err;
     }
     const int64_t grid = kv_ctas + (alone ? 0 : a.T);
-    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+    if (grid > 0x3fffffff) return cudaErrorInvalidValue;  // teams are numbered in 32 bits
     const auto kernel = append_blocks_kernel<XT, VEC, TEAM, KEEP, FOURS>;
     constexpr int smem = KEEP ? (int)sizeof(Kept<KEEP ? KEEP : 1>) : 0;
     static std::atomic<uint64_t> configured;
