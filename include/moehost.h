@@ -443,8 +443,8 @@ int moe_kv_destroy(moe_kv* kv);
  * head, so that no scale has to be known before the tokens are:
  *   value = scale[page][entry / scale_tokens][h] * code,
  * k_scale and v_scale device fp32 [n_pages][page_size / scale_tokens][kv_heads], contiguous, which
- * moe_kv_append writes and moe_kv_attend reads (a scale of the caller's own making may be any
- * number).  scale_tokens: 1 to 1024, a divisor of page_size.  The rest as moe_kv_create, and the handle
+ * moe_kv_append writes and moe_kv_attend reads (a scale of the caller's own making may have either
+ * sign).  scale_tokens: 1 to 1024, a divisor of page_size.  The rest as moe_kv_create, and the handle
  * is used in the same calls:
  *  moe_kv_append  gives a block the smallest power of two with which the largest magnitude among the
  *    tokens that it takes in, at most 448 * scale, held to 2^-126 and 2^119 (larger values, infinities among
@@ -453,7 +453,10 @@ int moe_kv_destroy(moe_kv* kv);
  *    where that is large enough; where it is not, the codes of its other entries are rewritten under the
  *    new one (exact but where codes of less than 2^-6 lose their low bits), so the block's scale has to be
  *    initialised (zero will do) before a block is begun in its middle.  The tokens of a call that go to
- *    one block have to follow one another in the call.
+ *    one block have to follow one another in the call, with none between them that goes elsewhere or
+ *    nowhere, and calls that append to one block have to be ordered.
+ *  moe_kv_attend  takes scales up to 2^96 in magnitude, keys and values of 2^104; a NaN among those of
+ *    attended tokens shows in that head's outputs.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA, MOE_ERR_NOMEM. */
 int moe_kv_create_blocks(const moe_kv_params* p, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
                          int scale_tokens, moe_kv** out);
@@ -511,7 +514,8 @@ int moe_kv_append_axes(moe_kv* kv, int type, const void* q, int64_t q_ts, int64_
  * timing of the GPU: the same call gives the same bits.
  * 0 <= B <= max_batch; scale finite.  The softmax is fp32; its weights meet the values as two
  * 16-bit terms each, which lose at most 2^-16 of a weight (bf16 caches), or 2^-22 of it and
- * 2^-31 of the largest one (f16, E4M3).
+ * 2^-31 of the largest one (f16, E4M3; with scales of blocks 2^-31 of the largest weight times the
+ * largest scale of a value met before it).
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
 int moe_kv_attend(moe_kv* kv, const void* q, int q_type, int64_t q_ts, int64_t q_hs, const int32_t* page_table,
                   int64_t table_stride, int max_pages, const int32_t* lengths, int B, float scale, int window,
@@ -551,7 +555,7 @@ int moe_linear(const void* x, int64_t x_stride, const void* w, int64_t w_stride,
  *  x_scale device fp32 [T][G], rows x_scale_stride apart; w_scale device fp32 [ceil(N / 128)][G], rows
  *    w_scale_stride apart: any numbers.
  * The rest as moe_linear.  The products of a block of K are summed by the tensor cores (fp32, towards zero
- * at every 32 of K), the blocks in fp32 to nearest.
+ * at every 32 of K), the blocks, times their two scales' product, in fp32 to nearest.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
 int moe_linear_blocks(const void* x, int64_t x_stride, const void* w, int64_t w_stride, int T, int N, int K,
                       const float* x_scale, int64_t x_scale_stride, const float* w_scale, int64_t w_scale_stride,

@@ -11,8 +11,11 @@
 // another in the call, so a team of threads (a warp where blocks are short, else four) takes what
 // the call puts into one block of one head of k or v: it turns the values, keeps them in registers
 // while their maximum is found, and writes codes and scale.  Teams look for the blocks that begin
-// in their window of tokens, so nothing has to be counted or sorted beforehand.  The queries are
-// turned by further CTAs of the same launch.
+// in their window of tokens, so nothing has to be counted or sorted beforehand.  The queries of small
+// calls are turned by further CTAs of the same launch, those of large ones by the plain append's kernel.
+//
+// Measured on a GB300: 8192 tokens of 32 + 8 + 8 heads of 128, bf16, into blocks of 64 64 us (29 of them the
+// queries'), blocks of 16 82; 8 tokens 3.4, 64 sequences 4.0, 512 sequences 11.0, 256 tokens of one 28.
 #include <algorithm>
 
 #include "kv_append.cuh"

@@ -5,8 +5,8 @@
 // Bound by the cache's bytes, each read once for a block of up to 32 query heads of a key
 // head (16 from head_dim 144 on).  Measured on a GB300, with the share of a plain copy's
 // rate: 32 ragged sequences (1.1 GB of bf16) 174 us (94%); 64 long ones in E4M3, 16 query
-// heads a key head (1.6 GB) 295 us (81%: issue latency); one sequence of 4097 tokens 13.5 us, 15.1
-// with its rows in memory and not in L2, a chain of latencies.
+// heads a key head (1.6 GB) 295 us (81%: issue latency), 307 with scales of blocks; one sequence of
+// 4097 tokens 13.5 us, 15.1 with its rows in memory and not in L2, a chain of latencies.
 //
 // Split.  The attended tokens of a (sequence, key head, block of query heads) form a
 // segment of units of 16 tokens (32 where a row is at most 128 bytes), and a few places more
@@ -24,7 +24,9 @@
 // same lanes for S and O, so rescaling needs no exchange.  E4M3 keys and values become
 // f16 in registers (exactly): the order of dimensions within a 16-wide step of the
 // contraction is free, so a lane's four consecutive bytes serve as its four elements, in the
-// tokens of V^T P^T as in the dimensions of K Q^T.  The weights P are two 16-bit terms each.
+// tokens of V^T P^T as in the dimensions of K Q^T.  The weights P are two 16-bit terms each.  With scales of
+// blocks of tokens each token's two come through the ring beside its rows: a key's multiplies its scores, a
+// value's its weights, over the largest power of two among them so far, in units of which the sums are kept.
 // mma.sync suffices: the products take 14% (bf16) and 46% (E4M3, 16 heads) of the tensor pipe,
 // and their operands come from registers.
 #pragma once
@@ -140,9 +142,9 @@ __device__ __forceinline__ int places_of(const Span& s, int unit) {
     return s.count > 0 ? (s.count + unit - 1) / unit + kStart : 0;
 }
 
-// T: 0 bf16, 1 f16, 2 E4M3 (computed in f16), 3 E4M3 with a scale for each block of tokens.  DP: head_dim (EXACT) or a bound of it; with
-// the dimension known no step of the products is conditional, and they overlap.  NT: blocks
-// of 8 query heads.
+// T: 0 bf16, 1 f16, 2 E4M3 (computed in f16), 3 E4M3 with a scale for each block of tokens.  DP:
+// head_dim (EXACT) or a bound of it; with the dimension known no step of the products is
+// conditional, and they overlap.  NT: blocks of 8 query heads.
 template <int T, int DP, int NT, bool EXACT>
 __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T >= 2 ? 1 : 2, NT))
     attend_kernel(const AttendArgs a, const AttendPlan p) {

@@ -10,11 +10,12 @@
 // elements) could not take, and the registers' sums are rounded to nearest, so that a long K loses less
 // than in the tensor cores' own sums.
 //
-// Measured on a GB300 (launches of a graph): 8192 x 6144 x 4096 with bias 184 us (2240 TFLOP/s; the plain
-// E4M3 product 117), 4096 x 4096 x 4096 73, 1024 x 4096 x 4096 24, 32 x 6144 x 4096 8.0, 1 x 4096 x 4096 5.2.
+// Measured on a GB300 (launches of a graph): 8192 x 6144 x 4096 with bias 173 us (2385 TFLOP/s; the plain
+// E4M3 product 115), with GELU 243, 4096 x 4096 x 4096 68, 1024 x 4096 x 4096 23, 777 x 5003 x 1424 f16 with GELU 27,
+// 32 x 6144 x 4096 7.8, 1 x 4096 x 4096 5.2 (6.4 with its weights in memory and not in L2).
 // What bounds the tiles is a circle of two accumulators: products (some 600 cycles for 256 x 256 outputs
 // and a block of K), their commit, the additions up to the last read of the accumulator (some 450) and the
-// arrival that lets the next products have it, 1550 cycles for two blocks of K.  The additions alone
+// arrival that lets the next products have it, 1500 cycles for two blocks of K.  The additions alone
 // are 256 cycles of fp32 work a block.
 #include <algorithm>
 
@@ -47,7 +48,7 @@ __global__ void __launch_bounds__(kThreads, CTAS)
     const int nkb = (a.K + kRowBytes - 1) / kRowBytes;
     const int kb0 = (int)((int64_t)nkb * rank / S), kb1 = (int)((int64_t)nkb * (rank + 1) / S);
     const int stage_bytes = kABytes + bn * kRowBytes;
-    constexpr int kPitch = CH == 1 ? 32 : 32 * CH;  // columns of an accumulator
+    constexpr int kPitch = 32 * CH;  // columns of an accumulator
     constexpr int kAccs = CTAS * kPitch >= 256 ? 2 : 4;
     constexpr int kCols = kAccs * kPitch;
     static_assert(CTAS * kCols <= 512 && kAccs <= kMaxAcc, "tensor memory of an SM");

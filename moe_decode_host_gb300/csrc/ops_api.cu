@@ -118,7 +118,6 @@ int append(moe_kv* kv, int type, const void* q, int64_t q_ts, int64_t q_hs, cons
     return cuda_status(kv->view.scale_tokens ? launch_append_blocks(a, S(stream)) : launch_append(a, S(stream)));
 }
 
-
 // What moe_linear and moe_linear_blocks check alike; `nothing`: a call without tokens, done.
 int linear_args(const void* x, int64_t x_stride, const void* w, int64_t w_stride, int in_type, int T, int N, int K,
                 const float* x_scale, const float* w_scale, const void* bias, int bias_type, int act,

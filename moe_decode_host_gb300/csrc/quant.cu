@@ -5,6 +5,9 @@
 // Memory bound: each element once in and once out.  A half warp holds a group, 8 elements a
 // lane, so that its maximum takes four exchanges and no shared memory; a half warp takes
 // several groups so that their loads are in flight together.
+//
+// Measured on a GB300: 8192 x 4096 bf16 21.0 us (4.8 TB/s, 72% of a plain copy's rate), 512 x 4096 2.3, 777 x 5003
+// fp32 at any alignment 5.5 (3.6 TB/s), 8 x 4096 1.3.
 #include <algorithm>
 
 #include "ptx.cuh"

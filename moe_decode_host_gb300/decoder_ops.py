@@ -1,7 +1,7 @@
 """The decoder-layer operators around the MoE layer: norm, cache append, attention, linear.
 
 Binding of moe_add_rms_norm, moe_quant_e4m3, moe_kv_*, moe_linear and moe_linear_blocks
-(include/moehost.h) for torch tensors.  Types, shapes and strides are read from the tensors and checked before the C
+(include/moehost.h) for torch tensors.  Types, shapes and strides are read from them and checked before the C
 call, which sees only pointers; a call that does not fit raises MoeError with
 MOE_ERR_INVALID_ARG and launches nothing.  Outputs are the caller's tensors.  The checks
 of the calls are native code (csrc/binding.cc), since a call on small inputs takes
