@@ -8,14 +8,14 @@
 // under them as under any other scale.
 //
 // Memory bound: q, k, v in, q_out and the codes out, each once.  The tokens of a block follow one
-// another in the call, so a team of threads (a warp where blocks are short, else four) takes what
+// another in the call, so a team of threads (a warp where that is little, else four) takes what
 // the call puts into one block of one head of k or v: it turns the values, keeps them in registers
 // while their maximum is found, and writes codes and scale.  Teams look for the blocks that begin
 // in their window of tokens, so nothing has to be counted or sorted beforehand.  The queries of small
 // calls are turned by further CTAs of the same launch, those of large ones by the plain append's kernel.
 //
 // Measured on a GB300: 8192 tokens of 32 + 8 + 8 heads of 128, bf16, into blocks of 64 64 us (29 of them the
-// queries'), blocks of 16 82; 8 tokens 3.4, 64 sequences 4.0, 512 sequences 11.0, 256 tokens of one 28.
+// queries'), blocks of 16 82; 8 tokens 3.4, 64 sequences 4.0, 512 sequences 11.5, 256 tokens of one 10.7.
 #include <algorithm>
 
 #include "kv_append.cuh"
@@ -83,12 +83,35 @@ struct Kept {
     int at[KEEP][kThreads];  // -1: not appended
 };
 
-// A team's share of k and v: the blocks that begin among `window` tokens from w0 on (at most 32), of
-// head `head` of k (side 0) or v (side 1).  KEEP > 0: 16-bit values and table rows that can be copied 16 bytes at
-// a time, KEEP tokens of a thread at once, so that a block that they hold is read once; 0: read twice.
+// The runs of tokens of one block that begin among `window` tokens from w0 on (at most 32), the same in every warp.
+struct Window {
+    int64_t mine;     // lane i: the slot of token w0 + i
+    Home home;        // and its home
+    uint32_t begins;  // bit i: a run begins with token w0 + i
+};
+__device__ __forceinline__ bool within(const AppendArgs& a, int64_t slot, int64_t first) {
+    return (uint64_t)(slot - first) < (uint64_t)a.kv.scale_tokens;
+}
+__device__ __forceinline__ Window window_of(const AppendArgs& a, int64_t w0, int window) {
+    const int lane = threadIdx.x & 31;
+    Window w;
+    // a block is scale_tokens slots in a row, so that only this takes a division: a run begins where the token before
+    // is in another one
+    w.mine = lane < window && w0 + lane < a.T ? a.slots[w0 + lane] : -1;
+    int64_t before = __shfl_up_sync(0xffffffffu, w.mine, 1);
+    if (lane == 0) before = w0 > 0 ? a.slots[w0 - 1] : -1;
+    w.home = home_of(a, w.mine);
+    w.begins = __ballot_sync(0xffffffffu, w.home.first >= 0 && (before < 0 || !within(a, before, w.home.first)));
+    return w;
+}
+
+// A team's share of k and v: the runs `begins` of the window, of head `head` of k (side 0) or v (side 1).
+// KEEP > 0: 16-bit values and table rows that can be copied 16 bytes at a time, KEEP tokens of a thread at
+// once, so that a block that they hold is read once; 0: read twice.
 template <int XT, int VEC, int TEAM, int KEEP, bool FOURS>
-__device__ __forceinline__ void append_block_runs(const AppendArgs& a, int64_t w0, int window, int side, int head,
-                                                  uint32_t* mask, float (*part)[kThreads / 32], Kept<KEEP ? KEEP : 1>& kept) {
+__device__ __forceinline__ void append_block_runs(const AppendArgs& a, const Window& win, uint32_t begins, int64_t w0,
+                                                  int window, int side, int head, uint32_t* mask,
+                                                  float (*part)[kThreads / 32], Kept<KEEP ? KEEP : 1>& kept) {
     const int me = threadIdx.x % TEAM, lane = threadIdx.x & 31;
     const int items = a.kv.head_dim / (2 * VEC), step = TEAM / items, g = me / items;
     const bool works = g < step;
@@ -99,27 +122,20 @@ __device__ __forceinline__ void append_block_runs(const AppendArgs& a, int64_t w
     uint8_t* cache = static_cast<uint8_t*>(side ? a.kv.v : a.kv.k) + head * a.kv.head_stride;
     float* scales = side ? a.kv.v_scale : a.kv.k_scale;
     const bool turn = it.turn && side == 0;
-    // lane i: the home of token w0 + i.  A block is scale_tokens slots in a row, so that only this takes a division:
-    // a run begins where the token before is in another one
-    const auto within = [&](int64_t slot, int64_t first) { return (uint64_t)(slot - first) < (uint64_t)a.kv.scale_tokens; };
-    const int64_t mine = lane < window && w0 + lane < a.T ? a.slots[w0 + lane] : -1;
-    int64_t before = __shfl_up_sync(0xffffffffu, mine, 1);
-    if (lane == 0) before = w0 > 0 ? a.slots[w0 - 1] : -1;
-    const Home my_home = home_of(a, mine);
-    uint32_t begins = __ballot_sync(0xffffffffu, my_home.first >= 0 && (before < 0 || !within(before, my_home.first)));
+    const int64_t mine = win.mine;
     while (begins) {  // the same in every warp of the team
         const int i0 = __ffs(begins) - 1;
         begins &= begins - 1;
-        const int64_t t0 = w0 + i0, first = __shfl_sync(0xffffffffu, my_home.first, i0);
-        const int page = __shfl_sync(0xffffffffu, my_home.page, i0), block = __shfl_sync(0xffffffffu, my_home.block, i0);
+        const int64_t t0 = w0 + i0, first = __shfl_sync(0xffffffffu, win.home.first, i0);
+        const int page = __shfl_sync(0xffffffffu, win.home.page, i0), block = __shfl_sync(0xffffffffu, win.home.block, i0);
         // the run's end: the next token of another home, maybe behind the window
-        const uint32_t others = __ballot_sync(0xffffffffu, lane > i0 && (mine < 0 || !within(mine, first)));
+        const uint32_t others = __ballot_sync(0xffffffffu, lane > i0 && (mine < 0 || !within(a, mine, first)));
         int64_t t1 = others ? w0 + __ffs(others) - 1 : w0 + 32;
         if (!others || t1 >= w0 + window) {
             t1 = w0 + window;
             for (bool on = true; on && t1 < a.T;) {
                 const int64_t t = t1 + lane;
-                const uint32_t same = __ballot_sync(0xffffffffu, t < a.T && within(a.slots[t], first));
+                const uint32_t same = __ballot_sync(0xffffffffu, t < a.T && within(a, a.slots[t], first));
                 on = same == 0xffffffffu;
                 t1 += on ? 32 : __ffs(~same) - 1;
             }
@@ -320,9 +336,12 @@ __device__ __forceinline__ void append_block_runs(const AppendArgs& a, int64_t w
 }
 
 // The first CTAs take k and v, a team per (window of tokens, head of either); the others, where there are any, a
-// token's queries each.
-template <int XT, int VEC, int TEAM, int KEEP, bool FOURS>
+// token's queries each.  FEW: a CTA per window of as many tokens as it has warps, which take a run each; the last run
+// is the only one that can reach behind the window, and if it does all of them take it (a prompt of 256 tokens
+// 10.7 us, 28 by a warp a block; 512 sequences of a token each 11.5 us, 11.0).
+template <int XT, int VEC, int TEAM, int KEEP, bool FOURS, bool FEW>
 __global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendArgs a, int window, int kv_ctas) {
+    static_assert(!FEW || TEAM == 32, "a run a warp");
     __shared__ uint32_t mask[kThreads / TEAM][kMaxScaleTokens / 32];
     __shared__ float part[2][kThreads / 32];
     extern __shared__ __align__(16) uint8_t room[];
@@ -330,14 +349,26 @@ __global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendArg
     grid_dep_wait();
     const int xt = XT == kAny ? a.type : XT;
     if ((int)blockIdx.x < kv_ctas) {
-        const int heads = 2 * a.kv.kv_heads;
-        const uint32_t unit = blockIdx.x * (kThreads / TEAM) + threadIdx.x / TEAM, w32 = unit / (uint32_t)heads;
-        const int64_t w = w32;
-        const int h = (int)(unit - w32 * heads);
-        if (w * window < a.T)  // a team of one warp leaves alone; a CTA's has the same w
-            append_block_runs<XT, VEC, TEAM, KEEP, FOURS>(a, w * window, window, h >= a.kv.kv_heads, h % a.kv.kv_heads,
-                                                          mask[threadIdx.x / TEAM], part,
-                                                          *reinterpret_cast<Kept<KEEP ? KEEP : 1>*>(room));
+        const int heads = 2 * a.kv.kv_heads, team = threadIdx.x / TEAM;
+        const uint32_t unit = FEW ? blockIdx.x : blockIdx.x * (kThreads / TEAM) + team, w32 = unit / (uint32_t)heads;
+        const int64_t w0 = (int64_t)w32 * window;
+        const int h = (int)(unit - w32 * heads), side = h >= a.kv.kv_heads, head = side ? h - a.kv.kv_heads : h;
+        Kept<KEEP ? KEEP : 1>& kept = *reinterpret_cast<Kept<KEEP ? KEEP : 1>*>(room);
+        if (w0 >= a.T) return;  // a team of one warp leaves alone; a CTA's has the same window
+        const Window win = window_of(a, w0, window);
+        if constexpr (FEW) {
+            if (!win.begins) return;  // the whole CTA
+            const int last = 31 - __clz(win.begins);
+            const int64_t first = __shfl_sync(0xffffffffu, win.home.first, last);
+            const bool beyond = w0 + window < a.T && within(a, a.slots[w0 + window], first) &&
+                                !__any_sync(0xffffffffu, threadIdx.x % 32 > last && threadIdx.x % 32 < window && !within(a, win.mine, first));
+            uint32_t own = beyond ? win.begins & ~(1u << last) : win.begins;
+            for (int i = 0; i < team; ++i) own &= own - 1;
+            if (own) append_block_runs<XT, VEC, 32, KEEP, FOURS>(a, win, own & -own, w0, window, side, head, mask[team], part, kept);
+            if (beyond) append_block_runs<XT, VEC, kThreads, KEEP, FOURS>(a, win, 1u << last, w0, window, side, head, mask[0], part, kept);
+        } else {
+            append_block_runs<XT, VEC, TEAM, KEEP, FOURS>(a, win, win.begins, w0, window, side, head, mask[team], part, kept);
+        }
         return;
     }
     const int64_t t = blockIdx.x - kv_ctas;
@@ -365,12 +396,12 @@ __global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendArg
     }
 }
 
-template <int XT, int VEC, int TEAM, int KEEP, bool FOURS>
+template <int XT, int VEC, int TEAM, int KEEP, bool FOURS, bool FEW = false>
 cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
-    // windows of a token while there are warps for them all, so that sequences' tokens go to teams of
-    // their own; else as long as a block, where most windows begin one
-    const int window = few(a) ? 1 : std::min(32, a.kv.scale_tokens);
-    const int64_t teams = ((int64_t)a.T + window - 1) / window * 2 * a.kv.kv_heads, per = kThreads / TEAM;
+    // short windows while there are warps for all tokens, so that sequences' tokens go to teams of their own; else as
+    // long as a block, where most windows begin one
+    const int window = FEW ? kThreads / 32 : few(a) ? 1 : std::min(32, a.kv.scale_tokens);
+    const int64_t teams = ((int64_t)a.T + window - 1) / window * 2 * a.kv.kv_heads, per = FEW ? 1 : kThreads / TEAM;
     const int64_t kv_ctas = (teams + per - 1) / per;
     // many queries go faster through the ring of the plain append's kernel, as tokens that are not appended
     const bool alone = !few(a);
@@ -383,7 +414,7 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
     }
     const int64_t grid = kv_ctas + (alone ? 0 : a.T);
     if (grid > 0x3fffffff) return cudaErrorInvalidValue;  // teams are numbered in 32 bits
-    const auto kernel = append_blocks_kernel<XT, VEC, TEAM, KEEP, FOURS>;
+    const auto kernel = append_blocks_kernel<XT, VEC, TEAM, KEEP, FOURS, FEW>;
     constexpr int smem = KEEP ? (int)sizeof(Kept<KEEP ? KEEP : 1>) : 0;
     static std::atomic<uint64_t> configured;
     cudaError_t err = ensure_smem_limit((const void*)kernel, smem, configured, true);
@@ -395,9 +426,10 @@ template <int XT, bool FOURS>
 cudaError_t launch_team(const AppendArgs& a, cudaStream_t st) {
     constexpr bool ring = FOURS && XT != MOE_F32;
     // a warp turns 512 / head_dim tokens at a time: few for a long block, which four warps share, and enough
-    // for a block that gets a token or two, as those of a decode step do
-    return a.kv.scale_tokens <= 8 || few(a) ? launch<XT, 8, 32, ring ? 2 : 0, FOURS>(a, st)
-                                            : launch<XT, 8, kThreads, ring ? 4 : 0, FOURS>(a, st);
+    // for a short one
+    if (few(a)) return launch<XT, 8, 32, ring ? 2 : 0, FOURS, true>(a, st);
+    return a.kv.scale_tokens <= 8 ? launch<XT, 8, 32, ring ? 2 : 0, FOURS>(a, st)
+                                  : launch<XT, 8, kThreads, ring ? 4 : 0, FOURS>(a, st);
 }
 
 template <int XT>

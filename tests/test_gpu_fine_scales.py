@@ -384,6 +384,17 @@ def test_blocks_many_tokens(m):
     check_blocks(m, g, run_slots(g, 64, [(i % 64, 1) for i in range(600)]), 8, 8, 128, 64, 32, 128, BF16)
 
 
+@pytest.mark.parametrize("size", [1e-6, 50.0])
+@pytest.mark.parametrize("xt,block", [(BF16, 64), (F16, 16), (F32, 64), (BF16, 4)])
+def test_blocks_long_and_short_runs(m, xt, block, size):
+    """Runs of one token to many blocks, which begin at every place among four tokens and in blocks that hold
+    some, under scales that are too small for the new tokens and such that are large enough."""
+    g = gen(block)
+    lens = [1, 1, 2, 70, 3, 1, 1, 1, 5, 4, 66, 1, 8, 40, 1, 1, 1, 1, 2, 33]
+    check_blocks(m, g, run_slots(g, 64, [((7 * i + 1) % 64, n) for i, n in enumerate(lens)]), 4, 2, 128, 64, block, 128, xt, size=size)
+    check_blocks(m, g, run_slots(g, 64, [(0, 200)]), 32, 8, 128, 64, block, 64, xt, size=size)
+
+
 def test_blocks_tokens_left_out(m):
     """Negative slots, in the middle of a block's tokens too; every scale large enough, and every one too small."""
     g = gen(5)
