@@ -513,7 +513,8 @@ PyMethodDef methods[] = {
      "instead of (i, i + rot_dim / 2).  q_out may be q.\n\n"
      "axes (bytes or a sequence of rot_dim / 2 small integers): pair i is turned by\n"
      "positions[axes[i]], positions being int32 [n_axes, T], at most four axes.  A cache\n"
-     "with scales of blocks: the tokens that share a block follow one another."},
+     "with scales of blocks: the tokens that share a block follow one another, with\n"
+     "none between them that goes elsewhere or nowhere."},
     {"moe_quant_e4m3", FAST(py_quant),
      "moe_quant_e4m3(x, y, scale, stream=None)\n--\n\n"
      "y = x / scale in float8_e4m3fn, scale the largest |x| / 448 of each 128 elements.\n\n"
