@@ -399,7 +399,8 @@ int moe_add_rms_norm(const void* x, int x_type, int64_t x_stride, const void* re
 
 /* Rows to E4M3 with one fp32 scale for each 128 elements, the operands of moe_linear_blocks:
  *   scale[t][g] = max(max_k |x_tk| / 448, 2^-126),  y_tk = x_tk / scale[t][g],  k in [128 g, 128 g + 128)
- * A group with a NaN or an infinity gets a NaN scale and NaN codes.  Each group is independent.
+ * scale as it is returned (a product with 1 / 448: within 2^-23), the quotient an fp32 division's.  A group with a NaN
+ * or an infinity gets a NaN scale and NaN codes.  Each group is independent.
  *  x     device [T][K] of x_type (MOE_BF16, MOE_F16 or MOE_F32), rows x_stride apart.
  *  y     device E4M3 [T][K], rows y_stride apart.
  *  scale device fp32 [T][ceil(K / 128)], rows scale_stride apart.

@@ -1,13 +1,13 @@
 // Rows to E4M3 with one scale for each 128 elements.
 //
-//   s = max(max |x| / 448, 2^-126) over a group,  y = E4M3(x / s)
+//   s = max(max |x| / 448, 2^-126) over a group,  y = E4M3(x / s) with s as it is returned
 //
 // Memory bound: each element once in and once out.  A half warp holds a group, 8 elements a
 // lane, so that its maximum takes four exchanges and no shared memory; a half warp takes
 // several groups so that their loads are in flight together.
 //
-// Measured on a GB300: 8192 x 4096 bf16 21.0 us (4.8 TB/s, 72% of a plain copy's rate), 512 x 4096 2.3, 777 x 5003
-// fp32 at any alignment 5.5 (3.6 TB/s), 8 x 4096 1.3.
+// Measured on a GB300: 8192 x 4096 bf16 22.0 us (4.6 TB/s, 69% of a plain copy's rate), 512 x 4096 2.3, 777 x 5003
+// fp32 at any alignment 5.5 (3.6 TB/s), 8 x 4096 1.4.
 #include <algorithm>
 
 #include "ptx.cuh"
@@ -19,14 +19,31 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kE4M3Max = 448.f;
 
-// The scale of a group with largest magnitude `top`, and the factor of its elements.  A NaN or
-// an infinity among them: both NaN.
-__device__ __forceinline__ float scale_of(float top, float& factor) {
+// The scale of a group with largest magnitude `top`.  A NaN or an infinity among them: NaN.
+__device__ __forceinline__ float scale_of(float top) {
     const float m = top < INFINITY ? top : __uint_as_float(0x7fc00000u);
     const float scale = m * (1.f / kE4M3Max);
-    const bool floor = scale < 1.17549435e-38f;  // 2^-126; false for NaN
-    factor = floor ? 8.50705917e+37f : kE4M3Max / m;
-    return floor ? 1.17549435e-38f : scale;
+    return scale < 1.17549435e-38f ? 1.17549435e-38f : scale;  // 2^-126; NaN stays
+}
+
+// v /= scale, to nearest as fp32's division, so that a code is that of the quotient by the scale that the caller gets,
+// at ties between codes too.  With r the scale's inverse to nearest, x r is within a step of the quotient, what it leaves
+// of x is exact in a fused product, and adding that remainder's quotient rounds as the division does (P. Markstein, IBM
+// J. Res. Dev. 34, 1990).  Scales near the smallest are taken 2^64 larger, with the values, so that the remainder is
+// exact there too.  The remainder's sign is such that -0 stays.
+template <int N>
+__device__ __forceinline__ void divide(float (&v)[N], float scale) {
+    if (scale < 8.67361738e-19f) {  // 2^-60
+        scale *= 1.84467441e19f;    // 2^64
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] *= 1.84467441e19f;
+    }
+    const float r = 1.f / scale;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float q = v[i] * r;
+        v[i] = fmaf(-fmaf(q, scale, -v[i]), r, q);
+    }
 }
 
 // The larger of two, NaN if either is.
@@ -69,15 +86,14 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const QuantArgs a, int 
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float v[8] = {}, top = 0.f, factor;
+        float v[8] = {}, top = 0.f;
         if (in[u]) r[u].get(XT, v);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) top = max_nan(top, max_nan(fabsf(v[i]), fabsf(v[i + 1])));
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float scale = scale_of(top, factor);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= factor;
+        const float scale = scale_of(top);
+        divide(v, scale);
         if (in[u]) {
             store_run<8>(a.y, row[u] * a.y_stride + g[u] * kScaleGroup + lane * 8, MOE_E4M3, v);
             if (lane == 0) a.scale[row[u] * a.scale_stride + g[u]] = scale;
@@ -100,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) quant_any_kernel(const QuantArgs a, 
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
         if (k0 + 32 * j < a.K) r[j].load(a.x, row * a.x_stride + k0 + 32 * j, a.x_type);
-    float v[kEach], top = 0.f, factor;
+    float v[kEach], top = 0.f;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
         float one[1] = {0.f};
@@ -110,10 +126,11 @@ __global__ void __launch_bounds__(kThreads) quant_any_kernel(const QuantArgs a, 
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float scale = scale_of(top, factor);
+    const float scale = scale_of(top);
+    divide(v, scale);
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
-        const float one[1] = {v[j] * factor};
+        const float one[1] = {v[j]};
         if (k0 + 32 * j < a.K) store_run<1>(a.y, row * a.y_stride + k0 + 32 * j, MOE_E4M3, one);
     }
     if (lane == 0) a.scale[row * a.scale_stride + g] = scale;
