@@ -451,9 +451,10 @@ int moe_kv_destroy(moe_kv* kv);
  *    tokens that it takes in, at most 448 * scale, held to 2^-126 and 2^119 (larger values, infinities among
  *    them, saturate; NaN stays NaN and does not count).  A block whose first entry is among them starts anew:
  *    what else it held means nothing any more, though its bytes stay.  Any other block keeps its scale
- *    where that is large enough; where it is not, the codes of its other entries are rewritten under the
- *    new one (exact but where codes of less than 2^-6 lose their low bits), so the block's scale has to be
- *    initialised (zero will do) before a block is begun in its middle.  The tokens of a call that go to
+ *    where its magnitude is large enough; where it is not, the codes of its other entries are rewritten under the
+ *    new one, so the block's scale has to be initialised (zero will do) before a block is begun in its middle.
+ *    Rewriting codes under a power of two, as the append's own scales are, is exact but where codes of less than
+ *    2^-6 lose their low bits; under any other scale it rounds each once more.  The tokens of a call that go to
  *    one block have to follow one another in the call, with none between them that goes elsewhere or
  *    nowhere, and calls that append to one block have to be ordered.
  *  moe_kv_attend  takes scales up to 2^96 in magnitude, keys and values of 2^104; a NaN among those of

@@ -3,9 +3,10 @@
 //   scale = 2^e, e the smallest with max |values| <= 448 * 2^e;  code = E4M3(value / scale)
 //
 // over the values that the call puts into the block; a block that had tokens keeps its scale if
-// that is as large, and else its other codes are rewritten under the new one.  Powers of two lose
-// nothing in the rewriting but low bits of codes that become subnormal, and E4M3 has as many bits
-// under them as under any other scale.
+// that is as large in magnitude, and else its other codes are rewritten under the new one.  Powers of two
+// lose nothing in the rewriting but low bits of codes that become subnormal, and E4M3 has as many
+// bits under them as under any other scale.  (Codes under a scale of the caller's own that is no power
+// of two are rounded again.)
 //
 // Memory bound: q, k, v in, q_out and the codes out, each once.  The tokens of a block follow one
 // another in the call, so a team of threads (a warp where that is little, else four) takes what
@@ -292,7 +293,10 @@ __device__ __forceinline__ void append_block_runs(const AppendArgs& a, const Win
             }
         }
         const float need = scale_for(top);
-        const float scale = anew || !(old >= need) ? need : old;
+        // one of the caller's own may be negative, or large enough though less than the power of two
+        const float had = fabsf(old);
+        const bool enough = had >= need || (had >= 1.17549435e-38f && top <= 448.f * had);  // 2^-126
+        const float scale = anew || !enough ? need : old;
         const float inv = 1.f / scale;
         all(true, [&](float (&x0)[VEC], float (&x1)[VEC], int entry) {
 #pragma unroll

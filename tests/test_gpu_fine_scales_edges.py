@@ -42,3 +42,59 @@ def test_quant_codes_are_quotients_at_the_ends(m, K, e):  # noqa: F811
     g = gen(e + 200)
     x = torch.randint(-448, 449, (200, K), generator=g, device="cuda").double() * torch.randint(1, 8, (200, 1), generator=g, device="cuda")
     check_quotients(m, (x * 2.0 ** e / 8).clamp(-3.4e38, 3.4e38).float())
+
+
+# ---- append onto scales of the caller's own making ---------------------------------
+
+
+@pytest.mark.parametrize("hkv,D,block", [(2, 64, 16), (1, 128, 64), (3, 80, 5)])
+@pytest.mark.parametrize("T", [1, 9, 3000])
+@pytest.mark.parametrize("xt", [BF16, F32])
+def test_append_onto_scales_of_either_sign(m, hkv, D, block, T, xt):  # noqa: F811
+    """Tokens in the middle of blocks under scales of both signs, powers of two and others, large enough and too small: a
+    scale that is large enough stays, and whatever a block held keeps its value."""
+    g = gen(T + D)
+    page, n_pages = 4 * block, T // 4 + 2
+    nb = n_pages * 4
+    x = (3 * randn(g, T, 1 * hkv + 2 * hkv, D)).to(xt)
+    # one to three tokens a block, behind its first entry
+    home = torch.randperm(nb, generator=g, device="cuda").tolist()
+    slots, i = [], 0
+    while len(slots) < T:
+        n = min(1 + i % 3, T - len(slots), block - 1)
+        slots += [home[i] * block + 1 + i % (block - n) + j for j in range(n)]
+        i += 1
+    slots = torch.tensor(slots, device="cuda")
+    wrote = torch.zeros(nb * block, dtype=torch.bool, device="cuda")
+    wrote[slots] = True
+    touched = torch.zeros(nb, dtype=torch.bool, device="cuda")
+    touched[slots // block] = True
+    top = torch.zeros(2, nb, hkv, device="cuda")
+    for side in range(2):
+        v = x[:, hkv * (1 + side):hkv * (2 + side)].float().abs().amax(2)
+        top[side].scatter_reduce_(0, (slots // block)[:, None].expand(-1, hkv), v, "amax")
+    for power in (True, False):
+        codes = [(100 * randn(g, n_pages, page, hkv, D)).clamp(-448, 448).to(E4M3) for _ in range(2)]
+        e = torch.randint(-9, 3, (2, n_pages, 4, hkv), generator=g, device="cuda").float()
+        scales = torch.exp2(e) * (1 if power else 0.3) * (torch.randint(0, 2, e.shape, generator=g, device="cuda") * 2 - 1)
+        old_codes, old = [c.clone() for c in codes], scales.clone()
+        kv = m.KvCache(codes[0], codes[1], q_heads=hkv, max_batch=1, k_scale=scales[0], v_scale=scales[1])
+        m.moe_kv_append(kv, x[:, :hkv], x[:, hkv:2 * hkv], x[:, 2 * hkv:], None, slots, None, torch.empty(T, hkv, D, dtype=xt, device="cuda"))
+        assert kv.status() == 0
+        for side in range(2):
+            s0, s1 = old[side].view(nb, hkv), scales[side].view(nb, hkv)
+            keeps = (448 * s0.double().abs() >= top[side].double()) | ~touched[:, None]
+            assert torch.equal(s1[keeps], s0[keeps])
+            new = s1[~keeps].double()
+            assert (new > 0).all() and (448 * new >= top[side][~keeps]).all() and (224 * new < top[side][~keeps]).all()
+            assert (torch.frexp(new)[0] == 0.5).all()
+            per = s1.double().repeat_interleave(block, 0)[..., None]
+            got = codes[side].double().view(-1, hkv, D) * per
+            was = old_codes[side].double().view(-1, hkv, D) * s0.double().repeat_interleave(block, 0)[..., None]
+            # half a step of a subnormal code; under scales that are no powers of two half a step of every code
+            slack = per.abs() * 2.0 ** -10 + (0 if power else was.abs() * 2.0 ** -4 * 1.000001)
+            grown = ~keeps.repeat_interleave(block, 0)[..., None]
+            err = (got - was).abs()
+            assert (err <= torch.where(grown, slack, torch.zeros_like(slack)))[~wrote].all()
+            want = x[:, hkv * (1 + side):hkv * (2 + side)].double()
+            assert ((got[slots] - want).abs() <= want.abs() * 2.0 ** -4 * 1.000001 + per[slots].abs() * 2.0 ** -10 * 1.000001).all()
