@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T >= 2 ? 1 : 2, NT))
     constexpr int U = unit_tokens(DP * ES), MT = U / 16;  // tokens of a unit, in tiles of 16
     constexpr uint32_t kAll = U == 32 ? 0xffffffffu : 0xffffu;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_m[kWarps][HC], s_l[kWarps][HC], s_scale[HC], s_inv[HC];
+    __shared__ float s_m[kWarps][HC], s_l[kWarps][HC], s_scale[HC], s_inv[HC], s_ref[kWarps];
     __shared__ uint32_t s_mask[kWarps][kMaxStages];
     __shared__ long long s_sum[kWarps], s_rest[kWarps], s_before;
     __shared__ int s_b, s_last, s_longest[kWarps];
@@ -648,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T >= 2 ? 1 : 2, NT))
                     s_l[warp][8 * t + 2 * c + j] = y;
                 }
             }
+        if (BLOCKS && lane == 0) s_ref[warp] = v_ref;
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
         float* mine_o = reinterpret_cast<float*>(ring);  // [HC][D + 4]; the ring is empty now
@@ -659,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T >= 2 ? 1 : 2, NT))
                 float top = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][h]);
-                const float f = m[t][j] == -INFINITY ? 0.f : fast_exp2(m[t][j] - top) * (BLOCKS ? v_ref : 1.f);
+                const float f = m[t][j] == -INFINITY ? 0.f : fast_exp2(m[t][j] - top);
 #pragma unroll
                 for (int i = 0; i < DP / 16; ++i) {
                     if (i < steps) {
@@ -686,9 +687,11 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T >= 2 ? 1 : 2, NT))
             // a warp with no maximum has seen nothing (sum 0) or NaN alone (sum NaN, which has to stay)
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) sum += s_l[w][tid] * part_weight(s_m[w][tid], top);
-            if (whole) {
+            if (whole || BLOCKS) {
                 s_inv[tid] = v_scale / sum;
                 if (!(sum != 0.f)) s_inv[tid] = 0.f;
+            }
+            if (whole) {
                 if (a.lse && tid < nh) a.lse[(int64_t)b * heads + h0 + tid] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
             } else {
                 slot_base[tid] = top;
@@ -705,11 +708,18 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T >= 2 ? 1 : 2, NT))
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float2 y = *reinterpret_cast<const float2*>(all + w * step + h * (D + 4) + d);
-                    v.x += y.x;
-                    v.y += y.y;
+                    if constexpr (BLOCKS) {
+                        // over the sum of weights before the unit is taken back: as an average of values it stays in
+                        // fp32's range where they do, however many the sum has and however large their weights
+                        v.x = fmaf(y.x * s_inv[h], s_ref[w], v.x);
+                        v.y = fmaf(y.y * s_inv[h], s_ref[w], v.y);
+                    } else {
+                        v.x += y.x;
+                        v.y += y.y;
+                    }
                 }
                 if (whole) {
-                    const float f = s_inv[h];
+                    const float f = BLOCKS ? 1.f : s_inv[h];
                     uint16_t* dst = static_cast<uint16_t*>(a.out) + b * a.out_ts + (h0 + h) * a.out_hs + d;
                     *reinterpret_cast<uint32_t*>(dst) =
                         a.q_type == MOE_BF16 ? pack_bf16(v.x * f, v.y * f) : pack_f16(v.x * f, v.y * f);
@@ -772,9 +782,14 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(DP, T >= 2 ? 1 : 2, NT))
                     sum *= part_weight(top, all);
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    for (int i = lane; i < parts; i += 32) weights[h * parts + i] = part_weight(weights[h * parts + i], all);
+                    const float inv = sum != 0.f ? v_scale / sum : 0.f;
+                    for (int i = lane; i < parts; i += 32) {
+                        float f = part_weight(weights[h * parts + i], all);
+                        if constexpr (BLOCKS) f *= part(i0 + i)[HC + h] * inv;  // of a part's average
+                        weights[h * parts + i] = f;
+                    }
                     if (lane == 0) {
-                        s_inv[h] = sum != 0.f ? v_scale / sum : 0.f;
+                        s_inv[h] = BLOCKS ? 1.f : inv;
                         if (a.lse) a.lse[(int64_t)b * heads + h0 + h] = sum == 0.f ? -INFINITY : (all + log2f(sum)) * kLn2;
                     }
                 }

@@ -6,7 +6,7 @@ Bounds come from the arithmetic; helpers and their bounds are those of the opera
 import pytest
 import torch
 
-from test_gpu_fine_scales import BF16, E4M3, F16, F32, gen, m, randn  # noqa: F401
+from test_gpu_fine_scales import BF16, E4M3, F16, F32, attend64, block_cache, gen, m, randn, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +98,35 @@ def test_append_onto_scales_of_either_sign(m, hkv, D, block, T, xt):  # noqa: F8
             assert (err <= torch.where(grown, slack, torch.zeros_like(slack)))[~wrote].all()
             want = x[:, hkv * (1 + side):hkv * (2 + side)].double()
             assert ((got[slots] - want).abs() <= want.abs() * 2.0 ** -4 * 1.000001 + per[slots].abs() * 2.0 ** -10 * 1.000001).all()
+
+
+# ---- attention under large scales ------------------------------------------------
+
+
+@pytest.mark.parametrize("hq,D", [(4, 64), (32, 128), (2, 256)])
+@pytest.mark.parametrize("lens", [[20000] * 32, [4000], [1, 17, 5000, 900]])
+@pytest.mark.parametrize("e", [-126, 96])
+def test_attend_long_under_scales_at_the_ends(m, hq, D, lens, e):  # noqa: F811
+    """Values' scales at both ends of their range, and values of one sign at the end of theirs, under long sequences in
+    which runs of tokens, the first among them, score a few units less than the rest, so that weights are counted from
+    a reference below their maximum."""
+    g = gen(D + e)
+    page, block = 16, 8
+    per = -(-max(lens) // page)
+    n_pages = len(lens) * per
+    pages = torch.randperm(n_pages, generator=g, device="cuda").to(torch.int32).view(len(lens), per)
+    k, ks = block_cache(g, n_pages, page, block, 2, D, 0.02)
+    v = torch.randint(320, 449, (n_pages, page, 2, D), generator=g, device="cuda").float().to(E4M3)
+    vs = torch.full_like(ks, 2.0 ** e)
+    q = torch.ones(len(lens), hq, D, device="cuda").to(BF16)
+    scale = 0.5
+    far = pages[:, torch.arange(per, device="cuda") // 8 % 8 == 0].reshape(-1).long()  # 128 tokens of 1024
+    k[far] = torch.full_like(k[far].float(), -1.0).to(E4M3)
+    ks[far] = 5.0 / (D * scale)  # scores of -5
+    kv = m.KvCache(k, v, q_heads=hq, max_batch=len(lens), k_scale=ks, v_scale=vs)
+    o, lse = torch.empty_like(q), torch.empty(len(lens), hq, device="cuda")
+    m.moe_kv_attend(kv, q, pages, torch.tensor(lens, dtype=torch.int32, device="cuda"), o, scale=scale, lse=lse)
+    o64, l64, ot, lt = attend64(q, k, v, ks, vs, pages, lens, scale, 0)
+    assert o64.abs().max() < 2.0 ** (e + 9)
+    within(o, o64, ot + 2.0 ** (e - 133))
+    within(lse, l64, lt)
