@@ -404,7 +404,8 @@ int moe_add_rms_norm(const void* x, int x_type, int64_t x_stride, const void* re
  *  x     device [T][K] of x_type (MOE_BF16, MOE_F16 or MOE_F32), rows x_stride apart.
  *  y     device E4M3 [T][K], rows y_stride apart.
  *  scale device fp32 [T][ceil(K / 128)], rows scale_stride apart.
- * The outputs must not share memory with x.  K >= 1; T = 0 is valid.
+ * The outputs must not share memory with x nor with one another (an output at another's or at x's address is
+ * refused).  K >= 1; T = 0 is valid.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */
 int moe_quant_e4m3(const void* x, int x_type, int64_t x_stride, int T, int K, void* y, int64_t y_stride, float* scale,
                    int64_t scale_stride, void* stream);

@@ -519,7 +519,7 @@ PyMethodDef methods[] = {
      "moe_quant_e4m3(x, y, scale, stream=None)\n--\n\n"
      "y = x / scale in float8_e4m3fn, scale the largest |x| / 448 of each 128 elements.\n\n"
      "x [T, K] bfloat16, float16 or float32; y [T, K] float8_e4m3fn; scale fp32\n"
-     "[T, ceil(K / 128)]."},
+     "[T, ceil(K / 128)].  None of the three shares memory with another."},
     {"moe_kv_attend", FAST(py_attend),
      "moe_kv_attend(kv, q, page_table, lengths, out, scale=None, window=0, lse=None, stream=None)\n--\n\n"
      "Attention of one query token per sequence over the cache.\n\n"

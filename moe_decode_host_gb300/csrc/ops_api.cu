@@ -223,6 +223,7 @@ int moe_quant_e4m3(const void* x, int x_type, int64_t x_stride, int T, int K, vo
     if (T < 0 || K < 1 || !is_float_type(x_type)) return MOE_ERR_INVALID_ARG;
     if (T == 0) return MOE_OK;
     if (!x || !y || !scale) return MOE_ERR_INVALID_ARG;
+    if (y == x || scale == x || scale == y) return MOE_ERR_INVALID_ARG;  // a group's codes would lie on another's elements
     if (T == 1) x_stride = y_stride = scale_stride = 0;  // of no meaning for one row
     QuantArgs a{x, x_type, x_stride, T, K, y, y_stride, scale, scale_stride};
     return cuda_status(launch_quant(a, S(stream)));
