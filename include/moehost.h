@@ -455,9 +455,10 @@ int moe_kv_destroy(moe_kv* kv);
  *    where its magnitude is large enough; where it is not, the codes of its other entries are rewritten under the
  *    new one, so the block's scale has to be initialised (zero will do) before a block is begun in its middle.
  *    Rewriting codes under a power of two, as the append's own scales are, is exact but where codes of less than
- *    2^-6 lose their low bits; under any other scale it rounds each once more.  The tokens of a call that go to
- *    one block have to follow one another in the call, with none between them that goes elsewhere or
- *    nowhere, and calls that append to one block have to be ordered.
+ *    2^-6 lose their low bits; under any other scale it rounds each once more.
+ *    The tokens of a call that go to one block have to follow one another in the call, with none between them
+ *    that goes elsewhere or nowhere.  Where they do not, MOE_ERR_BAD_INDEX is set in the handle's status, and what
+ *    that block holds is not defined.  Calls that append to one block have to be ordered.
  *  moe_kv_attend  takes scales up to 2^96 in magnitude, keys and values of 2^104; a NaN among those of
  *    attended tokens shows in that head's outputs.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA, MOE_ERR_NOMEM. */

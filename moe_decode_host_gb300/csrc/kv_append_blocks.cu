@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kAny = -1;   // a type known only at run time
+constexpr int kChecks = 256;  // most CTAs that look at runs
 
 // The smallest power of two s with top <= 448 s, from 2^-126 to 2^119.  448 = 1.75 * 2^8.
 __device__ __forceinline__ float scale_for(float top) {
@@ -104,6 +105,45 @@ __device__ __forceinline__ Window window_of(const AppendArgs& a, int64_t w0, int
     w.home = home_of(a, w.mine);
     w.begins = __ballot_sync(0xffffffffu, w.home.first >= 0 && (before < 0 || !within(a, before, w.home.first)));
     return w;
+}
+
+// Whether the runs that begin with tokens [w0, w0 + 32) are their blocks' only ones in the call, told in the status:
+// teams of their own would take two at a time.  One that begins with its block's first entry needs no look, for any
+// other of that block begins behind it; so a prompt has one to look for, a decode step as many as it has sequences.
+// CTAs of their own do it beside the others: 8 tokens 3.55 us (3.4 without), 512 sequences 11.5 (11.5), 8192 sequences
+// 441 (432), or 47 (37) with one key head; looking in every team before it writes took 512 sequences 15.2 us.
+__device__ __forceinline__ void check_runs(const AppendArgs& a, int64_t w0) {
+    const int lane = threadIdx.x & 31;
+    const auto slot_at = [&](int64_t t) { return t < a.T ? a.slots[t] : -1; };
+    int64_t next = slot_at(threadIdx.x);
+    const Window win = window_of(a, w0, 32);
+    const uint32_t starts = __ballot_sync(0xffffffffu, (win.begins >> lane & 1u) && win.mine != win.home.first);
+    if (!starts) return;
+    const uint32_t low = (uint32_t)win.home.first;
+    const bool many = __popc(starts) > 4;  // then all without branches
+    for (int64_t t = threadIdx.x; t - lane < a.T; t += kThreads) {
+        const int64_t slot = next;
+        next = slot_at(t + kThreads);
+        uint32_t near = 0;  // starts whose block this token's slot lies in, by the low halves of both
+        const auto look = [&](int j) {
+            if ((uint32_t)slot - __shfl_sync(0xffffffffu, low, j) < (uint32_t)a.kv.scale_tokens) near |= 1u << j;
+        };
+        if (many) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) look(j);
+        } else {
+            for (uint32_t left = starts; left; left &= left - 1) look(__ffs(left) - 1);
+        }
+        near &= starts;
+        if (t >= w0 && t < w0 + 32) near &= ~(1u << (t - w0));  // itself
+        for (uint32_t left = __reduce_or_sync(0xffffffffu, near); left; left &= left - 1) {
+            const int j = __ffs(left) - 1;
+            const int64_t first = __shfl_sync(0xffffffffu, win.home.first, j);
+            // another token of the block: one that does not go on with a run begins another
+            if ((near >> j & 1u) && within(a, slot, first) && (t == 0 || !within(a, a.slots[t - 1], first)))
+                set_status(a.kv.status, MOE_ERR_BAD_INDEX);
+        }
+    }
 }
 
 // A team's share of k and v: the runs `begins` of the window, of head `head` of k (side 0) or v (side 1).
@@ -339,12 +379,12 @@ __device__ __forceinline__ void append_block_runs(const AppendArgs& a, const Win
     }
 }
 
-// The first CTAs take k and v, a team per (window of tokens, head of either); the others, where there are any, a
-// token's queries each.  FEW: a CTA per window of as many tokens as it has warps, which take a run each; the last run
+// The first CTAs look whether runs are their blocks' only ones, the next take k and v, a team per (window of tokens,
+// head of either); the others, where there are any, a token's queries each.  FEW: a CTA per window of as many tokens as it has warps, which take a run each; the last run
 // is the only one that can reach behind the window, and if it does all of them take it (a prompt of 256 tokens
 // 10.7 us, 28 by a warp a block; 512 sequences of a token each 11.5 us, 11.0).
 template <int XT, int VEC, int TEAM, int KEEP, bool FOURS, bool FEW>
-__global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendArgs a, int window, int kv_ctas) {
+__global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendArgs a, int window, int checks, int kv_ctas) {
     static_assert(!FEW || TEAM == 32, "a run a warp");
     __shared__ uint32_t mask[kThreads / TEAM][kMaxScaleTokens / 32];
     __shared__ float part[2][kThreads / 32];
@@ -352,9 +392,14 @@ __global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendArg
     grid_launch_next();
     grid_dep_wait();
     const int xt = XT == kAny ? a.type : XT;
-    if ((int)blockIdx.x < kv_ctas) {
+    if ((int)blockIdx.x < checks) {
+        for (int64_t w0 = 32 * (int64_t)blockIdx.x; w0 < a.T; w0 += 32 * (int64_t)checks) check_runs(a, w0);
+        return;
+    }
+    const uint32_t cta = blockIdx.x - checks;
+    if ((int)cta < kv_ctas) {
         const int heads = 2 * a.kv.kv_heads, team = threadIdx.x / TEAM;
-        const uint32_t unit = FEW ? blockIdx.x : blockIdx.x * (kThreads / TEAM) + team, w32 = unit / (uint32_t)heads;
+        const uint32_t unit = FEW ? cta : cta * (kThreads / TEAM) + team, w32 = unit / (uint32_t)heads;
         const int64_t w0 = (int64_t)w32 * window;
         const int h = (int)(unit - w32 * heads), side = h >= a.kv.kv_heads, head = side ? h - a.kv.kv_heads : h;
         Kept<KEEP ? KEEP : 1>& kept = *reinterpret_cast<Kept<KEEP ? KEEP : 1>*>(room);
@@ -375,7 +420,7 @@ __global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendArg
         }
         return;
     }
-    const int64_t t = blockIdx.x - kv_ctas;
+    const int64_t t = cta - kv_ctas;
     const int items = a.kv.head_dim / (2 * VEC), step = kThreads / items, g = threadIdx.x / items;
     if (g >= step) return;
     const Item<VEC> it(a, threadIdx.x % items);
@@ -416,14 +461,15 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
         cudaError_t err = launch_append(q, st);
         if (err != cudaSuccess) return err;
     }
-    const int64_t grid = kv_ctas + (alone ? 0 : a.T);
+    const int checks = a.kv.scale_tokens > 1 ? std::min(kChecks, (a.T - 1) / 32 + 1) : 0;
+    const int64_t grid = checks + kv_ctas + (alone ? 0 : a.T);
     if (grid > 0x3fffffff) return cudaErrorInvalidValue;  // teams are numbered in 32 bits
     const auto kernel = append_blocks_kernel<XT, VEC, TEAM, KEEP, FOURS, FEW>;
     constexpr int smem = KEEP ? (int)sizeof(Kept<KEEP ? KEEP : 1>) : 0;
     static std::atomic<uint64_t> configured;
     cudaError_t err = ensure_smem_limit((const void*)kernel, smem, configured, true);
     if (err != cudaSuccess) return err;
-    return launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), smem, st, a, window, (int)kv_ctas);
+    return launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), smem, st, a, window, checks, (int)kv_ctas);
 }
 
 template <int XT, bool FOURS>

@@ -6,7 +6,7 @@ Bounds come from the arithmetic; helpers and their bounds are those of the opera
 import pytest
 import torch
 
-from test_gpu_fine_scales import BF16, E4M3, F16, F32, attend64, block_cache, gen, m, randn, within  # noqa: F401
+from test_gpu_fine_scales import BF16, E4M3, F16, F32, attend64, block_cache, gen, m, randn, table, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +130,50 @@ def test_attend_long_under_scales_at_the_ends(m, hq, D, lens, e):  # noqa: F811
     assert o64.abs().max() < 2.0 ** (e + 9)
     within(o, o64, ot + 2.0 ** (e - 133))
     within(lse, l64, lt)
+
+
+# ---- tokens of a block that do not follow one another --------------------------------
+
+
+def calls_that_come_apart(page, block, filler):
+    """Slots of calls in which one block's tokens, in the first page, are not in one run, and the same without those."""
+    def runs(at, *counts):  # consecutive tokens, each lot from a block's beginning on
+        for k in counts:
+            yield list(range(at, at + k))
+            at += -(-k // block) * block
+
+    n = block // 2
+    for between in (0, 1, filler):
+        for first, second in ((range(n), range(n, block)),  # begun, left and gone on with
+                              (range(n, block), range(n)),  # the other way about
+                              ([1], range(2, block))):      # both behind the first entry
+            head, middle, tail = runs(page, 3, between, filler)
+            middle = middle or [-1]
+            yield head + [*first] + middle + [*second] + tail, head + [-1] * len(first) + middle + [-1] * len(second) + tail
+
+
+@pytest.mark.parametrize("xt,hq,hkv,D,rot", [(BF16, 4, 2, 64, 64), (F16, 2, 1, 128, 64), (F32, 4, 2, 64, 64), (BF16, 5, 1, 48, 18),
+                                             (BF16, 16, 8, 128, 128)])
+@pytest.mark.parametrize("page,block", [(16, 4), (64, 32), (12, 6), (256, 128)])
+@pytest.mark.parametrize("filler", [2, 31, 5000])
+def test_append_tells_of_tokens_that_come_apart(m, xt, hq, hkv, D, rot, page, block, filler):  # noqa: F811
+    """The status is set, and blocks whose tokens follow one another are as in the call without the others."""
+    g = gen(D + block + filler)
+    n_pages = 5 + 2 * filler // page
+    k, ks = block_cache(g, n_pages, page, block, hkv, D, 0.01)
+    v, vs = block_cache(g, n_pages, page, block, hkv, D, 0.01)
+    cs = table(60, rot)
+    for slots, kept in calls_that_come_apart(page, block, filler):
+        T = len(slots)
+        x = (2 * randn(g, T, hq + 2 * hkv, D)).to(xt)
+        pos = torch.randint(0, 60, (T,), generator=g, device="cuda", dtype=torch.int32)
+        seen = []
+        for s, status in ((slots, m.MOE_ERR_BAD_INDEX), (kept, 0)):
+            c = [t.clone() for t in (k, v, ks, vs)]
+            kv = m.KvCache(c[0], c[1], q_heads=hq, max_batch=1, k_scale=c[2], v_scale=c[3])
+            qo = torch.full((T, hq, D), 7.0, device="cuda").to(xt)
+            m.moe_kv_append(kv, x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], pos, torch.tensor(s, device="cuda"), cs, qo)
+            assert kv.status() == status, (slots[:8], T)
+            seen.append([t.view(torch.uint8)[1:] for t in c] + [qo.view(torch.uint8)])
+        assert all(torch.equal(p, q) for p, q in zip(*seen))
+        assert not torch.equal(seen[0][0], k.view(torch.uint8)[1:])
