@@ -6,7 +6,9 @@ Bounds come from the arithmetic; helpers and their bounds are those of the opera
 import pytest
 import torch
 
-from test_gpu_fine_scales import BF16, E4M3, F16, F32, attend64, block_cache, gen, m, randn, table, within  # noqa: F401
+from test_gpu_fine_scales import (AXES, BF16, E4M3, F16, F32, SUB, U, attend64, block_cache, e4m3_tol, gen, m, put64,  # noqa: F401
+                                  randn, rows64, run_slots, table, turn64, within)
+from test_gpu_linear_blocks import operands
 
 pytestmark = pytest.mark.gpu
 
@@ -177,3 +179,90 @@ def test_append_tells_of_tokens_that_come_apart(m, xt, hq, hkv, D, rot, page, bl
             seen.append([t.view(torch.uint8)[1:] for t in c] + [qo.view(torch.uint8)])
         assert all(torch.equal(p, q) for p, q in zip(*seen))
         assert not torch.equal(seen[0][0], k.view(torch.uint8)[1:])
+
+
+# ---- kernels for many tokens, and blocks that a team cannot hold at once -----------------
+
+
+def check_many(m, g, xt, hkv, D, page, block, rot, il, axes, runs, n_axes=3):  # noqa: F811
+    hq = hkv
+    slots = run_slots(g, page, runs)
+    T = len(slots)
+    assert T * 2 * hkv > 16384  # else they are few
+    n_pages = max(slots) // page + 2
+    x = randn(g, T, hq + 2 * hkv, D).to(xt)
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    slots = torch.tensor(slots, device="cuda")
+    cs = table(90, rot)
+    pos = torch.randint(0, 90, (n_axes, T), generator=g, device="cuda", dtype=torch.int32)
+    pair = AXES[axes](rot // 2, n_axes) if axes else [0] * (rot // 2)
+    cos, sin = rows64(cs, pos, pair)
+    q64, qsz = turn64(q, cos, sin, il)
+    k64, ksz = turn64(k, cos, sin, il)
+    for size in (1e-4, 30.0):  # scales that are too small for the tokens, and such that are large enough
+        kc, ks = block_cache(g, n_pages, page, block, hkv, D, size)
+        vc, vs = block_cache(g, n_pages, page, block, hkv, D, size)
+        k0, v0, ks0, vs0 = kc.clone(), vc.clone(), ks.clone(), vs.clone()
+        kv = m.KvCache(kc, vc, q_heads=hq, max_batch=1, k_scale=ks, v_scale=vs)
+        qo = torch.empty(T, hq, D, dtype=xt, device="cuda")
+        m.moe_kv_append(kv, q, k, v, pos if axes else pos[0], slots, cs, qo, interleaved=il, axes=pair if axes else None)
+        assert kv.status() == 0
+        within(qo, q64, q64.abs() * U[xt] + qsz * 2.0 ** -23 + SUB[xt], "q")
+        for codes, scales, c0, s0, x64, sz in ((kc, ks, k0, ks0, k64, ksz), (vc, vs, v0, vs0, v.double(), torch.zeros_like(ksz))):
+            want, sc, wrote = put64(c0, s0, slots, x64, block, [True] * T)
+            assert torch.equal(scales.double(), sc)
+            per = sc.view(-1, hkv).repeat_interleave(block, 0)
+            slack = torch.zeros(n_pages * page, hkv, D, dtype=torch.float64, device="cuda")
+            slack[slots] = sz * 2.0 ** -22
+            within(codes.float().view(-1, hkv, D), want.view(-1, hkv, D), e4m3_tol(want.view(-1, hkv, D)) + slack / per[..., None], "codes")
+            same = (sc == s0.double()).view(-1, 1, hkv, 1).expand(-1, block, -1, D).reshape(-1, hkv, D) & ~wrote[:, None, None]
+            assert torch.equal(codes.view(torch.uint8).view(-1, hkv, D)[same], c0.view(torch.uint8).view(-1, hkv, D)[same])
+
+
+@pytest.mark.parametrize("xt", [BF16, F16, F32])
+@pytest.mark.parametrize("axes,il", [(None, True), ("turns", False), ("turns", True), ("fours", True), ("sections", False)])
+@pytest.mark.parametrize("block", [1, 8, 64])
+def test_many_tokens_of_every_kind(m, xt, il, block, axes):  # noqa: F811
+    check_many(m, gen(block), xt, 8, 32, 64, block, 32, il, axes, [(0, 700), (13, 400), (63, 2), (5, 100)])
+
+
+@pytest.mark.parametrize("xt", [BF16, F32])
+@pytest.mark.parametrize("D,rot,page,block", [(128, 128, 128, 128), (256, 128, 64, 64), (256, 256, 32, 32), (64, 64, 1024, 1024), (128, 64, 512, 256),
+                                              (48, 18, 64, 64), (80, 40, 200, 100)])
+def test_blocks_longer_than_a_team_holds(m, xt, D, rot, page, block):  # noqa: F811
+    """Read twice, with other runs before and behind them."""
+    check_many(m, gen(D + block), xt, 8, D, page, block, rot, False, None, [(0, 600), (7, 500), (page // 2, 3)])
+    check_many(m, gen(D + block), xt, 8, D, page, block, rot, True, "turns", [(page - 1, 1100), (0, 5)])
+
+
+# ---- what the quantiser and the product share with others ------------------------------
+
+
+def test_quant_of_the_norms_rows(m):  # noqa: F811
+    """The norm's own E4M3 rows and the quantiser's of the norm's fp32 rows: one group a row, so the scales are those of
+    the same numbers, a few roundings of fp32 apart, and either's codes are within half a step of them."""
+    g = gen(3)
+    x, w = (3 * randn(g, 500, 128)).to(BF16), randn(g, 128).to(BF16)
+    y32, y8, s8 = torch.empty(500, 128, device="cuda"), torch.empty(500, 128, dtype=E4M3, device="cuda"), torch.empty(500, device="cuda")
+    m.moe_add_rms_norm(x, w, y32)
+    m.moe_add_rms_norm(x, w, y8, scale=s8)
+    q, s = torch.empty(500, 128, dtype=E4M3, device="cuda"), torch.empty(500, 1, device="cuda")
+    m.moe_quant_e4m3(y32, q, s)
+    within(s[:, 0], s8.double(), s8.double() * 2.0 ** -22, "scale")  # a rounding each on the way to the maximum and to the scale
+    for codes, scale in ((y8, s8[:, None]), (q, s)):
+        want = y32.double() / scale.double()
+        within(codes.float(), want, e4m3_tol(want) + want.abs() * 2.0 ** -22, "codes")
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 256, 512), (30, 300, 1024), (100, 256, 2048), (300, 512, 512), (1000, 1024, 512)])
+def test_a_products_row_does_not_depend_on_its_neighbours(m, T, N, K):  # noqa: F811
+    g = gen(T)
+    x, w, xs, ws = operands(g, T, N, K)
+    keep = torch.arange(0, T, 7, device="cuda")
+    y, z = torch.empty(T, N, device="cuda"), torch.empty(T, N, device="cuda")
+    m.moe_linear_blocks(x, w, y, xs, ws)
+    x2, _, xs2, _ = operands(g, T, N, K)
+    x2.view(torch.uint8)[keep] = x.view(torch.uint8)[keep]
+    xs2[keep] = xs[keep]
+    m.moe_linear_blocks(x2, w, z, xs2, ws)
+    assert torch.equal(y[keep], z[keep]) and (T == 1 or not torch.equal(y, z))
