@@ -557,7 +557,8 @@ int moe_linear(const void* x, int64_t x_stride, const void* w, int64_t w_stride,
  *   y = act(sum_g x_scale[t][g] * w_scale[n / 128][g] * (sum_{k in g} x_tk w_nk) + bias) + residual
  *  x device E4M3 [T][K], w device E4M3 [N][K], as in moe_linear.
  *  x_scale device fp32 [T][G], rows x_scale_stride apart; w_scale device fp32 [ceil(N / 128)][G], rows
- *    w_scale_stride apart: any numbers.
+ *    w_scale_stride apart: any numbers.  The product of the two is an fp32 number (below 2^-126 it loses bits, from
+ *    2^128 it is infinite).
  * The rest as moe_linear.  The products of a block of K are summed by the tensor cores (fp32, towards zero
  * at every 32 of K), the blocks, times their two scales' product, in fp32 to nearest.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA. */

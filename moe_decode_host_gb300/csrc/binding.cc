@@ -514,7 +514,7 @@ PyMethodDef methods[] = {
      "axes (bytes or a sequence of rot_dim / 2 small integers): pair i is turned by\n"
      "positions[axes[i]], positions being int32 [n_axes, T], at most four axes.  A cache\n"
      "with scales of blocks: the tokens that share a block follow one another, with\n"
-     "none between them that goes elsewhere or nowhere."},
+     "none between them that goes elsewhere or nowhere (else kv.status() tells)."},
     {"moe_quant_e4m3", FAST(py_quant),
      "moe_quant_e4m3(x, y, scale, stream=None)\n--\n\n"
      "y = x / scale in float8_e4m3fn, scale the largest |x| / 448 of each 128 elements.\n\n"

@@ -10,13 +10,16 @@
 //
 // Memory bound: q, k, v in, q_out and the codes out, each once.  The tokens of a block follow one
 // another in the call, so a team of threads (a warp where that is little, else four) takes what
-// the call puts into one block of one head of k or v: it turns the values, keeps them in registers
+// the call puts into one block of one head of k or v: it turns the values, keeps them in shared memory
 // while their maximum is found, and writes codes and scale.  Teams look for the blocks that begin
 // in their window of tokens, so nothing has to be counted or sorted beforehand.  The queries of small
 // calls are turned by further CTAs of the same launch, those of large ones by the plain append's kernel.
 //
-// Measured on a GB300: 8192 tokens of 32 + 8 + 8 heads of 128, bf16, into blocks of 64 64 us (29 of them the
-// queries'), blocks of 16 82; 8 tokens 3.4, 64 sequences 4.0, 512 sequences 11.5, 256 tokens of one 10.7.
+// Measured on a GB300, bf16 of 32 + 8 + 8 heads of 128 into blocks whose scales stay: 8192 tokens into blocks of 64 63 us
+// (in the profiler 24 for the queries' launch and 36 for the keys' and values'; the rest passes between the two), of 128 75,
+// of 16 80, of 4 72, of 1 183; into blocks of 32 8 tokens 3.6, 64 sequences 4.2, 512 sequences 11.6; 256 tokens of one into
+// blocks of 64 10.9.  Over 30 caches in turn, whose blocks all have to be rewritten under larger scales, and the same calls
+// afterwards: 8 tokens 6.8 and 3.6, 512 sequences 34 and 13.9, 8192 tokens of 32 sequences 67.5 and 65.
 #include <algorithm>
 
 #include "kv_append.cuh"
@@ -382,7 +385,7 @@ __device__ __forceinline__ void append_block_runs(const AppendArgs& a, const Win
 // The first CTAs look whether runs are their blocks' only ones, the next take k and v, a team per (window of tokens,
 // head of either); the others, where there are any, a token's queries each.  FEW: a CTA per window of as many tokens as it has warps, which take a run each; the last run
 // is the only one that can reach behind the window, and if it does all of them take it (a prompt of 256 tokens
-// 10.7 us, 28 by a warp a block; 512 sequences of a token each 11.5 us, 11.0).
+// 10.9 us, 28 by a warp a block; 512 sequences of a token each 11.6 us, 11.0).
 template <int XT, int VEC, int TEAM, int KEEP, bool FOURS, bool FEW>
 __global__ void __launch_bounds__(kThreads) append_blocks_kernel(const AppendArgs a, int window, int checks, int kv_ctas) {
     static_assert(!FEW || TEAM == 32, "a run a warp");

@@ -11,8 +11,9 @@
 // than in the tensor cores' own sums.
 //
 // Measured on a GB300 (launches of a graph): 8192 x 6144 x 4096 with bias 173 us (2385 TFLOP/s; the plain
-// E4M3 product 115), with GELU 243, 4096 x 4096 x 4096 68, 1024 x 4096 x 4096 23, 777 x 5003 x 1424 f16 with GELU 27,
-// 32 x 6144 x 4096 7.8, 1 x 4096 x 4096 5.2 (6.4 with its weights in memory and not in L2).
+// E4M3 product 115), with ReLU 209, with GELU 243, 4096 x 4096 x 4096 64, 1024 x 4096 x 4096 20, 777 x 5003 x 1424 f16 with
+// GELU 27.5,
+// 32 x 6144 x 4096 7.6, 1 x 4096 x 4096 5.1 (6.3 with its weights in memory and not in L2).
 // What bounds the tiles is a circle of two accumulators: products (some 600 cycles for 256 x 256 outputs
 // and a block of K), their commit, the additions up to the last read of the accumulator (some 450) and the
 // arrival that lets the next products have it, 1500 cycles for two blocks of K.  The additions alone
@@ -788,6 +789,8 @@ cudaError_t launch_tiles(const LinearArgs& a, const BlockScales& sc, bool vec, c
 //         tiles of 256, 128 and 64 outputs.  1024 x 1024 x 1024 10.4, 7.2 and 6.9 us; 4096 x 2048 x 8192 67, 78 and 117.
 //  split  3000 + rounds * (45 bn for the join + blocks of K of a CTA * (200 + 1.2 bn)).  128 x 4096 x 4096 11.2 us
 //         against 12.0 in tiles, 128 x 1024 x 1024 8.8 against 6.0.
+// Fitted before the kernel without activation was an instance of its own, which takes less (8192 x 6144 x 4096 173 us, 212
+// by the formula), and blind to activations and unaligned rows, which take more (777 x 5003 x 1424 27 us, 20).
 cudaError_t launch_linear_blocks(const LinearArgs& args, int64_t xs_stride, int64_t ws_stride, cudaStream_t st) {
     if (args.T == 0) return cudaSuccess;
     const BlockScales sc{args.x_scale, args.w_scale, xs_stride, ws_stride,

@@ -6,8 +6,9 @@
 // lane, so that its maximum takes four exchanges and no shared memory; a half warp takes
 // several groups so that their loads are in flight together.
 //
-// Measured on a GB300: 8192 x 4096 bf16 22.0 us (4.6 TB/s, 69% of a plain copy's rate), 512 x 4096 2.3, 777 x 5003
-// fp32 at any alignment 5.5 (3.6 TB/s), 8 x 4096 1.4.
+// Measured on a GB300: 8192 x 4096 bf16 22.0 us (4.6 TB/s, 69% of a plain copy's rate), 512 x 4096 2.5, 777 x 5003
+// fp32 at any alignment 5.8 (3.4 TB/s), 8 x 4096 1.4.  A quotient takes two fused steps an
+// element more than a product by one factor, with which the first took 20.9 us.
 #include <algorithm>
 
 #include "ptx.cuh"
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) quant_any_kernel(const QuantArgs a, 
 template <int XT>
 cudaError_t launch(const QuantArgs& a, int groups, int64_t total, cudaStream_t st) {
     constexpr int each = kThreads / 16;
-    if (total <= 32768) {  // few groups: all of the GPU rather than several a half warp (512 x 4096 2.3 us, 3.2 with four)
+    if (total <= 32768) {  // few groups: all of the GPU rather than several a half warp (512 x 4096 2.5 us, 3.5 with four)
         return launch_pdl(quant_kernel<XT, 1>, dim3((unsigned)((total + each - 1) / each)), dim3(kThreads), 0, st, a, groups, total);
     }
     const int64_t grid = (total + 4 * each - 1) / (4 * each);
